@@ -25,8 +25,6 @@ struct PackGeom {
     size_t exp_off = 0;
 };
 
-tsl_status geometry(const tsl_shard &s, tsl_dtype wdtype, PackGeom *g);
-
 // Q4G64 packed record of 16 columns x 128 k: 1 KB of codes, then the 128
 // bytes of (scale, bias) pairs of its two 64-k groups.
 constexpr int kQ4Record = 1152;
@@ -89,6 +87,38 @@ hipError_t launch_gather_to_ranks(int n, const void *const *parts, size_t elem_b
 // Y (+)= sum_{s < ks} P[s], P is [ks][M][N] f32 contiguous, ascending s.
 hipError_t launch_splitk_reduce(const float *P, int ks, int64_t M, int64_t N, tsl_dtype ydtype,
                                 void *Y, int64_t ldy, int accumulate, hipStream_t stream);
+
+// ---- norm.hip: residual-adding root-mean-square norm and its backward ----
+constexpr int64_t kNormMaxWidth = 32768; // a row lives in one workgroup's registers
+struct NormArgs {
+    const void *parts[kMaxParts];
+    const void *residual; // null: none
+    void *sum_out;        // null: not kept; residual's type
+    const void *weight;   // null: ones
+    void *Y;
+    float *scales;        // e4m3 outputs: [M][groups]
+    float *rstd;          // null: not kept
+    int64_t M, n, ld_part, ldr, ld_sum, ldy;
+    float eps;
+    int32_t n_parts, p_bf16, r_bf16, w_bf16, y_type, group;
+};
+struct NormGradArgs {
+    const void *dY, *X, *weight, *dres; // weight, dres may be null
+    const float *rstd;                  // null: recomputed from X
+    void *dX;                           // null: not wanted; dres has its type
+    float *part;                        // null: no weight gradient
+    int64_t M, n, lddy, ldx, ld_dres, lddx, row_groups;
+    float eps;
+    int32_t dy_bf16, x_bf16, w_bf16, dx_bf16;
+};
+// vec: every base is 16-byte aligned and every row stride whole 16 bytes
+// (e4m3: 8 bytes)
+hipError_t launch_norm(const NormArgs &a, bool vec, hipStream_t stream);
+// row groups of a backward launch: its partial weight gradients take
+// row groups x (n rounded up to 8) binary32
+int64_t norm_grad_groups(int64_t M, int64_t n);
+hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accumulate,
+                            hipStream_t stream);
 
 // ---- embed.hip ----
 // Y[m][j] = table[(tokens[m] - k_off) * ld_table + j] when the token lies in
