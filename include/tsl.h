@@ -91,9 +91,12 @@ typedef enum tsl_proj {
 typedef enum tsl_dtype {
     TSL_F32 = 0,   /* IEEE binary32                                         */
     TSL_BF16 = 1,  /* bfloat16 (upper half of a binary32)                   */
-    TSL_Q4G64 = 2  /* weights only: 4-bit codes q in 0..15, affine groups of
+    TSL_Q4G64 = 2, /* weights only: 4-bit codes q in 0..15, affine groups of
                       64 input elements with a bf16 scale s and bias b:
                       w = s * q + b                                         */
+    TSL_E4M3 = 3   /* outputs of add_rms_norm (tsl_block.h): 8-bit floats (4 exponent
+                      and 3 mantissa bits, largest 448, no infinities) with
+                      binary32 scales                                       */
 } tsl_dtype;
 
 /* Dimensions of one transformer layer and the TP degree. */

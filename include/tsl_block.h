@@ -1,0 +1,115 @@
+/*
+ * tsl_block.h -- what lies between and around the shard products of tsl.h in
+ * a transformer layer, on one AMD Instinct MI355X (gfx950): the
+ * residual-adding root-mean-square norm and its backward pass.
+ *
+ * A library of its own (libtsl_block.so) beside libtsl.so: the same types,
+ * status codes, packed weights (pack_shard) and shard plans, and the same
+ * conventions -- buffers owned by the caller, work enqueued on `stream`
+ * without synchronising, every check on the host before anything is
+ * enqueued, leading dimensions in elements (tsl.h, "Conventions shared by
+ * every entry point").  Nothing throws across it.
+ */
+#ifndef TSL_BLOCK_H
+#define TSL_BLOCK_H
+
+#include "tsl.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#if defined(__GNUC__)
+#pragma GCC visibility push(default)
+#endif
+
+/*
+ * add_rms_norm -- the root-mean-square norm between a row-parallel product
+ * and the next column-parallel ones ([mlxcel] "Row Parallel": the rank
+ * partials of o_proj / down_proj are summed before the next block reads
+ * them), with the rank sum and the residual stream's addition in the same
+ * pass:
+ *     r[m][j] = (((P_0 + P_1) + P_2) + ...)[m][j] + residual[m][j]
+ *     y[m][j] = r[m][j] * rstd[m] * weight[j],
+ *     rstd[m] = 1 / sqrt(mean_j r[m][j]^2 + eps)
+ * in binary32 throughout (y is formed from the unrounded r).
+ *   parts:    HOST array of n_parts DEVICE pointers, [M][n] each, row stride
+ *             ld_part, type pdtype (F32 or BF16); 1 <= n_parts <= 64.  One
+ *             part and no residual is the plain norm.
+ *   residual: null, or DEVICE [M][n], row stride ldr, type rdtype (F32/BF16).
+ *   sum_out:  null, or DEVICE [M][n], row stride ld_sum, type rdtype:
+ *             receives r (rounded once), the new residual stream.  It may be
+ *             the residual itself (same address and row stride).
+ *   weight:   null (ones), or DEVICE [n], type wdtype (F32 or BF16).
+ *   Y:        DEVICE [M][n], row stride ldy, type ydtype: F32, BF16 (rounded
+ *             once), or E4M3: 8-bit values q with binary32 scales, y = s q,
+ *             one s per run of `group` columns (group 32, 64 or 128; the
+ *             last run of a row may be short) or per row (group 0):
+ *             s = max |y| / 448 over the run and q = y / s rounded to nearest
+ *             even; a run of zeros has s = 0, a run with a value that is not
+ *             finite an s that is not finite and q NaN.
+ *   scales:   DEVICE binary32 [M][ceil(n / group)] ([M] for group 0) for
+ *             E4M3, else null (and group 0).
+ *   rstd:     null, or DEVICE binary32 [M]: receives rstd (for the backward
+ *             pass).
+ * 1 <= n <= 32768 (TSL_ERR_UNSUPPORTED above); M < 2^22 and row strides below
+ * 2^31.  M == 0 enqueues nothing.  No output may overlap an input or another
+ * output (except sum_out as stated).  Errors: TSL_ERR_INVALID_ARG,
+ * TSL_ERR_UNSUPPORTED, TSL_ERR_MISALIGNED (pointers aligned to their element
+ * size; 16-byte aligned rows run fastest), TSL_ERR_HIP.
+ */
+tsl_status add_rms_norm(int32_t n_parts, const void *const *parts, tsl_dtype pdtype,
+                        int64_t ld_part, int64_t M, int64_t n, const void *residual,
+                        tsl_dtype rdtype, int64_t ldr, void *sum_out, int64_t ld_sum,
+                        const void *weight, tsl_dtype wdtype, float eps, tsl_dtype ydtype, void *Y,
+                        int64_t ldy, float *scales, int32_t group, float *rstd, void *stream);
+
+/* add_rms_norm_grad_workspace_size -- workspace bytes of add_rms_norm_grad
+ * with a weight gradient (without one it needs none). */
+tsl_status add_rms_norm_grad_workspace_size(int64_t M, int64_t n, size_t *bytes);
+
+/*
+ * add_rms_norm_grad -- the backward pass of add_rms_norm: with x the sum it
+ * kept (sum_out), t = dy * weight and xh = x * rstd,
+ *     dx[m][j] = rstd[m] * (t[m][j] - xh[m][j] * mean_j(t[m][j] xh[m][j]))
+ *                + dres[m][j]
+ *     dw[j] (+)= sum_m dy[m][j] * xh[m][j]
+ * dx is the gradient of the residual and of every part alike (the sum passes
+ * it on unchanged); dres is the gradient that reaches the residual stream
+ * (sum_out) from its other readers.
+ *   dY:     DEVICE [M][n], row stride lddy, type dydtype (F32 or BF16).
+ *   X:      DEVICE [M][n], row stride ldx, type xdtype (F32 or BF16).
+ *   weight: null (ones), or DEVICE [n], type wdtype.
+ *   rstd:   null (recomputed from X and eps), or DEVICE binary32 [M] as kept
+ *           by add_rms_norm (eps is then not read).
+ *   dres:   null, or DEVICE [M][n], row stride ld_dres, type dxdtype; it may
+ *           be dX itself (same address and row stride).
+ *   dX:     null, or DEVICE [M][n], row stride lddx, type dxdtype.
+ *   dW:     null, or DEVICE binary32 [n]; accumulate_dw 1 adds to it.  The
+ *           rows are added in a fixed order: equal calls give equal bits.
+ *   workspace: 256-byte aligned, add_rms_norm_grad_workspace_size() bytes
+ *           when dW is wanted (else may be null).
+ * M == 0 writes only dW (zeros, unless it accumulates).  Width and row limits
+ * as add_rms_norm.  Errors: TSL_ERR_INVALID_ARG, TSL_ERR_UNSUPPORTED,
+ * TSL_ERR_BUFFER_TOO_SMALL, TSL_ERR_MISALIGNED, TSL_ERR_HIP.
+ */
+tsl_status add_rms_norm_grad(int64_t M, int64_t n, const void *dY, tsl_dtype dydtype, int64_t lddy,
+                             const void *X, tsl_dtype xdtype, int64_t ldx, const void *weight,
+                             tsl_dtype wdtype, float eps, const float *rstd, const void *dres,
+                             int64_t ld_dres, void *dX, tsl_dtype dxdtype, int64_t lddx, float *dW,
+                             int accumulate_dw, void *workspace, size_t ws_bytes, void *stream);
+
+/* The HIP runtime's description of the error behind the most recent
+ * TSL_ERR_HIP an entry point of this header returned on the calling thread
+ * ("no error" if none). */
+const char *tsl_block_last_hip_error_string(void);
+
+#if defined(__GNUC__)
+#pragma GCC visibility pop
+#endif
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TSL_BLOCK_H */

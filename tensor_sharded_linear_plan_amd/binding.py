@@ -1,5 +1,5 @@
-"""ctypes binding of libtsl.so -- the entry points of include/tsl.h under the
-same names, argument marshalling only.  Every step of the compute runs in
+"""ctypes binding of libtsl.so and libtsl_block.so -- the entry points of
+include/tsl.h and include/tsl_block.h under the same names, argument marshalling only.  Every step of the compute runs in
 the library's HIP kernels; nothing here computes.
 
 Pointer arguments take either an integer device address or any object with
@@ -7,7 +7,7 @@ a ``data_ptr()`` method (a torch tensor).  ``stream=None`` means the current
 torch stream when torch has a GPU, else the null stream.  A non-OK status
 raises TslError carrying the status code.
 
-Importing this module loads libtsl.so; when it has not been built the
+Importing this module loads both libraries; when one has not been built the
 import fails with ImportError -- there is no fallback path.
 
 PyTorch wheels for ROCm carry their own HIP runtime, which torch's libraries
@@ -33,6 +33,11 @@ if not os.path.exists(LIBRARY):
     raise ImportError("libtsl.so is not built: run __graft_entry__.build() or "
                       "python tensor_sharded_linear_plan_amd/build.py")
 _lib = ctypes.CDLL(LIBRARY)
+BLOCK_LIBRARY = os.path.join(_PKG, "libtsl_block.so")
+if not os.path.exists(BLOCK_LIBRARY):
+    raise ImportError("libtsl_block.so is not built: run __graft_entry__.build() or "
+                      "python tensor_sharded_linear_plan_amd/build.py")
+_block = ctypes.CDLL(BLOCK_LIBRARY)
 
 # ---- enums (include/tsl.h) ----
 OK = 0
@@ -48,7 +53,7 @@ Q, K, V, O, GATE, UP, DOWN = range(7)
 NPROJ = 7
 LINEAR = 7
 EMBED, LM_HEAD = 8, 9
-F32, BF16, Q4G64 = 0, 1, 2
+F32, BF16, Q4G64, E4M3 = 0, 1, 2, 3
 ALL_REDUCE, REDUCE_SCATTER, ALL_GATHER = 0, 1, 2
 MAX_PARTS = 64
 
@@ -58,7 +63,9 @@ class TslError(RuntimeError):
         self.status = status
         msg = _lib.tsl_status_string(status).decode()
         if status == ERR_HIP:
-            msg += " [%s]" % _lib.tsl_last_hip_error_string().decode()
+            last = _block.tsl_block_last_hip_error_string if where in BLOCK_EXPORTS else \
+                _lib.tsl_last_hip_error_string
+            msg += " [%s]" % last().decode()
         super().__init__("%s: %s (%d)" % (where, msg, status))
 
 
@@ -149,6 +156,23 @@ EXPORTS = ("plan_shards", "plan_linear", "pack_shard_size", "pack_shard",
            "combine_to_ranks", "plan_vocab",
            "embed_lookup", "plan_experts", "moe_dispatch", "moe_gather", "moe_combine",
            "tsl_status_string", "tsl_last_hip_error_string")
+
+
+_block.add_rms_norm.argtypes = [_i32, ctypes.POINTER(_vp), ctypes.c_int, _i64, _i64, _i64, _vp,
+                              ctypes.c_int, _i64, _vp, _i64, _vp, ctypes.c_int, ctypes.c_float,
+                              ctypes.c_int, _vp, _i64, _vp, _i32, _vp, _vp]
+_block.add_rms_norm_grad_workspace_size.argtypes = [_i64, _i64, ctypes.POINTER(_sz)]
+_block.add_rms_norm_grad.argtypes = [_i64, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _i64,
+                                   _vp, ctypes.c_int, ctypes.c_float, _vp, _vp, _i64, _vp,
+                                   ctypes.c_int, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]
+_block.tsl_block_last_hip_error_string.argtypes = []
+_block.tsl_block_last_hip_error_string.restype = ctypes.c_char_p
+
+# the entry points of include/tsl_block.h
+BLOCK_EXPORTS = ("add_rms_norm", "add_rms_norm_grad_workspace_size", "add_rms_norm_grad",
+                 "tsl_block_last_hip_error_string")
+for _f in BLOCK_EXPORTS[:-1]:
+    getattr(_block, _f).restype = ctypes.c_int
 
 
 def _check(status, where):
@@ -329,3 +353,27 @@ def combine_to_ranks(op, parts, pdtype, M, n_each, ld_part, odtype, outs, ldo, s
         raise ValueError("combine_to_ranks: one output per part")
     _check(_lib.combine_to_ranks(op, n, parr, pdtype, M, n_each, ld_part, odtype, oarr, ldo,
                                  _stream(stream)), "combine_to_ranks")
+
+
+def add_rms_norm(parts, pdtype, ld_part, M, n, residual, rdtype, ldr, sum_out, ld_sum, weight,
+                 wdtype, eps, ydtype, Y, ldy, scales=None, group=0, rstd=None, stream=None):
+    arr = (_vp * max(len(parts), 1))(*[_ptr(p) for p in parts])
+    _check(_block.add_rms_norm(len(parts), arr, pdtype, ld_part, M, n, _ptr(residual), rdtype, ldr,
+                             _ptr(sum_out), ld_sum, _ptr(weight), wdtype, eps, ydtype, _ptr(Y), ldy,
+                             _ptr(scales), group, _ptr(rstd), _stream(stream)), "add_rms_norm")
+
+
+def add_rms_norm_grad_workspace_size(M, n):
+    b = _sz(0)
+    _check(_block.add_rms_norm_grad_workspace_size(M, n, ctypes.byref(b)),
+           "add_rms_norm_grad_workspace_size")
+    return b.value
+
+
+def add_rms_norm_grad(M, n, dY, dydtype, lddy, X, xdtype, ldx, weight, wdtype, eps, rstd, dres,
+                      ld_dres, dX, dxdtype, lddx, dW, accumulate_dw=0, workspace=None, ws_bytes=0,
+                      stream=None):
+    _check(_block.add_rms_norm_grad(M, n, _ptr(dY), dydtype, lddy, _ptr(X), xdtype, ldx, _ptr(weight),
+                                  wdtype, eps, _ptr(rstd), _ptr(dres), ld_dres, _ptr(dX), dxdtype,
+                                  lddx, _ptr(dW), accumulate_dw, _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "add_rms_norm_grad")
