@@ -318,7 +318,7 @@ def _prepare_own(case, d):
                                  residual=d["res"], res_dtype=yt,
                                  ld_res=d["res"].stride(0) if d["res"] is not None else 0)
                             if r == 0 else None)
-        s["nws"] = tsl.shard_linear_group_workspace_size(s["items"], s["wt"], m)
+        s["nws"] = tsl.shard_linear_group_epilogue_workspace_size(s["items"], s["eps"], s["wt"], m)
         s["ws"] = _bytes(s["nws"])
         s.pop("w")
     elif op == "gated":
