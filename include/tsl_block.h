@@ -1,7 +1,8 @@
 /*
  * tsl_block.h -- what lies between and around the shard products of tsl.h in
  * a transformer layer, on one AMD Instinct MI355X (gfx950): the
- * residual-adding root-mean-square norm and its backward pass.
+ * residual-adding root-mean-square norm, shard products with an epilogue
+ * (bias, activation, residual), and the gated feed-forward block.
  *
  * A library of its own (libtsl_block.so) beside libtsl.so: the same types,
  * status codes, packed weights (pack_shard) and shard plans, and the same
@@ -98,6 +99,113 @@ tsl_status add_rms_norm_grad(int64_t M, int64_t n, const void *dY, tsl_dtype dyd
                              tsl_dtype wdtype, float eps, const float *rstd, const void *dres,
                              int64_t ld_dres, void *dX, tsl_dtype dxdtype, int64_t lddx, float *dW,
                              int accumulate_dw, void *workspace, size_t ws_bytes, void *stream);
+
+/* Activations of the epilogue and of the gated block. */
+typedef enum tsl_act {
+    TSL_ACT_NONE = 0,
+    TSL_ACT_RELU = 1,     /* max(v, 0)                                         */
+    TSL_ACT_SILU = 2,     /* v / (1 + exp(-v))                                 */
+    TSL_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2                       */
+    TSL_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2   */
+} tsl_act;
+
+/* What a product goes through before it is stored (shard_linear_group_epilogue):
+ *     Y = act(X W + bias) + residual
+ * in binary32, rounded once to the item's ydtype.
+ *   bias:     null, or DEVICE [n_len] (the shard's own columns), type
+ *             bias_dtype (F32 or BF16).
+ *   residual: null, or DEVICE [rows][n_len], row stride ld_res, type
+ *             res_dtype (F32 or BF16): row i is added to row i of the
+ *             product.  It may be the item's Y itself (same address, row
+ *             stride and type): the residual stream updated in place.
+ *   pre:      null, or DEVICE [rows][n_len], row stride ld_pre, type
+ *             pre_dtype: receives X W + bias (rounded once), what the
+ *             activation's backward pass needs. */
+typedef struct tsl_epilogue {
+    const void *bias;
+    const void *residual;
+    void *pre;
+    int64_t ld_res;
+    int64_t ld_pre;
+    int32_t act; /* tsl_act */
+    int32_t bias_dtype, res_dtype, pre_dtype;
+} tsl_epilogue;
+
+/* shard_linear_group_epilogue_workspace_size -- workspace bytes
+ * shard_linear_group_epilogue needs (items as for
+ * shard_linear_group_workspace_size; of the epilogues only whether one is
+ * null is read). */
+tsl_status shard_linear_group_epilogue_workspace_size(int32_t n_items,
+                                                      const tsl_linear_item *items,
+                                                      const tsl_epilogue *const *epilogues,
+                                                      tsl_dtype wdtype, int64_t M, size_t *bytes);
+
+/*
+ * shard_linear_group_epilogue -- shard_linear_group (tsl.h) with bias,
+ * activation and residual in the products' epilogue: the same items, types,
+ * sum sets, row counts, row indices, workspace rules and errors.
+ *   epilogues: HOST array of n_items HOST pointers, read during the call
+ *              only; epilogues[i] belongs to item i (null: the plain
+ *              product).  Of a sum set the first item's applies, once, to the
+ *              set's sum -- bias and residual of a row-parallel layer are
+ *              added after the ranks' partials ([mlxcel] "Row Parallel") --
+ *              and those of its other members must be null.
+ * accumulate must be 0 for an item with an epilogue.  No output (Y, pre) may
+ * share an element with another output or with any X, bias or residual
+ * (except a residual that is its own item's Y).
+ */
+tsl_status shard_linear_group_epilogue(int32_t n_items, const tsl_linear_item *items,
+                                       const tsl_epilogue *const *epilogues, tsl_dtype wdtype,
+                                       tsl_dtype xdtype, int64_t M, void *workspace,
+                                       size_t ws_bytes, void *stream);
+
+/*
+ * One gated feed-forward block of a grouped call:
+ *     H = act(X W_gate) * (X W_up)
+ * ([mlxcel] "Architecture-aware shard plan": gate and up are column shards
+ * over the same columns, and H, sharded by those columns, is the input of
+ * the down projection's row shard.)  gate and up are HOST shards of equal
+ * k_len and n_len, packed by pack_shard with the call's wdtype, packed_bytes
+ * the size of either buffer.  X, ldx, rows, row_index and x_rows as in
+ * tsl_linear_item.  H: DEVICE [rows][n_len], row stride ldh, type hdtype
+ * (F32 or BF16), formed in binary32 from the two products and rounded once.
+ * G, U: null, or DEVICE [rows][n_len], row stride ld_gu, type hdtype: receive
+ * X W_gate and X W_up (rounded once) for the backward pass; either both or
+ * none.
+ */
+typedef struct tsl_gated_item {
+    const tsl_shard *gate, *up;
+    const void *packed_gate, *packed_up;
+    size_t packed_bytes;
+    const void *X;
+    int64_t ldx;
+    void *H;
+    int64_t ldh;
+    void *G, *U;
+    int64_t ld_gu;
+    const int32_t *row_index;
+    int64_t x_rows;
+    int32_t hdtype;
+    int32_t rows;
+} tsl_gated_item;
+
+/* shard_gated_group_workspace_size -- workspace bytes shard_gated_group needs
+ * for these items (only their shards, rows and whether row_index is null are
+ * read), weight type and M. */
+tsl_status shard_gated_group_workspace_size(int32_t n_items, const tsl_gated_item *items,
+                                            tsl_dtype wdtype, int64_t M, size_t *bytes);
+
+/*
+ * shard_gated_group -- gated feed-forward blocks with the same activation
+ * and types in one pass, each over M rows or its own row count: one rank's
+ * shard, every rank's, or the experts of a mixture-of-experts layer over the
+ * tokens routed to each (row_index).  Types, alignment, limits and errors as
+ * shard_linear_group; 1 <= n_items <= 2048.  No output (H, G, U) may share an
+ * element with another output or any X or row index.
+ */
+tsl_status shard_gated_group(int32_t n_items, const tsl_gated_item *items, tsl_act act,
+                             tsl_dtype wdtype, tsl_dtype xdtype, int64_t M, void *workspace,
+                             size_t ws_bytes, void *stream);
 
 /* The HIP runtime's description of the error behind the most recent
  * TSL_ERR_HIP an entry point of this header returned on the calling thread

@@ -55,6 +55,7 @@ LINEAR = 7
 EMBED, LM_HEAD = 8, 9
 F32, BF16, Q4G64, E4M3 = 0, 1, 2, 3
 ALL_REDUCE, REDUCE_SCATTER, ALL_GATHER = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 MAX_PARTS = 64
 
 
@@ -108,6 +109,25 @@ class LinearItem(ctypes.Structure):
                 ("ydtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
                 ("sum_next", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("row_index", ctypes.c_void_p), ("x_rows", ctypes.c_int64)]
+
+
+class Epilogue(ctypes.Structure):
+    """What a product goes through before it is stored (tsl_epilogue)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("pre", ctypes.c_void_p), ("ld_res", ctypes.c_int64), ("ld_pre", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("pre_dtype", ctypes.c_int32)]
+
+
+class GatedItem(ctypes.Structure):
+    """One gated feed-forward block of shard_gated_group (tsl_gated_item)."""
+    _fields_ = [("gate", ctypes.POINTER(Shard)), ("up", ctypes.POINTER(Shard)),
+                ("packed_gate", ctypes.c_void_p), ("packed_up", ctypes.c_void_p),
+                ("packed_bytes", ctypes.c_size_t), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("H", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("G", ctypes.c_void_p), ("U", ctypes.c_void_p), ("ld_gu", ctypes.c_int64),
+                ("row_index", ctypes.c_void_p), ("x_rows", ctypes.c_int64),
+                ("hdtype", ctypes.c_int32), ("rows", ctypes.c_int32)]
 
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
@@ -165,11 +185,23 @@ _block.add_rms_norm_grad_workspace_size.argtypes = [_i64, _i64, ctypes.POINTER(_
 _block.add_rms_norm_grad.argtypes = [_i64, _i64, _vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _i64,
                                    _vp, ctypes.c_int, ctypes.c_float, _vp, _vp, _i64, _vp,
                                    ctypes.c_int, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]
+_P_EPS = ctypes.POINTER(ctypes.POINTER(Epilogue))
+_P_GATED = ctypes.POINTER(GatedItem)
+_block.shard_linear_group_epilogue_workspace_size.argtypes = [_i32, _P_ITEM, _P_EPS, ctypes.c_int,
+                                                              _i64, ctypes.POINTER(_sz)]
+_block.shard_linear_group_epilogue.argtypes = [_i32, _P_ITEM, _P_EPS, ctypes.c_int, ctypes.c_int,
+                                               _i64, _vp, _sz, _vp]
+_block.shard_gated_group_workspace_size.argtypes = [_i32, _P_GATED, ctypes.c_int, _i64,
+                                                    ctypes.POINTER(_sz)]
+_block.shard_gated_group.argtypes = [_i32, _P_GATED, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64,
+                                     _vp, _sz, _vp]
 _block.tsl_block_last_hip_error_string.argtypes = []
 _block.tsl_block_last_hip_error_string.restype = ctypes.c_char_p
 
 # the entry points of include/tsl_block.h
 BLOCK_EXPORTS = ("add_rms_norm", "add_rms_norm_grad_workspace_size", "add_rms_norm_grad",
+                 "shard_linear_group_epilogue_workspace_size", "shard_linear_group_epilogue",
+                 "shard_gated_group_workspace_size", "shard_gated_group",
                  "tsl_block_last_hip_error_string")
 for _f in BLOCK_EXPORTS[:-1]:
     getattr(_block, _f).restype = ctypes.c_int
@@ -377,3 +409,71 @@ def add_rms_norm_grad(M, n, dY, dydtype, lddy, X, xdtype, ldx, weight, wdtype, e
                                   wdtype, eps, _ptr(rstd), _ptr(dres), ld_dres, _ptr(dX), dxdtype,
                                   lddx, _ptr(dW), accumulate_dw, _ptr(workspace), ws_bytes,
                                   _stream(stream)), "add_rms_norm_grad")
+
+
+def _epilogues(eps, n):
+    """eps: one dict (or Epilogue) per item with the tsl_epilogue fields
+    (types default to F32, act to ACT_NONE), or None for a plain product."""
+    if len(eps) != n:
+        raise ValueError("one epilogue (or None) per item")
+    arr = (ctypes.POINTER(Epilogue) * max(n, 1))()
+    for i, e in enumerate(eps):
+        if e is None:
+            continue
+        if not isinstance(e, Epilogue):
+            e = Epilogue(_ptr(e.get("bias")), _ptr(e.get("residual")), _ptr(e.get("pre")),
+                         e.get("ld_res", 0), e.get("ld_pre", 0), e.get("act", ACT_NONE),
+                         e.get("bias_dtype", F32), e.get("res_dtype", F32), e.get("pre_dtype", F32))
+        arr[i] = ctypes.pointer(e)
+    return arr
+
+
+def shard_linear_group_epilogue_workspace_size(items, epilogues, wdtype, M):
+    arr, n = _items(items)
+    b = _sz(0)
+    _check(_block.shard_linear_group_epilogue_workspace_size(n, arr, _epilogues(epilogues, n), wdtype,
+                                                             M, ctypes.byref(b)),
+           "shard_linear_group_epilogue_workspace_size")
+    return b.value
+
+
+def shard_linear_group_epilogue(items, epilogues, wdtype, xdtype, M, workspace=None, ws_bytes=0,
+                                stream=None):
+    arr, n = _items(items)
+    _check(_block.shard_linear_group_epilogue(n, arr, _epilogues(epilogues, n), wdtype, xdtype, M,
+                                              _ptr(workspace), ws_bytes, _stream(stream)),
+           "shard_linear_group_epilogue")
+
+
+def _gated(items):
+    """items: sequence of dicts (or GatedItem) with the tsl_gated_item fields
+    (hdtype defaults to F32, rows to 0, G, U and row_index to None)."""
+    arr = (GatedItem * max(len(items), 1))()
+    keep = []
+    for i, it in enumerate(items):
+        if isinstance(it, GatedItem):
+            arr[i] = it
+            continue
+        g, u = Shard(*it["gate"].as_tuple()), Shard(*it["up"].as_tuple())
+        keep += [g, u]
+        arr[i] = GatedItem(ctypes.pointer(g), ctypes.pointer(u), _ptr(it["packed_gate"]),
+                           _ptr(it["packed_up"]), it["packed_bytes"], _ptr(it["X"]), it["ldx"],
+                           _ptr(it["H"]), it["ldh"], _ptr(it.get("G")), _ptr(it.get("U")),
+                           it.get("ld_gu", 0), _ptr(it.get("row_index")), it.get("x_rows", 0),
+                           it.get("hdtype", F32), it.get("rows", 0))
+    arr._keep = keep
+    return arr, len(items)
+
+
+def shard_gated_group_workspace_size(items, wdtype, M):
+    arr, n = _gated(items)
+    b = _sz(0)
+    _check(_block.shard_gated_group_workspace_size(n, arr, wdtype, M, ctypes.byref(b)),
+           "shard_gated_group_workspace_size")
+    return b.value
+
+
+def shard_gated_group(items, act, wdtype, xdtype, M, workspace=None, ws_bytes=0, stream=None):
+    arr, n = _gated(items)
+    _check(_block.shard_gated_group(n, arr, act, wdtype, xdtype, M, _ptr(workspace), ws_bytes,
+                                    _stream(stream)), "shard_gated_group")

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cstddef>
 #include <vector>
 
 #include "group.hpp"
@@ -224,6 +225,253 @@ extern "C" tsl_status add_rms_norm_grad(int64_t M, int64_t n, const void *dY, ts
                          wide(dres, ld_dres, de) && wide(dX, lddx, de);
         return from_hip(launch_norm_grad(a, vec, dW, accumulate_dw,
                                          static_cast<hipStream_t>(stream)));
+    });
+}
+
+// the tables' layouts are part of the ABI
+static_assert(sizeof(tsl_epilogue) == 56 && offsetof(tsl_epilogue, act) == 40, "tsl_epilogue layout");
+static_assert(sizeof(tsl_gated_item) == 120 && offsetof(tsl_gated_item, hdtype) == 112,
+              "tsl_gated_item layout");
+
+namespace {
+
+// The items of a size query (shards, set links, rows, whether indexed).
+tsl_status sized_items(int32_t n_items, const tsl_linear_item *items, tsl_dtype wdtype, int64_t M,
+                       std::vector<LinearItem> *out) {
+    out->resize(n_items);
+    int32_t first = 0;
+    for (int32_t i = 0; i < n_items; ++i) {
+        LinearItem &L = (*out)[i];
+        if (!items[i].shard || (items[i].sum_next != 0 && items[i].sum_next != 1) ||
+            items[i].rows < 0 || items[i].rows > M)
+            return TSL_ERR_INVALID_ARG;
+        tsl_status st = geometry(*items[i].shard, wdtype, &L.g);
+        if (st != TSL_OK)
+            return st;
+        L.M = items[i].rows ? items[i].rows : M;
+        L.ridx = items[i].row_index;
+        L.x_rows = 1;
+        L.set_pos = i - first;
+        if (!items[i].sum_next || i == n_items - 1) {
+            (*out)[first].set_len = i - first + 1;
+            for (int32_t r = first + 1; r <= i; ++r)
+                (*out)[r].set_len = 0;
+            first = i + 1;
+        }
+    }
+    return TSL_OK;
+}
+
+bool valid_act(int a) { return a >= TSL_ACT_NONE && a <= TSL_ACT_GELU_TANH; }
+
+// One epilogue's fields for a product of n columns; its checks.
+tsl_status check_epilogue(const tsl_epilogue &e, int64_t n, Epilogue *out) {
+    if (!valid_act(e.act) || (e.bias && !dense_type(e.bias_dtype)) ||
+        (e.residual && (!dense_type(e.res_dtype) || e.ld_res < n)) ||
+        (e.pre && (!dense_type(e.pre_dtype) || e.ld_pre < n)))
+        return TSL_ERR_INVALID_ARG;
+    if ((e.residual && e.ld_res >= kMaxLd) || (e.pre && e.ld_pre >= kMaxLd))
+        return TSL_ERR_UNSUPPORTED;
+    if ((e.bias && !aligned(e.bias, elem(e.bias_dtype))) ||
+        (e.residual && !aligned(e.residual, elem(e.res_dtype))) ||
+        (e.pre && !aligned(e.pre, elem(e.pre_dtype))))
+        return TSL_ERR_MISALIGNED;
+    out->bias = e.bias;
+    out->res = e.residual;
+    out->pre = e.pre;
+    out->ldr = e.ld_res;
+    out->ldp = e.ld_pre;
+    out->act = e.act;
+    out->flags = (e.bias && e.bias_dtype == TSL_BF16 ? kEpBiasBf16 : 0) |
+                 (e.residual && e.res_dtype == TSL_BF16 ? kEpResBf16 : 0) |
+                 (e.pre && e.pre_dtype == TSL_BF16 ? kEpPreBf16 : 0);
+    return TSL_OK;
+}
+
+// The operands of validated items that the group's own checks do not see
+// (kept pre-activations, biases, residuals) against every output and input.
+bool epilogue_clash(const std::vector<LinearItem> &v, size_t xe) {
+    std::vector<Mat> kept, read; // outputs and inputs of the epilogues
+    for (const LinearItem &L : v) {
+        if (!L.ep)
+            continue;
+        const Epilogue &e = *L.ep;
+        const size_t pe = e.flags & kEpPreBf16 ? 2 : 4, re = e.flags & kEpResBf16 ? 2 : 4;
+        if (e.pre)
+            kept.push_back(Mat{e.pre, L.M, L.g.Ns, e.ldp, pe});
+        if (e.pre2)
+            kept.push_back(Mat{e.pre2, L.M, L.g.Ns, e.ldp, pe});
+        if (e.bias)
+            read.push_back(Mat{e.bias, 1, L.g.Ns, L.g.Ns, (size_t)(e.flags & kEpBiasBf16 ? 2 : 4)});
+        if (e.res)
+            read.push_back(Mat{e.res, L.M, L.g.Ns, e.ldr, re});
+    }
+    if (kept.empty() && read.empty())
+        return false;
+    if (any_clash(kept, read))
+        return true;
+    for (const LinearItem &L : v) {
+        const Mat x{L.X, L.ridx ? L.x_rows : L.M, L.g.Ks, L.ldx, xe};
+        const Mat ix{L.ridx, 1, L.M, L.M, 4};
+        const Mat y{L.Y, L.M, L.g.Ns, L.ldy, (size_t)(L.ydtype == TSL_F32 ? 4 : 2)};
+        for (const Mat &k : kept)
+            if (clash(k, x) || clash(k, ix) || clash(k, y))
+                return true;
+        for (const Mat &r : read) {
+            const bool own = L.ep && L.ep->res == r.p && r.p == L.Y && L.ep->ldr == L.ldy &&
+                             y.e == r.e && r.ld == y.ld && r.rows == y.rows && r.cols == y.cols;
+            if (!own && clash(y, r))
+                return true;
+        }
+    }
+    return false;
+}
+
+bool any_epilogue(int32_t n, const tsl_epilogue *const *e) {
+    for (int32_t i = 0; i < n; ++i)
+        if (e[i])
+            return true;
+    return false;
+}
+
+} // namespace
+
+extern "C" tsl_status shard_linear_group_epilogue_workspace_size(
+    int32_t n_items, const tsl_linear_item *items, const tsl_epilogue *const *epilogues,
+    tsl_dtype wdtype, int64_t M, size_t *bytes) {
+    if (!items || !epilogues || !bytes || n_items < 1 || n_items > kMaxItems || M < 0)
+        return TSL_ERR_INVALID_ARG;
+    return guarded([&] {
+        std::vector<LinearItem> v;
+        tsl_status st = sized_items(n_items, items, wdtype, M, &v);
+        if (st != TSL_OK)
+            return st;
+        Epilogue none;
+        for (int32_t i = 0; i < n_items; ++i)
+            if (epilogues[i])
+                v[i].ep = &none;
+        *bytes = group_workspace(v, wdtype, M);
+        return TSL_OK;
+    });
+}
+
+extern "C" tsl_status shard_linear_group_epilogue(int32_t n_items, const tsl_linear_item *items,
+                                                  const tsl_epilogue *const *epilogues,
+                                                  tsl_dtype wdtype, tsl_dtype xdtype, int64_t M,
+                                                  void *workspace, size_t ws_bytes, void *stream) {
+    if (!epilogues)
+        return TSL_ERR_INVALID_ARG;
+    return guarded([&] {
+        std::vector<LinearItem> v;
+        tsl_status st = gather(n_items, items, wdtype, xdtype, M, &v);
+        if (st != TSL_OK)
+            return st;
+        std::vector<Epilogue> eps(n_items);
+        for (int32_t i = 0; i < n_items; ++i) {
+            if (!epilogues[i])
+                continue;
+            if (v[i].set_pos > 0 || v[i].accumulate)
+                return TSL_ERR_INVALID_ARG;
+            st = check_epilogue(*epilogues[i], v[i].g.Ns, &eps[i]);
+            if (st != TSL_OK)
+                return st;
+            v[i].ep = &eps[i];
+        }
+        if (M > 0 && any_epilogue(n_items, epilogues) && epilogue_clash(v, xdtype == TSL_F32 ? 4 : 2))
+            return TSL_ERR_INVALID_ARG;
+        return run_group(v, wdtype, M, workspace, ws_bytes, stream);
+    });
+}
+
+namespace {
+
+// A gated item as the pair of products the group code sees.
+void gated_pair(const tsl_gated_item &g, tsl_linear_item *two) {
+    for (int q = 0; q < 2; ++q) {
+        tsl_linear_item &L = two[q];
+        L = tsl_linear_item{};
+        L.shard = q ? g.up : g.gate;
+        L.packed = q ? g.packed_up : g.packed_gate;
+        L.packed_bytes = g.packed_bytes;
+        L.X = g.X;
+        L.ldx = g.ldx;
+        L.Y = g.H;
+        L.ldy = g.ldh;
+        L.ydtype = g.hdtype;
+        L.sum_next = q == 0;
+        L.rows = g.rows;
+        L.row_index = g.row_index;
+        L.x_rows = g.x_rows;
+    }
+}
+
+constexpr int32_t kMaxGated = kMaxItems / 2;
+
+} // namespace
+
+extern "C" tsl_status shard_gated_group_workspace_size(int32_t n_items, const tsl_gated_item *items,
+                                                       tsl_dtype wdtype, int64_t M, size_t *bytes) {
+    if (!items || !bytes || n_items < 1 || n_items > kMaxGated || M < 0)
+        return TSL_ERR_INVALID_ARG;
+    return guarded([&] {
+        std::vector<tsl_linear_item> pairs(2 * (size_t)n_items);
+        for (int32_t i = 0; i < n_items; ++i)
+            gated_pair(items[i], &pairs[2 * i]);
+        std::vector<LinearItem> v;
+        tsl_status st = sized_items(2 * n_items, pairs.data(), wdtype, M, &v);
+        if (st != TSL_OK)
+            return st;
+        Epilogue gate;
+        gate.flags = kEpGated;
+        for (int32_t i = 0; i < n_items; ++i) {
+            if (v[2 * i].g.Ns != v[2 * i + 1].g.Ns || v[2 * i].g.Ks != v[2 * i + 1].g.Ks)
+                return TSL_ERR_INVALID_ARG;
+            v[2 * i].ep = &gate;
+            // the pair reads one X (any address that no other pair has)
+            v[2 * i].X = v[2 * i + 1].X = &pairs[2 * i];
+        }
+        *bytes = group_workspace(v, wdtype, M);
+        return TSL_OK;
+    });
+}
+
+extern "C" tsl_status shard_gated_group(int32_t n_items, const tsl_gated_item *items, tsl_act act,
+                                        tsl_dtype wdtype, tsl_dtype xdtype, int64_t M,
+                                        void *workspace, size_t ws_bytes, void *stream) {
+    if (!items || n_items < 1 || n_items > kMaxGated || !valid_act(act))
+        return TSL_ERR_INVALID_ARG;
+    return guarded([&] {
+        std::vector<tsl_linear_item> pairs(2 * (size_t)n_items);
+        for (int32_t i = 0; i < n_items; ++i)
+            gated_pair(items[i], &pairs[2 * i]);
+        std::vector<LinearItem> v;
+        tsl_status st = gather(2 * n_items, pairs.data(), wdtype, xdtype, M, &v);
+        if (st != TSL_OK)
+            return st;
+        std::vector<Epilogue> eps(n_items);
+        bool kept = false;
+        for (int32_t i = 0; i < n_items; ++i) {
+            const tsl_gated_item &g = items[i];
+            const LinearItem &L = v[2 * i];
+            if (L.g.Ks != v[2 * i + 1].g.Ks || (g.G == nullptr) != (g.U == nullptr) ||
+                (g.G && g.ld_gu < L.g.Ns))
+                return TSL_ERR_INVALID_ARG;
+            if (g.G && g.ld_gu >= kMaxLd)
+                return TSL_ERR_UNSUPPORTED;
+            if (!aligned(g.G, elem(g.hdtype)) || !aligned(g.U, elem(g.hdtype)))
+                return TSL_ERR_MISALIGNED;
+            Epilogue &e = eps[i];
+            e.pre = g.G;
+            e.pre2 = g.U;
+            e.ldp = g.ld_gu;
+            e.act = act;
+            e.flags = kEpGated | (g.hdtype == TSL_BF16 ? kEpPreBf16 : 0);
+            v[2 * i].ep = &e;
+            kept = kept || g.G;
+        }
+        if (M > 0 && kept && epilogue_clash(v, xdtype == TSL_F32 ? 4 : 2))
+            return TSL_ERR_INVALID_ARG;
+        return run_group(v, wdtype, M, workspace, ws_bytes, stream);
     });
 }
 

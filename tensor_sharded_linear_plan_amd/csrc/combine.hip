@@ -7,6 +7,7 @@
 // one thread per 4 columns (SUM) or per 16 bytes (CONCAT), rows over
 // blockIdx.y.  The sum runs in ascending rank order in binary32.
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "internal.hpp"
 
 namespace tsl {
@@ -125,7 +126,7 @@ struct SumSet {
     int32_t n_parts, y_bf16;
     int32_t start, pad_; // first workgroup of the set
 };
-struct SumSets {
+struct SumSets : Epilogues<kMaxSets> {
     int32_t n, pad_;
     SumSet s[kMaxSets];
 };
@@ -163,12 +164,31 @@ __global__ void __launch_bounds__(256) sum_sets_kernel(SumSets g) {
                 return v;
             };
             f32x4 acc = product(0);
+            if constexpr (kEpilogue) {
+                const Epilogue &e = g.ep(lo);
+                if (e.flags & kEpGated) {
+                    const f32x4 u = product(1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i] = ep_gate(e, acc[i], u[i], m, j + i);
+                    if (st.y_bf16)
+                        store4(static_cast<uint16_t *>(st.Y) + m * st.ldy + j, acc);
+                    else
+                        store4(static_cast<float *>(st.Y) + m * st.ldy + j, acc);
+                    continue;
+                }
+            }
             for (int r = 1; r < st.n_parts; ++r) {
                 const f32x4 v = product(r);
                 acc.x = acc.x + v.x;
                 acc.y = acc.y + v.y;
                 acc.z = acc.z + v.z;
                 acc.w = acc.w + v.w;
+            }
+            if constexpr (kEpilogue) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = ep_apply(g.ep(lo), acc[i], m, j + i);
             }
             if (st.y_bf16)
                 store4(static_cast<uint16_t *>(st.Y) + m * st.ldy + j, acc);
@@ -182,8 +202,18 @@ __global__ void __launch_bounds__(256) sum_sets_kernel(SumSets g) {
                 return v;
             };
             float acc = product(0);
-            for (int r = 1; r < st.n_parts; ++r)
+            bool gated = false;
+            if constexpr (kEpilogue) {
+                gated = (g.ep(lo).flags & kEpGated) != 0;
+                if (gated)
+                    acc = ep_gate(g.ep(lo), acc, product(1), m, j);
+            }
+            for (int r = 1; r < st.n_parts && !gated; ++r)
                 acc = acc + product(r);
+            if constexpr (kEpilogue) {
+                if (!gated)
+                    acc = ep_apply(g.ep(lo), acc, m, j);
+            }
             if (st.y_bf16)
                 store1(static_cast<uint16_t *>(st.Y) + m * st.ldy + j, acc);
             else
@@ -362,6 +392,7 @@ hipError_t launch_sum_sets(int n_sets, const SumSpec *sets, int64_t M, hipStream
             st.n = sp.n;
             st.M = sp.M;
             st.n_parts = sp.n_parts;
+            g.set_ep(i, sp.ep);
             st.y_bf16 = sp.ydtype == TSL_BF16;
             st.start = (int32_t)blocks;
             blocks += (sp.n + 256 * (vec ? 4 : 1) - 1) / (256 * (vec ? 4 : 1));

@@ -230,6 +230,13 @@ inline std::vector<LinearItem> launch_order(const std::vector<LinearItem> &items
     return v;
 }
 
+// A set of two whose results the gate combines (act(X W_0) * (X W_1)).
+inline bool gated(const LinearItem &L) { return L.ep && (L.ep->flags & kEpGated); }
+
+// Whether a lone product's own kernel applies its epilogue (unless it splits
+// k: then the sum launch that adds its k-partials does).
+inline bool fused_epilogue(const LinearItem &, tsl_dtype, int64_t) { return false; }
+
 // The GEMM regime: a sum set whose members have equal k-ranges becomes one
 // product over the members' k-ranges laid end to end in set order,
 // Y = [X_0 X_1 ...] [W_0; W_1; ...] -- the rank sum accumulated inside the
@@ -251,7 +258,7 @@ inline std::vector<LinearItem> concat_sets(const std::vector<LinearItem> &in, ts
     out.reserve(in.size());
     for (size_t i = 0; i < in.size();) {
         const size_t len = in[i].set_len;
-        bool join = len > 1 && len <= (size_t)kSetParts &&
+        bool join = len > 1 && len <= (size_t)kSetParts && !gated(in[i]) &&
                     (int64_t)len * in[i].g.Kpad < kPrefillMaxStride;
         for (size_t r = 0; join && r < len; ++r)
             join = in[i + r].g.Ks % unit == 0 && in[i + r].g.Ks == in[i].g.Ks &&
@@ -296,18 +303,21 @@ inline std::vector<LinearItem> concat_sets(const std::vector<LinearItem> &in, ts
 // Rewrites every sum set of *items into lone items writing binary32
 // partials at ws, ws + ...; returns the bytes used.  Call it once: the
 // items it leaves are no longer sets.  With ws == nullptr the partials'
-// addresses are null (for sizing; such items are never launched).
-inline size_t split_sets(std::vector<LinearItem> *items, int64_t M, char *ws) {
+// addresses are null (for sizing; such items are never launched).  A lone
+// product whose kernel does not apply its epilogue is a set of one here.
+inline size_t split_sets(std::vector<LinearItem> *items, tsl_dtype wdtype, int64_t M, char *ws) {
     size_t off = 0;
     for (size_t i = 0; i < items->size();) {
         const size_t len = (*items)[i].set_len;
-        if (len > 1) {
+        if (len > 1 || ((*items)[i].ep && !fused_epilogue((*items)[i], wdtype, M))) {
             void *const sY = (*items)[i].Y;
             const int64_t sldy = (*items)[i].ldy;
             const tsl_dtype sy = (*items)[i].ydtype;
+            // sets with an epilogue are added by the sum launch
+            const int flen = (*items)[i].ep || len < 2 ? 0 : (int)len;
             for (size_t r = 0; r < len; ++r) {
                 LinearItem &L = (*items)[i + r];
-                L.fset_len = (int)len;
+                L.fset_len = flen;
                 L.fset_pos = (int)r;
                 L.fset_Y = sY;
                 L.fset_ldy = sldy;
@@ -318,6 +328,7 @@ inline size_t split_sets(std::vector<LinearItem> *items, int64_t M, char *ws) {
                 L.accumulate = 0;
                 L.set_len = 1;
                 L.set_pos = 0;
+                L.ep = nullptr; // the set's first item keeps it in the caller's list
                 L.no_split = len > (size_t)kSetParts; // summed by launch_combine_sum
 
                 off += ((size_t)L.M * (size_t)L.g.Ns * 4 + 255) / 256 * 256;
@@ -381,7 +392,7 @@ inline size_t group_workspace(const std::vector<LinearItem> &in, tsl_dtype wdtyp
     std::vector<RowGather> jobs;
     const size_t gathered = plan_row_gathers(&src, wdtype, M, nullptr, &jobs);
     std::vector<LinearItem> items = launch_order(concat_sets(src, wdtype, M));
-    const size_t parts = split_sets(&items, M, nullptr);
+    const size_t parts = split_sets(&items, wdtype, M, nullptr);
     if (use_skinny(wdtype, M))
         return gathered + parts + skinny_plan(items.data(), (int)items.size(), wdtype, M).ws_bytes;
     return gathered + parts + prefill_plan(items.data(), (int)items.size(), wdtype, M).ws_bytes;
@@ -400,7 +411,7 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
     char *ws = ws0 ? ws0 + gathered : nullptr; // the rank partials, then the plan's
     const std::vector<LinearItem> ordered = launch_order(concat_sets(src, wdtype, M));
     std::vector<LinearItem> items = ordered;
-    const size_t parts = split_sets(&items, M, ws);
+    const size_t parts = split_sets(&items, wdtype, M, ws);
     const int n = (int)items.size();
     hipStream_t s = static_cast<hipStream_t>(stream);
     size_t need;
@@ -456,16 +467,19 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
     std::vector<SumSpec> sums;
     for (size_t i = 0; i < ordered.size();) {
         const size_t len = ordered[i].set_len;
-        if (len == 1 && kcount(i) > 1) { // a lone product: its k-partials into its Y
+        // a lone product: its k-partials (or, its epilogue still to come, its
+        // binary32 result) into its Y
+        if (len == 1 && (kcount(i) > 1 || (ordered[i].ep && !items[i].ep))) {
             SumSpec sp1;
             sp1.parts[0] = kparts(i);
             sp1.ks[0] = kcount(i);
             sp1.n_parts = 1;
             sp1.M = items[i].M;
             sp1.n = items[i].g.Ns;
-            sp1.Y = items[i].Y;
-            sp1.ldy = items[i].ldy;
-            sp1.ydtype = items[i].ydtype;
+            sp1.Y = ordered[i].Y;
+            sp1.ldy = ordered[i].ldy;
+            sp1.ydtype = ordered[i].ydtype;
+            sp1.ep = ordered[i].ep;
             sums.push_back(sp1);
         }
         i += len;
@@ -487,17 +501,25 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
             const float *p[kMaxParts];
             for (int r = 0; r < L.set_len; ++r)
                 p[r] = static_cast<const float *>(items[i + r].Y);
-            e = launch_combine_sum(L.set_len, p, L.M, L.g.Ns, L.g.Ns, L.ydtype, L.Y, L.ldy, s);
+            // with an epilogue: added into the first partial, which then goes
+            // through it
+            if (L.ep)
+                e = launch_combine_sum(L.set_len, p, L.M, L.g.Ns, L.g.Ns, TSL_F32, items[i].Y,
+                                       L.g.Ns, s);
+            else
+                e = launch_combine_sum(L.set_len, p, L.M, L.g.Ns, L.g.Ns, L.ydtype, L.Y, L.ldy, s);
             if (e != hipSuccess)
                 return from_hip(e);
-            continue;
+            if (!L.ep)
+                continue;
         }
         SumSpec sp;
-        for (int r = 0; r < L.set_len; ++r) {
+        sp.n_parts = L.set_len > kSetParts ? 1 : L.set_len;
+        for (int r = 0; r < sp.n_parts; ++r) {
             sp.parts[r] = kparts(i + r);
             sp.ks[r] = kcount(i + r);
         }
-        sp.n_parts = L.set_len;
+        sp.ep = L.ep;
         sp.M = L.M;
         sp.n = L.g.Ns;
         sp.Y = L.Y;

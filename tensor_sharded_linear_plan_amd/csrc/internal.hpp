@@ -40,6 +40,28 @@ constexpr int kQ4PairsAt = 1024;
 constexpr int kWeightExpBias = 14;
 constexpr int kActExpBias = 15;
 
+// The GEMM, streaming and sum sources are compiled twice: plain for
+// libtsl.so, and with an epilogue on every product (TSL_EPILOGUE 1) for
+// libtsl_block.so.  The plain build's kernels carry nothing of it.
+#ifndef TSL_EPILOGUE
+#define TSL_EPILOGUE 0
+#endif
+constexpr bool kEpilogue = TSL_EPILOGUE != 0;
+
+// What happens to a product's binary32 result v (row m, column n) before it
+// is rounded and stored: act(v + bias[n]) + residual[m][n], or, gated,
+// act(g) * u of the results of two weights.  pre (and pre2) receive the
+// value that enters the activation (and u), for a backward pass.
+struct Epilogue {
+    const void *bias = nullptr;
+    const void *res = nullptr;
+    void *pre = nullptr, *pre2 = nullptr;
+    int64_t ldr = 0, ldp = 0;
+    int32_t act = 0;   // tsl_act
+    int32_t flags = 0; // kEp*
+};
+constexpr int kEpBiasBf16 = 1, kEpResBf16 = 2, kEpPreBf16 = 4, kEpGated = 8;
+
 // ---- pack.hip ----
 hipError_t launch_pack_dense(const PackGeom &g, tsl_dtype wdtype, const void *W, int64_t stride_k,
                              int64_t stride_n, int64_t k_off, int64_t n_off, void *packed,
@@ -73,6 +95,7 @@ struct SumSpec {
     void *Y = nullptr;
     int64_t ldy = 0;
     tsl_dtype ydtype = TSL_F32;
+    const Epilogue *ep = nullptr; // applied to the sum (gated: to the two products)
 };
 hipError_t launch_sum_sets(int n_sets, const SumSpec *sets, int64_t M, hipStream_t stream);
 // Every rank's result of a collective (combine_to_ranks in tsl.h):
@@ -159,6 +182,9 @@ struct LinearItem {
     // the GEMM path may not split this product's k (a member of a sum set
     // too long for one sum launch)
     bool no_split = false;
+    // what its set's (or its own) result goes through; null: nothing.  A
+    // gated pair is a set of two whose results are combined by the gate
+    const Epilogue *ep = nullptr;
     // member fset_pos of a sum set of fset_len products that split_sets
     // turned into lone items (0: none), and the set's own output
     int fset_len = 0, fset_pos = 0;
