@@ -2,7 +2,8 @@
  * tsl_block.h -- what lies between and around the shard products of tsl.h in
  * a transformer layer, on one AMD Instinct MI355X (gfx950): the
  * residual-adding root-mean-square norm, shard products with an epilogue
- * (bias, activation, residual), and the gated feed-forward block.
+ * (bias, activation, residual), the gated feed-forward block, and their
+ * backward passes.
  *
  * A library of its own (libtsl_block.so) beside libtsl.so: the same types,
  * status codes, packed weights (pack_shard) and shard plans, and the same
@@ -206,6 +207,88 @@ tsl_status shard_gated_group_workspace_size(int32_t n_items, const tsl_gated_ite
 tsl_status shard_gated_group(int32_t n_items, const tsl_gated_item *items, tsl_act act,
                              tsl_dtype wdtype, tsl_dtype xdtype, int64_t M, void *workspace,
                              size_t ws_bytes, void *stream);
+
+/*
+ * transpose_shard -- the shard of W^T that a shard of W is: K and N, the
+ * offsets and lengths change places, a column shard becomes a row shard
+ * (combine SUM: the ranks' input gradients add up) and a row shard a column
+ * shard (CONCAT).  Packing it with the strides of W swapped,
+ *     pack_shard(&t, wdtype, W, stride_n, stride_k, ...),
+ * gives the weight that the backward pass reads.  Host only.
+ */
+tsl_status transpose_shard(const tsl_shard *shard, tsl_shard *out);
+
+/* shard_linear_grad_workspace_size -- workspace bytes shard_linear_grad needs
+ * at most for this shard, weight type and row count, whatever outputs are
+ * wanted. */
+tsl_status shard_linear_grad_workspace_size(const tsl_shard *shard, tsl_dtype wdtype, int64_t M,
+                                            size_t *bytes);
+
+/*
+ * shard_linear_grad -- the backward pass of one rank's shard product with an
+ * epilogue, Y = act(Z) + residual, Z = X W + bias (the residual's gradient is
+ * dY itself).  With dZ = dY act'(Z):
+ *     dX[m][i] = sum_j dZ[m][j] W[i][j]            i < k_len, j < n_len
+ *     dW[i][j] (+)= sum_m X[m][i] dZ[m][j]
+ *     db[j] (+)= sum_m dZ[m][j]
+ * For a column shard dX is the rank's partial of the input gradient (the
+ * ranks' partials add up, combine_partials SUM).
+ *   shard:    the forward's shard; wdtype F32 or BF16 (4-bit weights are
+ *             TSL_ERR_UNSUPPORTED: their groups run along the other axis).
+ *   packed_t: the transposed shard, packed (transpose_shard); not read when
+ *             dX is null.
+ *   X, Z, dY: DEVICE rows of wdtype at strides ldx, ldz, lddy (as
+ *             shard_linear's X: 16-byte aligned, strides whole 16 bytes).  Z
+ *             is the kept pre-activation (tsl_epilogue.pre), not read for
+ *             TSL_ACT_NONE; X is not read when dW is null.
+ *   dX:       null, or DEVICE [M][k_len], row stride lddx, F32 or BF16.
+ *   dW:       null, or DEVICE, type dwdtype (F32 or BF16): element (i, j) at
+ *             i * dw_stride_k + j * dw_stride_n, one of the strides 1 (a
+ *             [K][N] or an [N][K] array).  accumulate_dw 1 (F32 only) adds to
+ *             it, and to db.
+ *   db:       null, or DEVICE binary32 [n_len], summed from the unrounded dZ
+ *             in a fixed order.
+ * Products accumulate in binary32; with an activation dZ is their operand
+ * rounded once to wdtype.  Slope of relu at 0 is 0.  M == 0 writes zero
+ * weight and bias gradients (unless they accumulate).  M, k_len, n_len and
+ * input strides below 2^22.  No output may share an element with an input,
+ * another output or the workspace.  Errors as shard_linear.
+ */
+tsl_status shard_linear_grad(const tsl_shard *shard, tsl_dtype wdtype, const void *packed_t,
+                             size_t packed_t_bytes, int64_t M, const void *X, int64_t ldx,
+                             tsl_act act, const void *Z, int64_t ldz, const void *dY, int64_t lddy,
+                             tsl_dtype dxdtype, void *dX, int64_t lddx, tsl_dtype dwdtype, void *dW,
+                             int64_t dw_stride_k, int64_t dw_stride_n, int accumulate_dw, float *db,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/* shard_gated_grad_workspace_size -- workspace bytes shard_gated_grad needs
+ * at most for these shards, weight type and row count. */
+tsl_status shard_gated_grad_workspace_size(const tsl_shard *gate, const tsl_shard *up,
+                                           tsl_dtype wdtype, int64_t M, size_t *bytes);
+
+/*
+ * shard_gated_grad -- the backward pass of one gated feed-forward block
+ * (shard_gated_group), from the kept products G and U:
+ *     dG = dH U act'(G),  dU = dH act(G)
+ *     dX = dG W_gate^T + dU W_up^T
+ *     dW_gate (+)= X^T dG,  dW_up (+)= X^T dU
+ *   G, U:  DEVICE [M][n_len] of wdtype, row stride ld_gu.
+ *   dH:    DEVICE [M][n_len] of wdtype, row stride lddh.
+ *   packed_gate_t, packed_up_t: the transposed shards, packed; packed_t_bytes
+ *          the size of either buffer.
+ *   dW_gate, dW_up: both or neither, with the strides of shard_linear_grad's
+ *          dW.
+ * dG and dU are the products' operands, rounded once to wdtype; the two
+ * terms of dX are added in binary32.  Everything else as shard_linear_grad.
+ */
+tsl_status shard_gated_grad(const tsl_shard *gate, const tsl_shard *up, tsl_dtype wdtype,
+                            const void *packed_gate_t, const void *packed_up_t,
+                            size_t packed_t_bytes, int64_t M, const void *X, int64_t ldx,
+                            tsl_act act, const void *G, const void *U, int64_t ld_gu,
+                            const void *dH, int64_t lddh, tsl_dtype dxdtype, void *dX, int64_t lddx,
+                            tsl_dtype dwdtype, void *dW_gate, void *dW_up, int64_t dw_stride_k,
+                            int64_t dw_stride_n, int accumulate_dw, void *workspace,
+                            size_t ws_bytes, void *stream);
 
 /* The HIP runtime's description of the error behind the most recent
  * TSL_ERR_HIP an entry point of this header returned on the calling thread

@@ -195,6 +195,17 @@ _block.shard_gated_group_workspace_size.argtypes = [_i32, _P_GATED, ctypes.c_int
                                                     ctypes.POINTER(_sz)]
 _block.shard_gated_group.argtypes = [_i32, _P_GATED, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64,
                                      _vp, _sz, _vp]
+_block.transpose_shard.argtypes = [_P_SHARD, _P_SHARD]
+_block.shard_linear_grad_workspace_size.argtypes = [_P_SHARD, ctypes.c_int, _i64,
+                                                    ctypes.POINTER(_sz)]
+_block.shard_linear_grad.argtypes = [_P_SHARD, ctypes.c_int, _vp, _sz, _i64, _vp, _i64, ctypes.c_int,
+                                     _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i64, ctypes.c_int,
+                                     _vp, _i64, _i64, ctypes.c_int, _vp, _vp, _sz, _vp]
+_block.shard_gated_grad_workspace_size.argtypes = [_P_SHARD, _P_SHARD, ctypes.c_int, _i64,
+                                                   ctypes.POINTER(_sz)]
+_block.shard_gated_grad.argtypes = [_P_SHARD, _P_SHARD, ctypes.c_int, _vp, _vp, _sz, _i64, _vp, _i64,
+                                    ctypes.c_int, _vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i64,
+                                    ctypes.c_int, _vp, _vp, _i64, _i64, ctypes.c_int, _vp, _sz, _vp]
 _block.tsl_block_last_hip_error_string.argtypes = []
 _block.tsl_block_last_hip_error_string.restype = ctypes.c_char_p
 
@@ -202,6 +213,8 @@ _block.tsl_block_last_hip_error_string.restype = ctypes.c_char_p
 BLOCK_EXPORTS = ("add_rms_norm", "add_rms_norm_grad_workspace_size", "add_rms_norm_grad",
                  "shard_linear_group_epilogue_workspace_size", "shard_linear_group_epilogue",
                  "shard_gated_group_workspace_size", "shard_gated_group",
+                 "transpose_shard", "shard_linear_grad_workspace_size", "shard_linear_grad",
+                 "shard_gated_grad_workspace_size", "shard_gated_grad",
                  "tsl_block_last_hip_error_string")
 for _f in BLOCK_EXPORTS[:-1]:
     getattr(_block, _f).restype = ctypes.c_int
@@ -477,3 +490,45 @@ def shard_gated_group(items, act, wdtype, xdtype, M, workspace=None, ws_bytes=0,
     arr, n = _gated(items)
     _check(_block.shard_gated_group(n, arr, act, wdtype, xdtype, M, _ptr(workspace), ws_bytes,
                                     _stream(stream)), "shard_gated_group")
+
+
+def transpose_shard(shard):
+    out = Shard()
+    _check(_block.transpose_shard(ctypes.byref(shard), ctypes.byref(out)), "transpose_shard")
+    return out
+
+
+def shard_linear_grad_workspace_size(shard, wdtype, M):
+    b = _sz(0)
+    _check(_block.shard_linear_grad_workspace_size(ctypes.byref(shard), wdtype, M, ctypes.byref(b)),
+           "shard_linear_grad_workspace_size")
+    return b.value
+
+
+def shard_linear_grad(shard, wdtype, packed_t, packed_t_bytes, M, X, ldx, act, Z, ldz, dY, lddy,
+                      dxdtype, dX, lddx, dwdtype, dW, dw_stride_k, dw_stride_n, accumulate_dw=0,
+                      db=None, workspace=None, ws_bytes=0, stream=None):
+    _check(_block.shard_linear_grad(ctypes.byref(shard), wdtype, _ptr(packed_t), packed_t_bytes, M,
+                                    _ptr(X), ldx, act, _ptr(Z), ldz, _ptr(dY), lddy, dxdtype,
+                                    _ptr(dX), lddx, dwdtype, _ptr(dW), dw_stride_k, dw_stride_n,
+                                    accumulate_dw, _ptr(db), _ptr(workspace), ws_bytes,
+                                    _stream(stream)), "shard_linear_grad")
+
+
+def shard_gated_grad_workspace_size(gate, up, wdtype, M):
+    b = _sz(0)
+    _check(_block.shard_gated_grad_workspace_size(ctypes.byref(gate), ctypes.byref(up), wdtype, M,
+                                                  ctypes.byref(b)),
+           "shard_gated_grad_workspace_size")
+    return b.value
+
+
+def shard_gated_grad(gate, up, wdtype, packed_gate_t, packed_up_t, packed_t_bytes, M, X, ldx, act, G,
+                     U, ld_gu, dH, lddh, dxdtype, dX, lddx, dwdtype, dW_gate, dW_up, dw_stride_k,
+                     dw_stride_n, accumulate_dw=0, workspace=None, ws_bytes=0, stream=None):
+    _check(_block.shard_gated_grad(ctypes.byref(gate), ctypes.byref(up), wdtype, _ptr(packed_gate_t),
+                                   _ptr(packed_up_t), packed_t_bytes, M, _ptr(X), ldx, act, _ptr(G),
+                                   _ptr(U), ld_gu, _ptr(dH), lddh, dxdtype, _ptr(dX), lddx, dwdtype,
+                                   _ptr(dW_gate), _ptr(dW_up), dw_stride_k, dw_stride_n,
+                                   accumulate_dw, _ptr(workspace), ws_bytes, _stream(stream)),
+           "shard_gated_grad")

@@ -475,6 +475,453 @@ extern "C" tsl_status shard_gated_group(int32_t n_items, const tsl_gated_item *i
     });
 }
 
+extern "C" tsl_status transpose_shard(const tsl_shard *shard, tsl_shard *out) {
+    if (!out)
+        return TSL_ERR_INVALID_ARG;
+    tsl_status st = check_shard(shard);
+    if (st != TSL_OK)
+        return st;
+    tsl_shard t = *shard;
+    t.K = shard->N;
+    t.N = shard->K;
+    t.k_off = shard->n_off;
+    t.k_len = shard->n_len;
+    t.n_off = shard->k_off;
+    t.n_len = shard->k_len;
+    if (shard->strategy == TSL_COLUMN) {
+        t.strategy = TSL_ROW;
+        t.combine = TSL_COMBINE_SUM;
+    } else if (shard->strategy == TSL_ROW) {
+        t.strategy = TSL_COLUMN;
+        t.combine = TSL_COMBINE_CONCAT;
+    }
+    *out = t;
+    return TSL_OK;
+}
+
+namespace {
+
+// The backward pass of one weight (linear: n_w 1) or of a gated pair (2).
+struct GradCall {
+    const tsl_shard *shard[2] = {};
+    int n_w = 1;
+    const void *packed_t[2] = {};
+    size_t packed_t_bytes = 0;
+    tsl_dtype wdtype = TSL_BF16;
+    int64_t M = 0;
+    const void *X = nullptr;
+    int64_t ldx = 0;
+    int act = 0;
+    // linear: a = dY, b = Z (null without an activation); gated: dH, G, U
+    const void *a = nullptr, *b = nullptr, *c = nullptr;
+    int64_t lda = 0, ldb = 0;
+    int dxdtype = 0, dwdtype = 0;
+    void *dX = nullptr;
+    int64_t lddx = 0;
+    void *dW[2] = {};
+    int64_t sk = 0, sn = 0;
+    int accumulate = 0;
+    float *db = nullptr;
+};
+
+// Workspace parts of a call and the products it runs.  Everything but the
+// addresses follows from the shapes and from which outputs are wanted.
+struct GradPlan {
+    size_t row[2] = {}, tr[2] = {}, xt = 0, part = 0, products = 0, total = 0;
+    int64_t K = 0, N = 0, Mp = 0, Np = 0;
+    bool need_row = false, need_tr = false;
+};
+
+bool nk_order(const GradCall &c) { return c.sk == 1 && c.sn != 1; }
+
+// The products of a call: dX (a set of n_w), then dW of each weight, with
+// the operands of `p` at ws (null: sizing).
+void grad_items(const GradCall &c, const GradPlan &p, const PackGeom &gt, char *ws,
+                std::vector<LinearItem> *dx, std::vector<LinearItem> *dw) {
+    auto at = [&](size_t off) { return ws ? ws + off : nullptr; };
+    if (c.dX)
+        for (int q = 0; q < c.n_w; ++q) {
+            LinearItem L;
+            L.g = gt;
+            L.M = c.M;
+            L.packed = c.packed_t[q];
+            L.X = p.need_row ? at(p.row[q]) : c.a;
+            L.ldx = p.need_row ? p.Np : c.lda;
+            // the copy's columns are zero up to Np, as the packed rows are
+            if (p.need_row)
+                L.g.Ks = p.Np;
+            L.Y = q == 0 ? c.dX : nullptr;
+            L.ldy = q == 0 ? c.lddx : 0;
+            L.ydtype = (tsl_dtype)c.dxdtype;
+            L.set_len = q == 0 ? c.n_w : 0;
+            L.set_pos = q;
+            dx->push_back(L);
+        }
+    if (!c.dW[0])
+        return;
+    for (int q = 0; q < c.n_w; ++q) {
+        LinearItem L;
+        const bool nk = nk_order(c);
+        const int64_t cols = nk ? p.K : p.N;
+        L.g.Ks = L.g.Kpad = p.Mp;
+        L.g.Ns = cols;
+        L.g.Nt = (cols + 15) / 16;
+        L.g.KT = p.Mp / (c.wdtype == TSL_F32 ? 16 : 32);
+        L.M = nk ? p.N : p.K;
+        L.X = at(nk ? p.tr[q] : p.xt);
+        L.packed = at(nk ? p.xt : p.tr[q]);
+        L.ldx = p.Mp;
+        L.Y = c.dW[q];
+        L.ldy = nk ? c.sn : c.sk;
+        L.ydtype = (tsl_dtype)c.dwdtype;
+        L.accumulate = c.accumulate;
+        dw->push_back(L);
+    }
+}
+
+// dX and dW share a launch where both take the same kernels.
+bool one_group(const GradCall &c, const GradPlan &p) {
+    return c.dX && c.dW[0] &&
+           use_skinny(c.wdtype, c.M) == use_skinny(c.wdtype, nk_order(c) ? p.N : p.K);
+}
+
+// Fills the plan; gt receives the geometry of the packed transposed weight.
+tsl_status plan_grad(const GradCall &c, GradPlan *p, PackGeom *gt) {
+    for (int q = 0; q < c.n_w; ++q) {
+        tsl_shard t;
+        tsl_status st = transpose_shard(c.shard[q], &t);
+        if (st == TSL_OK)
+            st = geometry(t, c.wdtype, gt);
+        if (st != TSL_OK)
+            return st;
+        if (q > 0 && (gt->Ns != p->K || gt->Ks != p->N))
+            return TSL_ERR_INVALID_ARG;
+        p->K = gt->Ns;
+        p->N = gt->Ks;
+    }
+    if (c.M >= kPrefillMaxStride - 64 || p->K >= kPrefillMaxStride - 64 ||
+        p->N >= kPrefillMaxStride - 64)
+        return TSL_ERR_UNSUPPORTED;
+    // every launch's workgroups stay countable (kMaxBlocks): tiles of at least
+    // 64 x 64 (binary32: 16 x 64) elements
+    const int64_t most = int64_t(1) << (c.wdtype == TSL_F32 ? 32 : 34);
+    if (p->K * p->N > most || c.M * p->K > most || c.M * p->N > most)
+        return TSL_ERR_UNSUPPORTED;
+    p->Mp = (c.M + 63) / 64 * 64;
+    p->Np = (p->N + 63) / 64 * 64;
+    const size_t e = c.wdtype == TSL_F32 ? 4 : 2;
+    // without an activation dY itself feeds dX
+    p->need_row = c.dX && (c.n_w > 1 || c.act != TSL_ACT_NONE);
+    p->need_tr = c.dW[0] != nullptr;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round_up(bytes, 256);
+        return at;
+    };
+    const auto tr_cols = [&](int64_t n, bool packed) {
+        return (size_t)(packed ? (n + 15) / 16 * 16 : n);
+    };
+    for (int q = 0; q < c.n_w; ++q) {
+        if (p->need_row)
+            p->row[q] = take((size_t)c.M * p->Np * e);
+        if (p->need_tr)
+            p->tr[q] = take(tr_cols(p->N, !nk_order(c)) * p->Mp * e);
+    }
+    if (p->need_tr)
+        p->xt = take(tr_cols(p->K, nk_order(c)) * p->Mp * e);
+    if (c.db)
+        p->part = take((size_t)(p->Mp / 64) * ((p->N + 7) / 8 * 8) * 4);
+    p->products = off;
+    std::vector<LinearItem> dx, dw;
+    grad_items(c, *p, *gt, nullptr, &dx, &dw);
+    if (c.M > 0) {
+        const int64_t rows = nk_order(c) ? p->N : p->K;
+        if (one_group(c, *p)) {
+            dx.insert(dx.end(), dw.begin(), dw.end());
+            off += group_workspace(dx, c.wdtype, c.M > rows ? c.M : rows);
+        } else { // one after the other: they share the space
+            const size_t a = dx.empty() ? 0 : group_workspace(dx, c.wdtype, c.M);
+            const size_t b = dw.empty() ? 0 : group_workspace(dw, c.wdtype, rows);
+            off += a > b ? a : b;
+        }
+    }
+    p->total = off;
+    return TSL_OK;
+}
+
+// No rows: the gradients of the weights and of the bias are zero.
+tsl_status zero_rows(const GradCall &c, const GradPlan &p, hipStream_t s) {
+    if (c.accumulate)
+        return TSL_OK;
+    for (int q = 0; q < c.n_w; ++q)
+        if (c.dW[q]) {
+            const hipError_t e = launch_zero_rows(c.dW[q], nk_order(c) ? p.N : p.K,
+                                                  nk_order(c) ? p.K : p.N,
+                                                  nk_order(c) ? c.sn : c.sk,
+                                                  c.dwdtype == TSL_BF16, s);
+            if (e != hipSuccess)
+                return from_hip(e);
+        }
+    return c.db ? from_hip(launch_column_sum(nullptr, 0, p.N, c.db, 0, s)) : TSL_OK;
+}
+
+tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *stream) {
+    const bool f32 = c.wdtype == TSL_F32;
+    const size_t e = f32 ? 4 : 2;
+    if (c.M < 0 || !valid_act(c.act) || (c.accumulate != 0 && c.accumulate != 1))
+        return TSL_ERR_INVALID_ARG;
+    if (c.wdtype != TSL_F32 && c.wdtype != TSL_BF16)
+        return c.wdtype == TSL_Q4G64 ? TSL_ERR_UNSUPPORTED : TSL_ERR_INVALID_ARG;
+    if (!c.dX && !c.dW[0] && !c.db)
+        return TSL_ERR_INVALID_ARG;
+    for (int q = 0; q < c.n_w; ++q)
+        if (!c.shard[q] || (c.dX && !c.packed_t[q]) || (c.n_w == 2 && !c.dW[0] != !c.dW[1]))
+            return TSL_ERR_INVALID_ARG;
+    if (!c.a || (c.dW[0] && !c.X) || (c.n_w == 2 ? !c.b || !c.c : !c.b && c.act != TSL_ACT_NONE))
+        return TSL_ERR_INVALID_ARG;
+    GradPlan p;
+    PackGeom gt;
+    tsl_status st = plan_grad(c, &p, &gt);
+    if (st != TSL_OK)
+        return st;
+    const int64_t K = p.K, N = p.N, M = c.M;
+    const bool uses_b = c.n_w == 2 || c.act != TSL_ACT_NONE;
+    const bool nk = nk_order(c);
+    if (c.lda < N || (uses_b && c.ldb < N) || (c.dW[0] && c.ldx < K) || (c.dX && c.lddx < K))
+        return TSL_ERR_INVALID_ARG;
+    if ((c.dX && !dense_type(c.dxdtype)) || (c.dW[0] && !dense_type(c.dwdtype)))
+        return TSL_ERR_INVALID_ARG;
+    if (c.dW[0] && !((c.sn == 1 && c.sk >= N) || (c.sk == 1 && c.sn >= K)))
+        return TSL_ERR_INVALID_ARG;
+    if (c.dW[0] && c.accumulate && c.dwdtype != TSL_F32)
+        return TSL_ERR_UNSUPPORTED;
+    if (c.lda >= kPrefillMaxStride || c.ldx >= kPrefillMaxStride || c.ldb >= kPrefillMaxStride ||
+        c.lddx >= kMaxLd || c.sk >= kMaxLd || c.sn >= kMaxLd)
+        return TSL_ERR_UNSUPPORTED;
+    if (c.dX && c.packed_t_bytes < gt.total_bytes)
+        return TSL_ERR_BUFFER_TOO_SMALL;
+    const int64_t xa = f32 ? 4 : 8;
+    const size_t dxe = elem(c.dxdtype), dwe = elem(c.dwdtype);
+    if (!aligned(c.a, 16) || c.lda % xa || (uses_b && (!aligned(c.b, 16) || c.ldb % xa)) ||
+        !aligned(c.c, 16) || (c.dW[0] && (!aligned(c.X, 16) || c.ldx % xa)) ||
+        (c.dX && !aligned(c.dX, dxe)) || !aligned(c.db, 4))
+        return TSL_ERR_MISALIGNED;
+    for (int q = 0; q < c.n_w; ++q)
+        if ((c.dX && !aligned(c.packed_t[q], 256)) || (c.dW[q] && !aligned(c.dW[q], dwe)))
+            return TSL_ERR_MISALIGNED;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.total > 0) {
+        if (!workspace || ws_bytes < p.total)
+            return TSL_ERR_BUFFER_TOO_SMALL;
+        if (!aligned(workspace, 256))
+            return TSL_ERR_MISALIGNED;
+    }
+    std::vector<Mat> ins = {{c.a, M, N, c.lda, e},
+                            {uses_b ? c.b : nullptr, M, N, c.ldb, e},
+                            {c.c, M, N, c.ldb, e},
+                            {c.dW[0] ? c.X : nullptr, M, K, c.ldx, e}};
+    std::vector<Mat> outs = {{c.dX, M, K, c.lddx, dxe}, {c.db, 1, N, N, 4}};
+    for (int q = 0; q < c.n_w; ++q) {
+        outs.push_back(Mat{c.dW[q], nk ? N : K, nk ? K : N, nk ? c.sn : c.sk, dwe});
+        if (c.dX)
+            ins.push_back(Mat{c.packed_t[q], 1, (int64_t)gt.total_bytes, (int64_t)gt.total_bytes, 1});
+    }
+    if (p.total > 0)
+        outs.push_back(Mat{workspace, 1, (int64_t)p.total, (int64_t)p.total, 1});
+    if (any_clash(outs, ins))
+        return TSL_ERR_INVALID_ARG;
+    if (M == 0)
+        return zero_rows(c, p, s);
+    char *ws = static_cast<char *>(workspace);
+    // 1. the operands
+    GradJob jobs[kGradJobs];
+    int n_jobs = 0;
+    if (p.need_row || p.need_tr || c.db) {
+        GradJob &j = jobs[n_jobs++];
+        j.kind = c.n_w == 2 ? kGradGated : (c.act != TSL_ACT_NONE ? kGradAct : kGradCopy);
+        j.a = c.a;
+        j.b = c.b;
+        j.c = c.c;
+        j.lda = c.lda;
+        j.ldb = j.ldc = c.ldb;
+        j.act = c.act;
+        j.ld_row = p.Np;
+        j.packed = !nk;
+        for (int q = 0; q < c.n_w; ++q) {
+            j.row[q] = p.need_row ? ws + p.row[q] : nullptr;
+            j.tr[q] = p.need_tr ? ws + p.tr[q] : nullptr;
+        }
+        j.part = c.db ? reinterpret_cast<float *>(ws + p.part) : nullptr;
+        j.M = M;
+        j.N = N;
+    }
+    if (p.need_tr) {
+        GradJob &j = jobs[n_jobs++];
+        j.a = c.X;
+        j.lda = c.ldx;
+        j.tr[0] = ws + p.xt;
+        j.packed = nk;
+        j.M = M;
+        j.N = K;
+    }
+    int64_t blocks = 0;
+    for (int i = 0; i < n_jobs; ++i)
+        blocks += grad_blocks(jobs[i]);
+    if (blocks > kMaxBlocks)
+        return TSL_ERR_UNSUPPORTED;
+    hipError_t he = launch_grad_rows(jobs, n_jobs, !f32, s);
+    if (he == hipSuccess && c.db)
+        he = launch_column_sum(reinterpret_cast<const float *>(ws + p.part), p.Mp / 64, N, c.db,
+                               c.accumulate, s);
+    if (he != hipSuccess)
+        return from_hip(he);
+    // 2. the products
+    std::vector<LinearItem> dx, dw;
+    grad_items(c, p, gt, ws, &dx, &dw);
+    const int64_t rows = nk ? N : K;
+    char *gws = ws + p.products;
+    const size_t gbytes = p.total - p.products;
+    if (one_group(c, p)) {
+        dx.insert(dx.end(), dw.begin(), dw.end());
+        return run_group(dx, c.wdtype, M > rows ? M : rows, gws, gbytes, stream);
+    }
+    st = dx.empty() ? TSL_OK : run_group(dx, c.wdtype, M, gws, gbytes, stream);
+    if (st != TSL_OK || dw.empty())
+        return st;
+    return run_group(dw, c.wdtype, rows, gws, gbytes, stream);
+}
+
+// A size query's call: every output wanted, an activation in between.
+tsl_status size_grad(const GradCall &in, size_t *bytes) {
+    if (in.M < 0 || !bytes)
+        return TSL_ERR_INVALID_ARG;
+    if (in.wdtype != TSL_F32 && in.wdtype != TSL_BF16)
+        return in.wdtype == TSL_Q4G64 ? TSL_ERR_UNSUPPORTED : TSL_ERR_INVALID_ARG;
+    static char any[1];
+    GradCall c = in;
+    size_t most = 0;
+    for (int order = 0; order < 2; ++order)
+        for (int mask = 1; mask < 4; ++mask)
+            for (int act = 0; act < 2; ++act) {
+                c.act = act ? TSL_ACT_SILU : TSL_ACT_NONE;
+                c.dX = mask & 1 ? any : nullptr;
+                c.dW[0] = mask & 2 ? any : nullptr;
+                c.dW[1] = c.n_w == 2 ? c.dW[0] : nullptr;
+                c.db = c.n_w == 1 ? reinterpret_cast<float *>(any) : nullptr;
+                c.sk = order ? 1 : 2;
+                c.sn = order ? 2 : 1;
+                GradPlan p;
+                PackGeom gt;
+                tsl_status st = plan_grad(c, &p, &gt);
+                if (st != TSL_OK)
+                    return st;
+                most = p.total > most ? p.total : most;
+            }
+    *bytes = most;
+    return TSL_OK;
+}
+
+} // namespace
+
+extern "C" tsl_status shard_linear_grad_workspace_size(const tsl_shard *shard, tsl_dtype wdtype,
+                                                       int64_t M, size_t *bytes) {
+    return guarded([&] {
+        GradCall c;
+        c.shard[0] = shard;
+        c.wdtype = wdtype;
+        c.M = M;
+        return size_grad(c, bytes);
+    });
+}
+
+extern "C" tsl_status shard_linear_grad(const tsl_shard *shard, tsl_dtype wdtype,
+                                        const void *packed_t, size_t packed_t_bytes, int64_t M,
+                                        const void *X, int64_t ldx, tsl_act act, const void *Z,
+                                        int64_t ldz, const void *dY, int64_t lddy,
+                                        tsl_dtype dxdtype, void *dX, int64_t lddx,
+                                        tsl_dtype dwdtype, void *dW, int64_t dw_stride_k,
+                                        int64_t dw_stride_n, int accumulate_dw, float *db,
+                                        void *workspace, size_t ws_bytes, void *stream) {
+    return guarded([&] {
+        GradCall c;
+        c.shard[0] = shard;
+        c.packed_t[0] = packed_t;
+        c.packed_t_bytes = packed_t_bytes;
+        c.wdtype = wdtype;
+        c.M = M;
+        c.X = X;
+        c.ldx = dW ? ldx : 0;
+        c.act = act;
+        c.b = act != TSL_ACT_NONE ? Z : nullptr;
+        c.ldb = act != TSL_ACT_NONE ? ldz : 0;
+        c.a = dY;
+        c.lda = lddy;
+        c.dxdtype = dxdtype;
+        c.dX = dX;
+        c.lddx = dX ? lddx : 0;
+        c.dwdtype = dwdtype;
+        c.dW[0] = dW;
+        c.sk = dW ? dw_stride_k : 0;
+        c.sn = dW ? dw_stride_n : 0;
+        c.accumulate = accumulate_dw;
+        c.db = db;
+        return run_grad(c, workspace, ws_bytes, stream);
+    });
+}
+
+extern "C" tsl_status shard_gated_grad_workspace_size(const tsl_shard *gate, const tsl_shard *up,
+                                                      tsl_dtype wdtype, int64_t M, size_t *bytes) {
+    return guarded([&] {
+        GradCall c;
+        c.shard[0] = gate;
+        c.shard[1] = up;
+        c.n_w = 2;
+        c.wdtype = wdtype;
+        c.M = M;
+        return size_grad(c, bytes);
+    });
+}
+
+extern "C" tsl_status shard_gated_grad(const tsl_shard *gate, const tsl_shard *up, tsl_dtype wdtype,
+                                       const void *packed_gate_t, const void *packed_up_t,
+                                       size_t packed_t_bytes, int64_t M, const void *X, int64_t ldx,
+                                       tsl_act act, const void *G, const void *U, int64_t ld_gu,
+                                       const void *dH, int64_t lddh, tsl_dtype dxdtype, void *dX,
+                                       int64_t lddx, tsl_dtype dwdtype, void *dW_gate, void *dW_up,
+                                       int64_t dw_stride_k, int64_t dw_stride_n, int accumulate_dw,
+                                       void *workspace, size_t ws_bytes, void *stream) {
+    return guarded([&] {
+        GradCall c;
+        c.shard[0] = gate;
+        c.shard[1] = up;
+        c.n_w = 2;
+        c.packed_t[0] = packed_gate_t;
+        c.packed_t[1] = packed_up_t;
+        c.packed_t_bytes = packed_t_bytes;
+        c.wdtype = wdtype;
+        c.M = M;
+        c.X = X;
+        c.ldx = dW_gate ? ldx : 0;
+        c.act = act;
+        c.a = dH;
+        c.lda = lddh;
+        c.b = G;
+        c.c = U;
+        c.ldb = ld_gu;
+        c.dxdtype = dxdtype;
+        c.dX = dX;
+        c.lddx = dX ? lddx : 0;
+        c.dwdtype = dwdtype;
+        c.dW[0] = dW_gate;
+        c.dW[1] = dW_up;
+        c.sk = dW_gate ? dw_stride_k : 0;
+        c.sn = dW_gate ? dw_stride_n : 0;
+        c.accumulate = accumulate_dw;
+        return run_grad(c, workspace, ws_bytes, stream);
+    });
+}
+
 extern "C" const char *tsl_block_last_hip_error_string(void) {
     return hipGetErrorString(g_last_hip);
 }

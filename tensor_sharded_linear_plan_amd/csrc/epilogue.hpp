@@ -64,6 +64,40 @@ __device__ __forceinline__ float act_value(float v, int act) {
     }
 }
 
+// An activation and its slope.  With s = s(t): (v s)' = s + v s (1 - s) t'.
+// The cubic's arguments are clamped where s is 0 or 1 to the last bit, so
+// that t' stays finite.
+__device__ __forceinline__ void act_both(float v, int act, float &a, float &d) {
+    switch (act) {
+    case TSL_ACT_RELU:
+        a = v < 0.f ? 0.f : v;
+        d = v > 0.f ? 1.f : 0.f;
+        break;
+    case TSL_ACT_SILU: {
+        const float s = logistic(v);
+        a = v * s;
+        d = __builtin_fmaf(a, 1.f - s, s);
+        break;
+    }
+    case TSL_ACT_GELU: {
+        const float p = 0.5f * erfcf(-0.707106781f * v);
+        a = v * p;
+        d = __builtin_fmaf(v, 0.398942280f * __builtin_amdgcn_exp2f(-0.721347520f * v * v), p);
+        break;
+    }
+    case TSL_ACT_GELU_TANH: {
+        const float c = v > 64.f ? 64.f : (v < -64.f ? -64.f : v);
+        const float s = logistic(c * __builtin_fmaf(kGeluC1 * c, c, kGeluC0));
+        a = v * s;
+        d = __builtin_fmaf(c * s * (1.f - s), __builtin_fmaf(3.f * kGeluC1 * c, c, kGeluC0), s);
+        break;
+    }
+    default:
+        a = v;
+        d = 1.f;
+    }
+}
+
 // v with its bias, kept in pre, through the activation, plus the residual.
 __device__ __forceinline__ float ep_apply(const Epilogue &e, float v, int64_t m, int64_t n) {
     if (e.bias)

@@ -143,6 +143,39 @@ int64_t norm_grad_groups(int64_t M, int64_t n);
 hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accumulate,
                             hipStream_t stream);
 
+// out[j] (+)= sum of `groups` partial rows of n binary32 (row stride n
+// rounded up to 8), in a fixed order
+hipError_t launch_column_sum(const float *part, int64_t groups, int64_t n, float *out,
+                             int accumulate, hipStream_t stream);
+
+// ---- grad.hip: operands of a product's backward pass ----
+// One pass over [M][N] rows: the gradient at the product's output (kind) in
+// the layouts its two products read.
+enum { kGradCopy = 0, kGradAct = 1, kGradGated = 2 };
+struct GradJob {
+    // copy: a.  act: dY, Z.  gated: dH, G, U
+    const void *a = nullptr, *b = nullptr, *c = nullptr;
+    int64_t lda = 0, ldb = 0, ldc = 0;
+    // row-major results (null: not wanted), zero columns up to ld_row
+    void *row[2] = {};
+    int64_t ld_row = 0;
+    // transposed results (null: not wanted): [N][Mp] rows, or (packed) the
+    // packed layout of a weight W[Mp][N]; zero from M to Mp = M rounded up to 64
+    void *tr[2] = {};
+    int32_t packed = 0;
+    int32_t kind = kGradCopy, act = 0;
+    // binary32 column sums of the result, one row per 64 rows of the job
+    // (row stride N rounded up to 8); null: not wanted
+    float *part = nullptr;
+    int64_t M = 0, N = 0;
+    int32_t nblk = 0, start = 0; // set by the launcher
+};
+constexpr int kGradJobs = 2;
+int64_t grad_blocks(const GradJob &j);
+hipError_t launch_grad_rows(GradJob *jobs, int n, bool bf16, hipStream_t stream);
+hipError_t launch_zero_rows(void *out, int64_t rows, int64_t cols, int64_t ld, bool bf16,
+                            hipStream_t stream);
+
 // ---- embed.hip ----
 // Y[m][j] = table[(tokens[m] - k_off) * ld_table + j] when the token lies in
 // [k_off, k_off + k_len), else -0.0; j < n_len.  Types F32 / BF16.

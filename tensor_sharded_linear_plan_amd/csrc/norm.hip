@@ -14,76 +14,10 @@
 // 32768.  All sums are binary32.
 #include "device.hpp"
 #include "internal.hpp"
+#include "rows.hpp"
 
 namespace tsl {
 namespace {
-
-typedef float f32x8 __attribute__((ext_vector_type(8)));
-
-// 8 consecutive columns col .. col + 7 of a row (element type by `bf`),
-// zero past n.  VEC: the run is 16-byte aligned, so a whole one takes wide
-// loads; otherwise, and for the run that crosses n, one element at a time.
-template <bool VEC>
-__device__ __forceinline__ f32x8 load8(const void *row, bool bf, int64_t col, int64_t n) {
-    f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (col >= n)
-        return v;
-    if (VEC && col + 8 <= n) {
-        if (bf) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(row) + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = bf16_lo(w[i]);
-                v[2 * i + 1] = bf16_hi(w[i]);
-            }
-        } else {
-            const f32x4 *p = reinterpret_cast<const f32x4 *>(static_cast<const float *>(row) + col);
-            const f32x4 a = p[0], b = p[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        }
-        return v;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i < n)
-            v[i] = bf ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(row)[col + i] << 16)
-                      : static_cast<const float *>(row)[col + i];
-    return v;
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(void *row, bool bf, int64_t col, int64_t n, f32x8 v) {
-    if (col >= n)
-        return;
-    if (VEC && col + 8 <= n) {
-        if (bf) {
-            u32x4 w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(row) + col) = w;
-        } else {
-            f32x4 *p = reinterpret_cast<f32x4 *>(static_cast<float *>(row) + col);
-            p[0] = f32x4{v[0], v[1], v[2], v[3]};
-            p[1] = f32x4{v[4], v[5], v[6], v[7]};
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i < n) {
-            if (bf) {
-                __bf16 h = (__bf16)v[i];
-                static_cast<uint16_t *>(row)[col + i] = __builtin_bit_cast(uint16_t, h);
-            } else {
-                static_cast<float *>(row)[col + i] = v[i];
-            }
-        }
-}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -282,7 +216,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(NormArgs a)
 // ---- backward ----------------------------------------------------------------
 // Row groups walk the rows with the grid's stride; each thread keeps the
 // weight gradient of its own columns over its rows and leaves it in the
-// workspace, [row groups][n rounded up to 8], which norm_dw_kernel adds in
+// workspace, [row groups][n rounded up to 8], which column_sum_kernel adds in
 // order.
 template <int TPR, int NV, bool VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGradArgs a) {
@@ -358,7 +292,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGr
 
 // dW[j] (+)= sum over the row groups' partials, 16 columns per workgroup:
 // 16 threads per column take every 16th partial, then add up in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float *__restrict__ part, int64_t groups,
+__global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict__ part, int64_t groups,
                                                       int64_t n, float *__restrict__ dW,
                                                       int accumulate) {
     __shared__ float red[16][17];
@@ -411,6 +345,13 @@ int64_t norm_grad_groups(int64_t M, int64_t n) {
     return M < most ? M : most;
 }
 
+hipError_t launch_column_sum(const float *part, int64_t groups, int64_t n, float *out,
+                             int accumulate, hipStream_t stream) {
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, stream, part,
+                       groups, n, out, accumulate);
+    return hipGetLastError();
+}
+
 hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accumulate,
                             hipStream_t stream) {
     if (a.M > 0) {
@@ -433,12 +374,8 @@ hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accu
         if (e != hipSuccess)
             return e;
     }
-    if (dW) {
-        hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, stream,
-                           a.part, a.M > 0 ? a.row_groups : 0, a.n, dW, accumulate);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+    return dW ? launch_column_sum(a.part, a.M > 0 ? a.row_groups : 0, a.n, dW, accumulate, stream)
+              : hipSuccess;
 }
 
 } // namespace tsl
