@@ -228,15 +228,24 @@ def _check(status, where):
 def _ptr(x):
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return int(x)
+    except AttributeError:
+        return int(x)
+
+
+_raw_stream = getattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is not None:
         return getattr(stream, "cuda_stream", stream)
-    if _torch is not None and _torch.cuda.is_available():
+    if _torch is None:
+        return None
+    # the current stream's handle, without building a Stream object per call
+    if _raw_stream is not None and _torch.cuda.is_initialized():
+        return _raw_stream(_torch.cuda.current_device())
+    if _torch.cuda.is_available():
         return _torch.cuda.current_stream().cuda_stream
     return None
 
@@ -345,23 +354,23 @@ def _items(items):
     """items: sequence of dicts (or LinearItem) with the tsl_linear_item
     fields (ydtype defaults to F32, accumulate, sum_next and rows to 0,
     row_index to None); shard is a Shard; a set member's Y may be None.
-    Returns the ctypes array (which keeps the shard copies alive) and its
-    length."""
-    arr = (LinearItem * max(len(items), 1))()
+    Returns the ctypes array (which keeps the shards alive) and its length."""
+    n = len(items)
+    arr = (LinearItem * (n or 1))()
     keep = []
     for i, it in enumerate(items):
         if isinstance(it, LinearItem):
             arr[i] = it
             continue
-        sh = Shard(*it["shard"].as_tuple())
+        get = it.get
+        sh = it["shard"]
         keep.append(sh)
         arr[i] = LinearItem(ctypes.pointer(sh), _ptr(it["packed"]), it["packed_bytes"],
-                            _ptr(it["X"]), it["ldx"], _ptr(it.get("Y")), it.get("ldy", 0),
-                            it.get("ydtype", F32), it.get("accumulate", 0),
-                            it.get("sum_next", 0), it.get("rows", 0),
-                            _ptr(it.get("row_index")), it.get("x_rows", 0))
+                            _ptr(it["X"]), it["ldx"], _ptr(get("Y")), get("ldy", 0),
+                            get("ydtype", F32), get("accumulate", 0), get("sum_next", 0),
+                            get("rows", 0), _ptr(get("row_index")), get("x_rows", 0))
     arr._keep = keep
-    return arr, len(items)
+    return arr, n
 
 
 def shard_linear_group_workspace_size(items, wdtype, M):
@@ -434,9 +443,10 @@ def _epilogues(eps, n):
         if e is None:
             continue
         if not isinstance(e, Epilogue):
-            e = Epilogue(_ptr(e.get("bias")), _ptr(e.get("residual")), _ptr(e.get("pre")),
-                         e.get("ld_res", 0), e.get("ld_pre", 0), e.get("act", ACT_NONE),
-                         e.get("bias_dtype", F32), e.get("res_dtype", F32), e.get("pre_dtype", F32))
+            get = e.get
+            e = Epilogue(_ptr(get("bias")), _ptr(get("residual")), _ptr(get("pre")),
+                         get("ld_res", 0), get("ld_pre", 0), get("act", ACT_NONE),
+                         get("bias_dtype", F32), get("res_dtype", F32), get("pre_dtype", F32))
         arr[i] = ctypes.pointer(e)
     return arr
 
@@ -461,21 +471,22 @@ def shard_linear_group_epilogue(items, epilogues, wdtype, xdtype, M, workspace=N
 def _gated(items):
     """items: sequence of dicts (or GatedItem) with the tsl_gated_item fields
     (hdtype defaults to F32, rows to 0, G, U and row_index to None)."""
-    arr = (GatedItem * max(len(items), 1))()
+    n = len(items)
+    arr = (GatedItem * (n or 1))()
     keep = []
     for i, it in enumerate(items):
         if isinstance(it, GatedItem):
             arr[i] = it
             continue
-        g, u = Shard(*it["gate"].as_tuple()), Shard(*it["up"].as_tuple())
+        get, g, u = it.get, it["gate"], it["up"]
         keep += [g, u]
         arr[i] = GatedItem(ctypes.pointer(g), ctypes.pointer(u), _ptr(it["packed_gate"]),
                            _ptr(it["packed_up"]), it["packed_bytes"], _ptr(it["X"]), it["ldx"],
-                           _ptr(it["H"]), it["ldh"], _ptr(it.get("G")), _ptr(it.get("U")),
-                           it.get("ld_gu", 0), _ptr(it.get("row_index")), it.get("x_rows", 0),
-                           it.get("hdtype", F32), it.get("rows", 0))
+                           _ptr(it["H"]), it["ldh"], _ptr(get("G")), _ptr(get("U")),
+                           get("ld_gu", 0), _ptr(get("row_index")), get("x_rows", 0),
+                           get("hdtype", F32), get("rows", 0))
     arr._keep = keep
-    return arr, len(items)
+    return arr, n
 
 
 def shard_gated_group_workspace_size(items, wdtype, M):

@@ -407,6 +407,18 @@ void gated_pair(const tsl_gated_item &g, tsl_linear_item *two) {
 
 constexpr int32_t kMaxGated = kMaxItems / 2;
 
+// Pairs of bf16 and 4-bit weights run as one dual product each: the second
+// of a checked pair leaves the list (its packed weight is ep->up).
+void merge_pairs(std::vector<LinearItem> *v, tsl_dtype wdtype) {
+    if (wdtype == TSL_F32)
+        return;
+    for (size_t i = 0; 2 * i < v->size(); ++i) {
+        (*v)[i] = (*v)[2 * i];
+        (*v)[i].set_len = 1;
+    }
+    v->resize(v->size() / 2);
+}
+
 } // namespace
 
 extern "C" tsl_status shard_gated_group_workspace_size(int32_t n_items, const tsl_gated_item *items,
@@ -423,6 +435,7 @@ extern "C" tsl_status shard_gated_group_workspace_size(int32_t n_items, const ts
             return st;
         Epilogue gate;
         gate.flags = kEpGated;
+        gate.up = wdtype == TSL_F32 ? nullptr : &gate;
         for (int32_t i = 0; i < n_items; ++i) {
             if (v[2 * i].g.Ns != v[2 * i + 1].g.Ns || v[2 * i].g.Ks != v[2 * i + 1].g.Ks)
                 return TSL_ERR_INVALID_ARG;
@@ -430,6 +443,7 @@ extern "C" tsl_status shard_gated_group_workspace_size(int32_t n_items, const ts
             // the pair reads one X (any address that no other pair has)
             v[2 * i].X = v[2 * i + 1].X = &pairs[2 * i];
         }
+        merge_pairs(&v, wdtype);
         *bytes = group_workspace(v, wdtype, M);
         return TSL_OK;
     });
@@ -466,11 +480,13 @@ extern "C" tsl_status shard_gated_group(int32_t n_items, const tsl_gated_item *i
             e.ldp = g.ld_gu;
             e.act = act;
             e.flags = kEpGated | (g.hdtype == TSL_BF16 ? kEpPreBf16 : 0);
+            e.up = wdtype == TSL_F32 ? nullptr : g.packed_up;
             v[2 * i].ep = &e;
             kept = kept || g.G;
         }
         if (M > 0 && kept && epilogue_clash(v, xdtype == TSL_F32 ? 4 : 2))
             return TSL_ERR_INVALID_ARG;
+        merge_pairs(&v, wdtype);
         return run_group(v, wdtype, M, workspace, ws_bytes, stream);
     });
 }

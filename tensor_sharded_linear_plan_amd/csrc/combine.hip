@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(256) sum_sets_kernel(SumSets g) {
             };
             f32x4 acc = product(0);
             if constexpr (kEpilogue) {
-                const Epilogue &e = g.ep(lo);
+                const Epilogue e = g.ep(lo);
                 if (e.flags & kEpGated) {
                     const f32x4 u = product(1);
 #pragma unroll

@@ -233,10 +233,6 @@ inline std::vector<LinearItem> launch_order(const std::vector<LinearItem> &items
 // A set of two whose results the gate combines (act(X W_0) * (X W_1)).
 inline bool gated(const LinearItem &L) { return L.ep && (L.ep->flags & kEpGated); }
 
-// Whether a lone product's own kernel applies its epilogue (unless it splits
-// k: then the sum launch that adds its k-partials does).
-inline bool fused_epilogue(const LinearItem &, tsl_dtype, int64_t) { return false; }
-
 // The GEMM regime: a sum set whose members have equal k-ranges becomes one
 // product over the members' k-ranges laid end to end in set order,
 // Y = [X_0 X_1 ...] [W_0; W_1; ...] -- the rank sum accumulated inside the
@@ -303,18 +299,18 @@ inline std::vector<LinearItem> concat_sets(const std::vector<LinearItem> &in, ts
 // Rewrites every sum set of *items into lone items writing binary32
 // partials at ws, ws + ...; returns the bytes used.  Call it once: the
 // items it leaves are no longer sets.  With ws == nullptr the partials'
-// addresses are null (for sizing; such items are never launched).  A lone
-// product whose kernel does not apply its epilogue is a set of one here.
-inline size_t split_sets(std::vector<LinearItem> *items, tsl_dtype wdtype, int64_t M, char *ws) {
+// addresses are null (for sizing; such items are never launched).
+inline size_t split_sets(std::vector<LinearItem> *items, char *ws) {
     size_t off = 0;
     for (size_t i = 0; i < items->size();) {
         const size_t len = (*items)[i].set_len;
-        if (len > 1 || ((*items)[i].ep && !fused_epilogue((*items)[i], wdtype, M))) {
+        if (len > 1) {
             void *const sY = (*items)[i].Y;
             const int64_t sldy = (*items)[i].ldy;
             const tsl_dtype sy = (*items)[i].ydtype;
-            // sets with an epilogue are added by the sum launch
-            const int flen = (*items)[i].ep || len < 2 ? 0 : (int)len;
+            const Epilogue *const ep = (*items)[i].ep;
+            // a gated pair's results are combined by the sum launch
+            const int flen = gated((*items)[i]) ? 0 : (int)len;
             for (size_t r = 0; r < len; ++r) {
                 LinearItem &L = (*items)[i + r];
                 L.fset_len = flen;
@@ -328,7 +324,8 @@ inline size_t split_sets(std::vector<LinearItem> *items, tsl_dtype wdtype, int64
                 L.accumulate = 0;
                 L.set_len = 1;
                 L.set_pos = 0;
-                L.ep = nullptr; // the set's first item keeps it in the caller's list
+                L.ep = nullptr; // the whole set's, once its products are added
+                L.fset_ep = flen > 0 && r == 0 ? ep : nullptr;
                 L.no_split = len > (size_t)kSetParts; // summed by launch_combine_sum
 
                 off += ((size_t)L.M * (size_t)L.g.Ns * 4 + 255) / 256 * 256;
@@ -392,7 +389,7 @@ inline size_t group_workspace(const std::vector<LinearItem> &in, tsl_dtype wdtyp
     std::vector<RowGather> jobs;
     const size_t gathered = plan_row_gathers(&src, wdtype, M, nullptr, &jobs);
     std::vector<LinearItem> items = launch_order(concat_sets(src, wdtype, M));
-    const size_t parts = split_sets(&items, wdtype, M, nullptr);
+    const size_t parts = split_sets(&items, nullptr);
     if (use_skinny(wdtype, M))
         return gathered + parts + skinny_plan(items.data(), (int)items.size(), wdtype, M).ws_bytes;
     return gathered + parts + prefill_plan(items.data(), (int)items.size(), wdtype, M).ws_bytes;
@@ -411,7 +408,7 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
     char *ws = ws0 ? ws0 + gathered : nullptr; // the rank partials, then the plan's
     const std::vector<LinearItem> ordered = launch_order(concat_sets(src, wdtype, M));
     std::vector<LinearItem> items = ordered;
-    const size_t parts = split_sets(&items, wdtype, M, ws);
+    const size_t parts = split_sets(&items, ws);
     const int n = (int)items.size();
     hipStream_t s = static_cast<hipStream_t>(stream);
     size_t need;
@@ -467,19 +464,22 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
     std::vector<SumSpec> sums;
     for (size_t i = 0; i < ordered.size();) {
         const size_t len = ordered[i].set_len;
-        // a lone product: its k-partials (or, its epilogue still to come, its
-        // binary32 result) into its Y
-        if (len == 1 && (kcount(i) > 1 || (ordered[i].ep && !items[i].ep))) {
+        if (len == 1 && kcount(i) > 1) { // a lone product: its k-partials into its Y
             SumSpec sp1;
             sp1.parts[0] = kparts(i);
             sp1.ks[0] = kcount(i);
             sp1.n_parts = 1;
+            if (dual(items[i])) { // the second weight's partials follow the first's
+                sp1.parts[1] = sp1.parts[0] + (int64_t)kcount(i) * items[i].M * items[i].g.Ns;
+                sp1.ks[1] = kcount(i);
+                sp1.n_parts = 2;
+            }
             sp1.M = items[i].M;
             sp1.n = items[i].g.Ns;
-            sp1.Y = ordered[i].Y;
-            sp1.ldy = ordered[i].ldy;
-            sp1.ydtype = ordered[i].ydtype;
-            sp1.ep = ordered[i].ep;
+            sp1.Y = items[i].Y;
+            sp1.ldy = items[i].ldy;
+            sp1.ydtype = items[i].ydtype;
+            sp1.ep = items[i].ep;
             sums.push_back(sp1);
         }
         i += len;

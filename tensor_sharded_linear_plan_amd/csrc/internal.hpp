@@ -56,6 +56,7 @@ struct Epilogue {
     const void *bias = nullptr;
     const void *res = nullptr;
     void *pre = nullptr, *pre2 = nullptr;
+    const void *up = nullptr; // a dual product's second packed weight
     int64_t ldr = 0, ldp = 0;
     int32_t act = 0;   // tsl_act
     int32_t flags = 0; // kEp*
@@ -216,8 +217,11 @@ struct LinearItem {
     // too long for one sum launch)
     bool no_split = false;
     // what its set's (or its own) result goes through; null: nothing.  A
-    // gated pair is a set of two whose results are combined by the gate
+    // gated pair of binary32 weights is a set of two whose results the gate
+    // combines; of other weights it is one dual product, whose kernel holds
+    // both results (ep->up: the second packed weight, of the same geometry)
     const Epilogue *ep = nullptr;
+    const Epilogue *fset_ep = nullptr; // of the sum set it is a member of
     // member fset_pos of a sum set of fset_len products that split_sets
     // turned into lone items (0: none), and the set's own output
     int fset_len = 0, fset_pos = 0;
@@ -235,6 +239,10 @@ struct LinearItem {
     const int32_t *seg_ridx[kSetParts] = {};
     int64_t seg_xrows[kSetParts] = {};
 };
+
+inline bool dual(const LinearItem &L) { return kEpilogue && L.ep && L.ep->up; }
+// result columns of a product, counting both of a dual one
+inline int64_t result_columns(const LinearItem &L) { return dual(L) ? 2 * L.g.Ns : L.g.Ns; }
 
 // Workgroups per CU of the fused 4-bit GEMM for a bm x bn tile with wm row
 // waves: two when one row wave per SIMD leaves room for a second workgroup
@@ -255,8 +263,9 @@ hipError_t noalloc_scratch(void **ptr);
 constexpr int kGroupMax = 128;
 // ... for the prefill GEMMs and their activation pass: 256 (up to ~27 KB of
 // kernel arguments, within the 32 KB this runtime launches correctly), so
-// that e.g. the gate and up products of 128 experts share one launch.
-constexpr int kPrefillGroupMax = 256;
+// that e.g. the gate and up products of 128 experts share one launch; 128
+// where every item brings its epilogue (64 bytes more).
+constexpr int kPrefillGroupMax = kEpilogue ? 128 : 256;
 // ... of them joined sum sets (their member tables ride in the kernel
 // arguments too)
 constexpr int kMaxJoined = 16;

@@ -53,6 +53,7 @@
 #include <vector>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "internal.hpp"
 
@@ -71,16 +72,16 @@ struct GemmItem {
     int32_t R;         // members of a joined sum set (1: a lone product)
     int32_t start;     // first workgroup
     int32_t accumulate;
-    int32_t flags;     // bit 0: bf16 output
+    int32_t flags;     // bit 0: bf16 output, bit 1: an epilogue
     int64_t M;         // rows of this item
     float *P;          // ks > 1: binary32 k-partials [ks][M][Ns]
     int32_t ks;        // k-splits: tile t of split q covers stages [q nst / ks, (q+1) nst / ks)
     int32_t seg;       // R > 1: the set's row of the member tables
 };
 static_assert(sizeof(GemmItem) == 104, "item table size");
-constexpr int kYBf16 = 1;
+constexpr int kYBf16 = 1, kHasEpilogue = 2;
 
-struct GemmGroup {
+struct GemmGroup : Epilogues<kPrefillGroupMax> {
     int64_t M;
     int32_t n, pad_;
     GemmItem it[kPrefillGroupMax];
@@ -126,10 +127,14 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-template <int BM, int BN, int WM, int WN>
+// DUAL: the product's columns are those of two weights, 32 of the first and
+// 32 of the second in turn, so that a wave's neighbouring accumulator tiles
+// hold the two results of the same rows and columns.
+template <int BM, int BN, int WM, int WN, bool DUAL = false>
 __global__ void __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) gemm_kernel(GemmGroup grp) {
     using C = G<BM, BN, WM, WN>;
+    static_assert(!DUAL || C::NT % 2 == 0, "a wave holds both columns of a pair");
     __shared__ __attribute__((aligned(1024))) char lds[C::NS * C::STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); // scalar
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     const int bm_cnt = a.MB - first_m < 8 ? a.MB - first_m : 8;
     const int in_band = t - band * 8 * a.NB;
     const int64_t mb = first_m + in_band % bm_cnt, nb = in_band / bm_cnt;
-    const int64_t m0 = mb * BM, n0 = nb * BN;
+    const int64_t m0 = mb * BM, n0 = nb * (DUAL ? BN / 2 : BN);
     const int nst_all = a.KT64 * (64 / C::BK); // stages of the whole k-range
     const int kb = ksi * nst_all / a.ks;       // this split's first stage
     const int nst = (ksi + 1) * nst_all / a.ks - kb;
@@ -190,6 +195,10 @@ __global__ void __launch_bounds__(64 * WM * WN)
         const int r = lane < a.R ? lane : 0;
         const char *xm = a.R > 1 ? grp.segx[seg][r] : reinterpret_cast<const char *>(a.X);
         const char *wm0 = a.R > 1 ? grp.segb[seg][r] : reinterpret_cast<const char *>(a.B);
+        if constexpr (DUAL) { // odd lanes: the second weight
+            if (lane & 1)
+                wm0 = static_cast<const char *>(grp.ep(lo).up);
+        }
         const int64_t ld = a.R > 1 ? (int64_t)grp.segld[seg][r] : a.ldx;
         const uint64_t xv = (uint64_t)(uintptr_t)(xm + m0 * ld * 2);
         const uint64_t bv = (uint64_t)(uintptr_t)(wm0 + t0 * (int64_t)a.KT32 * 1024);
@@ -200,8 +209,9 @@ __global__ void __launch_bounds__(64 * WM * WN)
         xl = (uint32_t)ld;
     }
     // the activation and record bases and the activation row stride of
-    // stage kt of this split
-    auto src = [&](int kt, const char *&xs, const char *&bs, uint32_t &xld)
+    // stage kt of this split (DUAL: bs, bs1 for this wave's weight copies of
+    // an even and an odd index)
+    auto src = [&](int kt, const char *&xs, const char *&bs, const char *&bs1, uint32_t &xld)
                    __attribute__((always_inline)) {
         int r = 0, gl = kt + kb;
         while (gl >= spm) { // uniform, at most R - 1 + NS / spm steps
@@ -211,10 +221,16 @@ __global__ void __launch_bounds__(64 * WM * WN)
         xld = (uint32_t)__builtin_amdgcn_readlane((int)xl, r);
         const uint64_t xv = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)xr[0], r) |
                             ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)xr[1], r) << 32);
-        const uint64_t bv = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)br[0], r) |
-                            ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)br[1], r) << 32);
+        auto wbase = [&](int l) __attribute__((always_inline)) {
+            const uint64_t bv = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)br[0], l) |
+                                ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)br[1], l) << 32);
+            return reinterpret_cast<const char *>((uintptr_t)bv) + gl * (C::BK / 32 * 1024);
+        };
         xs = reinterpret_cast<const char *>((uintptr_t)xv) + gl * (C::BK * 2);
-        bs = reinterpret_cast<const char *>((uintptr_t)bv) + gl * (C::BK / 32 * 1024);
+        // (DUAL: copy j's 32-column block is wave / S16 + NW / S16 j, of
+        // weight block mod 2)
+        bs = wbase(DUAL ? (wave / C::S16) & 1 : r);
+        bs1 = DUAL ? wbase((wave / C::S16 + C::NW / C::S16) & 1) : bs;
     };
     const int arow = lane / C::CPR; // row of this lane in its block
     const uint32_t chunk = 8 * ((lane % C::CPR) ^ swz<C::CPR>(arow));
@@ -227,28 +243,47 @@ __global__ void __launch_bounds__(64 * WM * WN)
     const int tfirst = 2 * (wave / C::S16) + ((lane & 31) >> 4);
     constexpr int TPJ = 2 * (C::NW / C::S16); // 16-column tiles per weight block step
     const uint32_t lds0 = (uint32_t)(uintptr_t)(void __attribute__((address_space(3))) *)lds;
+    // DUAL: a wave-uniform address pinned to scalar registers, where the copy
+    // needs it (with two weight bases alive the compiler may hold them in
+    // vector registers)
+    auto scalar = [](const char *p) __attribute__((always_inline)) {
+        if constexpr (DUAL) {
+            const uint64_t v = (uint64_t)(uintptr_t)p;
+            const uint64_t lo32 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+            const uint64_t hi32 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+            return reinterpret_cast<const char *>((uintptr_t)(lo32 | (hi32 << 32)));
+        }
+        return p;
+    };
     // copy j (0 <= j < FPW) of this wave for the stage whose bases are xs,
-    // bs (activation row stride xld) into LDS slot `slot`
-    auto issue1 = [&](const char *xs, const char *bs, uint32_t xld, int slot, int j)
+    // bs, bs1 (activation row stride xld) into LDS slot `slot`
+    auto issue1 = [&](const char *xs, const char *bs, const char *bs1, uint32_t xld, int slot, int j)
                       __attribute__((always_inline)) {
         const uint32_t dst = lds0 + slot * C::STAGE + wave * 1024 + C::NW * j * 1024;
         uint32_t a0 = arow0, b0 = boff0;
         asm volatile("" : "+v"(a0), "+v"(b0)); // keep the per-j offsets out of registers
         if (j < C::AF / C::NW) {
             const uint32_t row = a0 + (uint32_t)(j * C::NW * C::RPB);
-            dma16(xs, ((row < last_row ? row : last_row) * xld + chunk) * 2, dst);
+            dma16(scalar(xs), ((row < last_row ? row : last_row) * xld + chunk) * 2, dst);
         } else {
-            const int tt = tfirst + TPJ * (j - C::AF / C::NW);
-            dma16(bs, b0 + (uint32_t)(tt < tmax ? tt : tmax) * tstep, dst);
+            if constexpr (DUAL) { // 32-column block cb: weight cb % 2, its block cb / 2
+                const int jw = j - C::AF / C::NW;
+                const int cb = wave / C::S16 + C::NW / C::S16 * jw;
+                const int tt = 2 * (cb >> 1) + ((lane & 31) >> 4);
+                dma16(scalar(jw & 1 ? bs1 : bs), b0 + (uint32_t)(tt < tmax ? tt : tmax) * tstep, dst);
+            } else {
+                const int tt = tfirst + TPJ * (j - C::AF / C::NW);
+                dma16(bs, b0 + (uint32_t)(tt < tmax ? tt : tmax) * tstep, dst);
+            }
         }
     };
     auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
-        const char *xs, *bs;
+        const char *xs, *bs, *bs1;
         uint32_t xld;
-        src(kt, xs, bs, xld);
+        src(kt, xs, bs, bs1, xld);
 #pragma unroll
         for (int j = 0; j < C::FPW; ++j)
-            issue1(xs, bs, xld, slot, j);
+            issue1(xs, bs, bs1, xld, slot, j);
     };
 
     f32x16 acc[C::MT][C::NT];
@@ -300,7 +335,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     int slot = 0;
     for (int kt = 0; kt < nst; ++kt) {
         const int next = slot + 1 == C::NS ? 0 : slot + 1;
-        const char *cxs = nullptr, *cbs = nullptr; // stage kt + NS's bases
+        const char *cxs = nullptr, *cbs = nullptr, *cbs1 = nullptr; // stage kt + NS's bases
         uint32_t cxld = 0;
 #pragma unroll
         for (int s = 0; s < C::S16; ++s) {
@@ -318,7 +353,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
                     rd(next, 0, af[b ^ 1], bfr[b ^ 1]);
                     copies = kt + C::NS < nst;
                     if (copies)
-                        src(kt + C::NS, cxs, cbs, cxld);
+                        src(kt + C::NS, cxs, cbs, cbs1, cxld);
                 }
             }
             // the copies of stage kt + NS go into the slot of stage kt,
@@ -333,7 +368,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
 #pragma unroll
                     for (int f = q * C::FPW / (C::MT * C::NT); f < (q + 1) * C::FPW / (C::MT * C::NT); ++f)
                         if (copies)
-                            issue1(cxs, cbs, cxld, slot, f);
+                            issue1(cxs, cbs, cbs1, cxld, slot, f);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -348,9 +383,23 @@ __global__ void __launch_bounds__(64 * WM * WN)
     // One base address per lane; every store is that base plus a
     // compile-time row/column step times the (uniform) row stride.
     const int64_t row0 = m0 + wm * C::MT * 32 + 4 * (lane >> 5);
-    const int64_t col0 = n0 + wn * C::NT * 32 + (lane & 31);
-    // a k-split writes its binary32 partial, [M][Ns] at split ksi
+    const int64_t col0 = n0 + wn * (DUAL ? C::NT / 2 : C::NT) * 32 + (lane & 31);
+    // a k-split writes its binary32 partial, [M][Ns] at split ksi (DUAL: the
+    // second weight's splits follow the first's)
     const bool part = a.ks > 1;
+    auto result = [&](int i, int j, int r) __attribute__((always_inline)) { return acc[i][j][r]; };
+    if constexpr (kEpilogue) {
+        if (!part && (DUAL || (a.flags & kHasEpilogue))) {
+            ep_store<C::MT, C::NT, DUAL>(grp.ep(lo), a.Y, (a.flags & kYBf16) != 0, a.ldy, row0, col0,
+                                         M, a.Ns, result);
+            return;
+        }
+    }
+    if constexpr (DUAL) {
+        float *const p0 = a.P + (int64_t)ksi * M * a.Ns;
+        dual_partials<C::MT, C::NT>(p0, p0 + (int64_t)a.ks * M * a.Ns, row0, col0, M, a.Ns, result);
+        return;
+    }
     const bool ybf = part ? false : (a.flags & kYBf16) != 0;
     const bool accu = part ? false : a.accumulate;
     const int64_t ldy = part ? a.Ns : a.ldy;
@@ -615,9 +664,17 @@ struct Variant {
 };
 // tile shapes with a kernel instance: bf16 operands, and the fused 4-bit
 // kernel (waves WM x 4; two workgroups per CU where they fit)
-constexpr Variant kVariants[] = {{256, 256, 2, 4}, {256, 160, 4, 1}, {256, 128, 4, 2},
-                                 {128, 256, 2, 4}, {128, 128, 2, 2}, {256, 64, 4, 1},
-                                 {128, 64, 2, 2},  {64, 64, 2, 2}};
+constexpr Variant kVariants[] = {
+    {256, 256, 2, 4},
+#if !TSL_EPILOGUE // its epilogue store does not unroll (ten tiles a wave): registers spill
+    {256, 160, 4, 1},
+#endif
+    {256, 128, 4, 2}, {128, 256, 2, 4}, {128, 128, 2, 2},
+    {256, 64, 4, 1},  {128, 64, 2, 2},  {64, 64, 2, 2}};
+// ... of dual products: both columns of a pair in one wave
+constexpr Variant kDualVariants[] = {{256, 256, 2, 4}, {256, 128, 4, 2}, {128, 256, 2, 4},
+                                     {128, 128, 2, 2}, {256, 64, 4, 1},  {64, 128, 2, 2}};
+constexpr Variant kQ4DualVariants[] = {{256, 256, 2, 4}, {128, 256, 2, 4}, {64, 256, 1, 4}};
 constexpr Variant kQ4Variants[6] = {{256, 256, 2, 4}, {256, 128, 1, 4}, {128, 256, 2, 4},
                                     {128, 128, 1, 4}, {64, 256, 1, 4},  {64, 128, 1, 4}};
 // workgroups of a 4-bit tile shape per CU
@@ -627,10 +684,25 @@ GemmFn pick(const Variant &v) {
 #define TSL_CASE(BM_, BN_, WM_, WN_)                                                               \
     if (v.bm == BM_ && v.bn == BN_ && v.wm == WM_ && v.wn == WN_)                                  \
         return gemm_kernel<BM_, BN_, WM_, WN_>;
-    TSL_CASE(256, 256, 2, 4) TSL_CASE(256, 160, 4, 1) TSL_CASE(256, 128, 4, 2)
+    TSL_CASE(256, 256, 2, 4) TSL_CASE(256, 128, 4, 2)
+#if !TSL_EPILOGUE
+    TSL_CASE(256, 160, 4, 1)
+#endif
     TSL_CASE(128, 256, 2, 4) TSL_CASE(128, 128, 2, 2) TSL_CASE(256, 64, 4, 1)
     TSL_CASE(128, 64, 2, 2) TSL_CASE(64, 64, 2, 2)
 #undef TSL_CASE
+    return nullptr;
+}
+
+GemmFn pick_dual(const Variant &v) {
+    if constexpr (kEpilogue) {
+#define TSL_CASE(BM_, BN_, WM_, WN_)                                                               \
+    if (v.bm == BM_ && v.bn == BN_ && v.wm == WM_ && v.wn == WN_)                                  \
+        return gemm_kernel<BM_, BN_, WM_, WN_, kEpilogue>;
+        TSL_CASE(256, 256, 2, 4) TSL_CASE(256, 128, 4, 2) TSL_CASE(128, 256, 2, 4)
+        TSL_CASE(128, 128, 2, 2) TSL_CASE(256, 64, 4, 1) TSL_CASE(64, 128, 2, 2)
+#undef TSL_CASE
+    }
     return nullptr;
 }
 
@@ -686,15 +758,15 @@ double chunk_cost(const Variant &v, double pen, const LinearItem *items, int c0,
     double span = 0.0, extra = 0.0;
     int64_t tiles = 0;
     for (int i = c0; i < c1; ++i) {
-        tiles += mbk(i) * ((items[i].g.Ns + v.bn - 1) / v.bn) * ks[i - c0];
+        tiles += mbk(i) * ((result_columns(items[i]) + v.bn - 1) / v.bn) * ks[i - c0];
         if (ks[i - c0] > 1) // partials written and read once, ~3.3 KB per clock
-            extra += 2.0 * ks[i - c0] * (double)items[i].M * (double)items[i].g.Ns * 4 / 3333.0;
+            extra += 2.0 * ks[i - c0] * (double)items[i].M * (double)result_columns(items[i]) * 4 / 3333.0;
     }
     if (tiles > 16384) { // large: every CU busy to the end, to a tile
         double work = 0.0, longest = 0.0;
         for (int i = c0; i < c1; ++i) {
             const double len = (double)kpad64(items[i].g.Ks) / 64.0 / ks[i - c0];
-            work += (double)(mbk(i) * ((items[i].g.Ns + v.bn - 1) / v.bn) * ks[i - c0]) * len;
+            work += (double)(mbk(i) * ((result_columns(items[i]) + v.bn - 1) / v.bn) * ks[i - c0]) * len;
             longest = len > longest ? len : longest;
         }
         span = work / 256.0 + longest;
@@ -705,7 +777,7 @@ double chunk_cost(const Variant &v, double pen, const LinearItem *items, int c0,
             cu.push(0.0);
         for (int i = c0; i < c1; ++i) {
             const double len = (double)kpad64(items[i].g.Ks) / 64.0 / ks[i - c0] * per_cu;
-            const int64_t T = mbk(i) * ((items[i].g.Ns + v.bn - 1) / v.bn) * ks[i - c0];
+            const int64_t T = mbk(i) * ((result_columns(items[i]) + v.bn - 1) / v.bn) * ks[i - c0];
             for (int64_t t = 0; t < T; ++t) {
                 const double f = cu.top() + len;
                 cu.pop();
@@ -763,7 +835,7 @@ double variant_cost(const Variant &v, const LinearItem *items, int n, std::vecto
         const int per_cu = q4 ? q4_per_cu(v) : 1;
         int64_t tiles = 0;
         for (int i = c0; i < c1; ++i)
-            tiles += ((items[i].M + v.bm - 1) / v.bm) * ((items[i].g.Ns + v.bn - 1) / v.bn);
+            tiles += ((items[i].M + v.bm - 1) / v.bm) * ((result_columns(items[i]) + v.bn - 1) / v.bn);
         int *kc = &(*ks)[c0];
         if (tiles < kSplitBelow)
             split_ks(items, c0, c1, (int)((256 + tiles - 1) / tiles), kc);
@@ -819,7 +891,8 @@ std::string plan_key(const LinearItem *items, int n, tsl_dtype wdtype) {
     for (int i = 0; i < n; ++i) {
         const int64_t f[3] = {items[i].M, items[i].g.Ks, items[i].g.Ns};
         std::memcpy(p, f, 24);
-        p[24] = (char)((items[i].accumulate ? 1 : 0) | (items[i].no_split ? 2 : 0));
+        p[24] = (char)((items[i].accumulate ? 1 : 0) | (items[i].no_split ? 2 : 0) |
+                       (dual(items[i]) ? 4 : 0));
         p += 25;
     }
     return key;
@@ -848,8 +921,13 @@ PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64
         double best_cost = 1e300;
         std::vector<int> ks;
         const Variant *vs = q4 ? kQ4Variants : kVariants;
-        const int nv = q4 ? (int)(sizeof(kQ4Variants) / sizeof(Variant))
-                          : (int)(sizeof(kVariants) / sizeof(Variant));
+        int nv = q4 ? (int)(sizeof(kQ4Variants) / sizeof(Variant))
+                    : (int)(sizeof(kVariants) / sizeof(Variant));
+        if (dual(items[0])) { // all of a call's items are, or none
+            vs = q4 ? kQ4DualVariants : kDualVariants;
+            nv = q4 ? (int)(sizeof(kQ4DualVariants) / sizeof(Variant))
+                    : (int)(sizeof(kDualVariants) / sizeof(Variant));
+        }
         for (int vi = 0; vi < nv; ++vi) {
             const double cost = variant_cost(vs[vi], items, n, &ks, q4);
             if (cost < best_cost - 1e-9) {
@@ -907,7 +985,7 @@ PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64
     for (int i = 0; i < n; ++i)
         if (best.ks[i] > 1) {
             best.p_off[i] = off;
-            off += ((size_t)best.ks[i] * (size_t)items[i].M * (size_t)items[i].g.Ns * 4 + 255) /
+            off += ((size_t)best.ks[i] * (size_t)items[i].M * (size_t)result_columns(items[i]) * 4 + 255) /
                    256 * 256;
         }
     best.ws_bytes = off;
@@ -1041,7 +1119,8 @@ hipError_t launch_prefill(const PrefillPlan &p, const LinearItem *items, int n, 
         hipError_t e = launch_xprep(p, items, 0, n, true, ws, stream);
         return e != hipSuccess ? e : launch_q4_gemm(p, items, n, ws, stream);
     }
-    GemmFn fn = pick(Variant{p.bm, p.bn, p.wm, p.wn});
+    const Variant var{p.bm, p.bn, p.wm, p.wn};
+    GemmFn fn = dual(items[0]) ? pick_dual(var) : pick(var);
     if (!fn)
         return hipErrorInvalidValue;
     for (int c0 = 0; c0 < n;) {
@@ -1060,6 +1139,7 @@ hipError_t launch_prefill(const PrefillPlan &p, const LinearItem *items, int n, 
             const LinearItem &L = items[c0 + i];
             const PackGeom &g = L.g;
             GemmItem &a = grp.it[i];
+            grp.set_ep(i, L.ep);
             const bool copied = p.x_first[c0 + i] >= 0;
             a.R = L.cat;
             a.seg = 0;
@@ -1087,12 +1167,12 @@ hipError_t launch_prefill(const PrefillPlan &p, const LinearItem *items, int n, 
             a.KT64 = (int32_t)(kpad64(g.Ks) / 64);
             a.M = L.M;
             a.MB = (int32_t)((L.M + p.bm - 1) / p.bm);
-            a.NB = (int32_t)((g.Ns + p.bn - 1) / p.bn);
+            a.NB = (int32_t)((result_columns(L) + p.bn - 1) / p.bn);
             a.ks = p.ks[c0 + i];
             a.P = reinterpret_cast<float *>(ws + p.p_off[c0 + i]);
             a.start = (int32_t)blocks;
             a.accumulate = L.accumulate;
-            a.flags = L.ydtype == TSL_BF16 ? kYBf16 : 0;
+            a.flags = (L.ydtype == TSL_BF16 ? kYBf16 : 0) | (L.ep ? kHasEpilogue : 0);
             blocks += (int64_t)a.MB * a.NB * a.ks;
         }
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * p.wm * p.wn), 0, stream, grp);
@@ -1111,7 +1191,7 @@ int64_t prefill_blocks(const PrefillPlan &p, const LinearItem *items, int n, int
         const int c1 = prefill_chunk_end(items, n, c0);
         int64_t blocks = 0;
         for (int i = c0; i < c1; ++i)
-            blocks += ((items[i].M + p.bm - 1) / p.bm) * ((items[i].g.Ns + p.bn - 1) / p.bn) *
+            blocks += ((items[i].M + p.bm - 1) / p.bm) * ((result_columns(items[i]) + p.bn - 1) / p.bn) *
                       p.ks[i];
         most = blocks > most ? blocks : most;
         c0 = c1;

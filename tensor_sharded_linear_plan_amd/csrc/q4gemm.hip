@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "internal.hpp"
 
@@ -59,16 +60,16 @@ struct Q4Item {
     int32_t nst;       // 32-k activation stages of the whole k-range
     int32_t MB, NB;    // tile grid
     int32_t pad0_, start; // first workgroup
-    int32_t flags, ks; // flags: bit 0 bf16 output, bit 1 accumulate
+    int32_t flags, ks; // flags: bit 0 bf16 output, bit 1 accumulate, bit 2 an epilogue
     int32_t seg, R;    // joined sum set: member table row (-1: none) and member count
 };
 static_assert(sizeof(Q4Item) == 96, "item table size");
-constexpr int kQ4YBf16 = 1, kQ4Accumulate = 2;
+constexpr int kQ4YBf16 = 1, kQ4Accumulate = 2, kQ4HasEpilogue = 4;
 
 // Joined sum sets of a launch: member r's records (the product runs over the
 // members' k-ranges laid end to end).
 
-struct Q4Group {
+struct Q4Group : Epilogues<kPrefillGroupMax> {
     int32_t n, pad_;
     Q4Item it[kPrefillGroupMax];
     const char *segw[kMaxJoined][kSetParts];
@@ -119,12 +120,15 @@ __device__ __forceinline__ void q4_pair(uint32_t sb, int f, uint32_t &ss, uint32
 // row tiles' activations and a few column tiles' records in its L2.
 constexpr int kBandM = 2;
 
-template <int BM, int BN, int WM, int WN>
+// DUAL: as the bf16 GEMM's (prefill.hip): 32 columns of the one weight and 32
+// of the other in turn.
+template <int BM, int BN, int WM, int WN, bool DUAL = false>
 __global__ void __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(WM * WN / 4 * q4_tiles_per_cu(BM, BN, WM),
                                        WM * WN / 4 * q4_tiles_per_cu(BM, BN, WM))))
     q4_gemm_kernel(Q4Group grp) {
     using C = Q4G<BM, BN, WM, WN>;
+    static_assert(!DUAL || C::NT % 2 == 0, "a wave holds both columns of a pair");
     __shared__ __attribute__((aligned(1024))) char lds[C::NS * C::ASLOT + C::NBS * C::BSLOT];
     __shared__ const char *mtab[kSetParts];
     const int lane = threadIdx.x & 63;
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     const int bm_cnt = a.MB - first_m < kBandM ? a.MB - first_m : kBandM;
     const int in_band = t - band * kBandM * a.NB;
     const int64_t mb = first_m + in_band % bm_cnt, nb = in_band / bm_cnt;
-    const int64_t m0 = mb * BM, n0 = nb * BN;
+    const int64_t m0 = mb * BM, n0 = nb * (DUAL ? BN / 2 : BN);
     // this split's k-range, in whole 128-k record blocks
     const int nblk = (a.nst + 3) / 4;
     const int blk0 = ksi * nblk / a.ks;
@@ -191,6 +195,11 @@ __global__ void __launch_bounds__(64 * WM * WN)
     // records with full 64-bit per-lane addresses.
     int KBm = a.KBm, tmax = a.Nt16 - 1;
     asm volatile("" : "+s"(KBm), "+s"(tmax));
+    // DUAL: from the first weight's records to the second's
+    int64_t to_up = 0;
+    if constexpr (DUAL) {
+        to_up = static_cast<const char *>(grp.ep(lo).up) - a.W;
+    }
     if (threadIdx.x < kSetParts)
         mtab[threadIdx.x] = a.R > 1 ? grp.segw[a.seg][threadIdx.x < a.R ? threadIdx.x : 0] : a.W;
     __syncthreads();
@@ -199,6 +208,10 @@ __global__ void __launch_bounds__(64 * WM * WN)
     // blk0 + b and the block's index within it
     auto block_src = [&](int b, int &lb) __attribute__((always_inline)) {
         const int gb = blk0 + b;
+        if constexpr (DUAL) {
+            lb = gb;
+            return mtab[0];
+        }
         const int r = gb / KBm;
         lb = gb - r * KBm;
         return mtab[r];
@@ -210,16 +223,18 @@ __global__ void __launch_bounds__(64 * WM * WN)
         const uint32_t dst = ldsb + bslot * C::BSLOT;
         if (c < C::CCW) {
             const int rr = wave + C::NW * c;
-            const int nt = t0 + rr < tmax ? t0 + rr : tmax;
+            const int rc = DUAL ? 2 * (rr >> 2) + (rr & 1) : rr; // 16-column tile of its weight
+            const int nt = t0 + rc < tmax ? t0 + rc : tmax;
             const uint32_t off = (uint32_t)((nt * KBm + lb) * kQ4Record) + 16 * (uint32_t)lane;
-            dma16_at(base + off, dst + rr * 1024);
+            dma16_at((DUAL && (rr >> 1 & 1) ? base + to_up : base) + off, dst + rr * 1024);
         } else {
             const int p = wave + C::NW * (c - C::CCW);
             const int rr = 2 * p + (lane >> 5);
-            const int nt = t0 + rr < tmax ? t0 + rr : tmax;
+            const int rc = DUAL ? 2 * (p >> 1) + (lane >> 5) : rr;
+            const int nt = t0 + rc < tmax ? t0 + rc : tmax;
             const uint32_t off = (uint32_t)((nt * KBm + lb) * kQ4Record) + kQ4PairsAt +
                                  4 * (uint32_t)(lane & 31);
-            dma4_at(base + off, dst + C::NR * 1024 + p * 256);
+            dma4_at((DUAL && (p & 1) ? base + to_up : base) + off, dst + C::NR * 1024 + p * 256);
         }
     };
     // the batch of stage kt (the first NS stages): its record block's copies
@@ -259,11 +274,13 @@ __global__ void __launch_bounds__(64 * WM * WN)
         const size_t eoff = ((size_t)a.Nt16 * a.KBm * kQ4Record + 255) / 256 * 256;
 #pragma unroll
         for (int j = 0; j < C::NT; ++j) {
-            int64_t n = n0 + C::TN * wn + 32 * j + (lane & 31);
+            int64_t n = n0 + (DUAL ? C::TN / 2 * wn + 32 * (j >> 1) : C::TN * wn + 32 * j) + (lane & 31);
             n = n < (int64_t)a.Nt16 * 16 ? n : (int64_t)a.Nt16 * 16 - 1;
             int f = -1000;
             for (int r = 0; r < a.R; ++r) {
                 const char *base = a.R > 1 ? grp.segw[a.seg][r] : a.W;
+                if (DUAL && (j & 1))
+                    base += to_up;
                 const int fr = reinterpret_cast<const int32_t *>(base + eoff)[n];
                 f = fr > f ? fr : f;
             }
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
 
     // ---- epilogue: acc reg r of lane l is row 8*(r/4) + 4*(l/32) + r%4, column l%32 ----
     const int64_t row0 = m0 + wm * C::TM + 4 * (lane >> 5);
-    const int64_t col0 = n0 + C::TN * wn + (lane & 31);
+    const int64_t col0 = n0 + C::TN / (DUAL ? 2 : 1) * wn + (lane & 31);
     const bool part = a.ks > 1;
     const bool ybf = part ? false : (a.flags & kQ4YBf16) != 0;
     const bool accu = part ? false : (a.flags & kQ4Accumulate) != 0;
@@ -530,6 +547,26 @@ __global__ void __launch_bounds__(64 * WM * WN)
             rblk[i] = re[m0 + wm * C::TM + i * 32 + (lane & 31)];
     }
     const bool hi_half = (lane >> 5) != 0;
+    // the result at register r of tile (i, j): undo the operand scales, one
+    // exact power-of-two step (rounded only where the result leaves the
+    // normal range)
+    auto result = [&](int i, int j, int r) __attribute__((always_inline)) {
+        const int q = 8 * (r >> 2) + (r & 3);
+        const int lo_e = __builtin_amdgcn_readlane(rblk[i], q);
+        const int hi_e = __builtin_amdgcn_readlane(rblk[i], q + 4);
+        return __builtin_amdgcn_ldexpf(acc[i][j][r], (hi_half ? hi_e : lo_e) + fcol[j]);
+    };
+    if constexpr (kEpilogue) {
+        if (!part && (DUAL || (a.flags & kQ4HasEpilogue))) {
+            ep_store<C::MT, C::NT, DUAL>(grp.ep(lo), a.Y, ybf, a.ldy, row0, col0, M, a.Ns, result);
+            return;
+        }
+    }
+    if constexpr (DUAL) {
+        float *const p0 = a.P + (int64_t)ksi * M * a.Ns;
+        dual_partials<C::MT, C::NT>(p0, p0 + (int64_t)a.ks * M * a.Ns, row0, col0, M, a.Ns, result);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < C::MT; ++i) {
 #pragma unroll
@@ -579,12 +616,26 @@ Q4Fn pick_q4(int bm, int bn, int *threads) {
     return nullptr;
 }
 
+// ... of dual products (tiles whose waves hold pairs of columns)
+Q4Fn pick_q4_dual(int bm, int bn, int *threads) {
+    if constexpr (kEpilogue) {
+#define TSL_Q4(BM_, BN_, WM_, WN_)                                                                 \
+    if (bm == BM_ && bn == BN_) {                                                                  \
+        *threads = 64 * WM_ * WN_;                                                                 \
+        return q4_gemm_kernel<BM_, BN_, WM_, WN_, kEpilogue>;                                      \
+    }
+        TSL_Q4(256, 256, 2, 4) TSL_Q4(128, 256, 2, 4) TSL_Q4(64, 256, 1, 4)
+#undef TSL_Q4
+    }
+    return nullptr;
+}
+
 } // namespace
 
 hipError_t launch_q4_gemm(const PrefillPlan &p, const LinearItem *items, int n, const char *ws,
                           hipStream_t stream) {
     int threads = 0;
-    Q4Fn fn = pick_q4(p.bm, p.bn, &threads);
+    Q4Fn fn = dual(items[0]) ? pick_q4_dual(p.bm, p.bn, &threads) : pick_q4(p.bm, p.bn, &threads);
     if (!fn)
         return hipErrorInvalidValue;
     for (int c0 = 0; c0 < n;) {
@@ -596,6 +647,7 @@ hipError_t launch_q4_gemm(const PrefillPlan &p, const LinearItem *items, int n, 
         for (; c < c1; ++c) {
             const LinearItem &L = items[c];
             const PackGeom &g = L.g;
+            grp.set_ep(grp.n, L.ep);
             Q4Item &a = grp.it[grp.n++];
             a.R = L.cat;
             a.seg = -1;
@@ -616,11 +668,12 @@ hipError_t launch_q4_gemm(const PrefillPlan &p, const LinearItem *items, int n, 
             a.KBm = (int32_t)(g.KT / L.cat);
             a.nst = (int32_t)(g.Ks / 32);
             a.MB = (int32_t)((L.M + p.bm - 1) / p.bm);
-            a.NB = (int32_t)((g.Ns + p.bn - 1) / p.bn);
+            a.NB = (int32_t)((result_columns(L) + p.bn - 1) / p.bn);
             a.ks = p.ks[c];
             a.P = reinterpret_cast<float *>(const_cast<char *>(ws) + p.p_off[c]);
             a.start = (int32_t)blocks;
-            a.flags = (L.ydtype == TSL_BF16 ? kQ4YBf16 : 0) | (L.accumulate ? kQ4Accumulate : 0);
+            a.flags = (L.ydtype == TSL_BF16 ? kQ4YBf16 : 0) | (L.accumulate ? kQ4Accumulate : 0) |
+                      (L.ep ? kQ4HasEpilogue : 0);
             blocks += (int64_t)a.MB * a.NB * a.ks;
         }
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), 0, stream, grp);

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "epilogue.hpp"
 #include "internal.hpp"
 
 namespace tsl {
@@ -70,7 +71,7 @@ struct FusedSet {
 };
 constexpr int kMaxFused = 16;
 
-struct SkinnyGroup {
+struct SkinnyGroup : Epilogues<kGroupMax> {
     int64_t M;
     int32_t n;
     int32_t xstr;     // streaming kernel, resident activations: LDS bytes per row
@@ -199,7 +200,11 @@ __global__ void __launch_bounds__(256) f32_kernel(SkinnyGroup grp) {
             const int64_t row = m0 + 16 * i + 4 * kg + r;
             if (row >= M)
                 continue;
-            const float v = acc[i][r];
+            float v = acc[i][r];
+            if constexpr (kEpilogue) {
+                if (a.ks == 1)
+                    v = ep_apply(grp.ep(lo), v, row, col);
+            }
             if (a.ks > 1) {
                 a.P[((int64_t)ksi * M + row) * a.Ns + col] = v;
             } else if (a.y_bf16) {
@@ -254,11 +259,14 @@ struct SB {
 // ONE: a single token row (M == 1, resident activations): only the first
 // accumulator row of each lane is ever stored, so the group epilogue
 // updates that one alone.
-template <int WT, int MT, int NTW, bool XRES, bool ONE = false, bool IDX = false>
+// DUAL: a wave's two tiles are the same columns of two weights, and the gate
+// combines their results before the store.
+template <int WT, int MT, int NTW, bool XRES, bool ONE = false, bool IDX = false, bool DUAL = false>
 __global__ void __launch_bounds__(256) stream_kernel(SkinnyGroup grp) {
     // IDX: items may read their rows through an index; only resident
     // kernels stage rows that way (once per workgroup, through xload)
     static_assert(!IDX || XRES, "rows through an index need the resident kernel");
+    static_assert(!DUAL || NTW == 2, "a dual product's wave holds one tile of each weight");
     using S = SB<WT, MT>;
     // XRES: [M rows][xstr bytes] sized at launch; else two [ROWS][XROW] windows
     extern __shared__ __attribute__((aligned(16))) char xl[];
@@ -293,9 +301,12 @@ __global__ void __launch_bounds__(256) stream_kernel(SkinnyGroup grp) {
     int64_t ntile[NTW];
 #pragma unroll
     for (int j = 0; j < NTW; ++j) {
-        ntile[j] = ((int64_t)tg * 4 + wave) * NTW + j;
+        ntile[j] = DUAL ? (int64_t)tg * 4 + wave : ((int64_t)tg * 4 + wave) * NTW + j;
         const int64_t nt = ntile[j] < a.Nt - 1 ? ntile[j] : a.Nt - 1;
-        wsrc[j] = static_cast<const char *>(a.B) + nt * (int64_t)a.KC * CS;
+        const void *w = a.B;
+        if constexpr (DUAL)
+            w = j ? grp.ep(lo).up : a.B;
+        wsrc[j] = static_cast<const char *>(w) + nt * (int64_t)a.KC * CS;
     }
 
     // weight ring: [slot][tile][load], plus scale/bias pairs for 4-bit
@@ -603,6 +614,29 @@ __global__ void __launch_bounds__(256) stream_kernel(SkinnyGroup grp) {
             step(I1{}, I2{}, I0{}, b + 1, Tail{});
     }
 
+    if constexpr (DUAL) {
+        const int64_t col = ntile[0] * 16 + (lane & 15);
+        if (col >= a.Ns)
+            return;
+        const int64_t plane = M * a.Ns;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < (ONE ? 1 : 4); ++r) {
+                const int64_t row = m0 + 16 * i + 4 * kg + r;
+                if (row >= M)
+                    continue;
+                if (a.ks > 1) { // the second weight's partials follow the first's
+                    float *p = a.P + ksi * plane + row * a.Ns + col;
+                    p[0] = acc[i][0][r];
+                    p[a.ks * plane] = acc[i][1][r];
+                } else {
+                    ep_put(a.Y, a.y_bf16, row * a.ldy + col,
+                           ep_gate(grp.ep(lo), acc[i][0][r], acc[i][1][r], row, col));
+                }
+            }
+        return;
+    }
     // acc[i][j] lane l: rows 16 i + 4 (l / 16) + r, column l % 16 of tile j
 #pragma unroll
     for (int j = 0; j < NTW; ++j) {
@@ -616,7 +650,11 @@ __global__ void __launch_bounds__(256) stream_kernel(SkinnyGroup grp) {
                 const int64_t row = m0 + 16 * i + 4 * kg + r;
                 if (row >= M)
                     continue;
-                const float v = acc[i][j][r];
+                float v = acc[i][j][r];
+                if constexpr (kEpilogue) {
+                    if (a.ks == 1 && a.fset < 0)
+                        v = ep_apply(grp.ep(lo), v, row, col);
+                }
                 if (a.ks > 1) {
                     a.P[((int64_t)ksi * M + row) * a.Ns + col] = v;
                 } else if (a.fset >= 0) { // a set member's product: written through
@@ -705,6 +743,8 @@ __global__ void __launch_bounds__(256) stream_kernel(SkinnyGroup grp) {
                     for (int q = 1; q < fs.R; ++q)
                         v = v + __hip_atomic_load(p + q * fs.pstride, __ATOMIC_RELAXED,
                                                   __HIP_MEMORY_SCOPE_AGENT);
+                    if constexpr (kEpilogue) // the set's, with its first member's item
+                        v = ep_apply(grp.ep(lo - a.fpos), v, row, col);
                     if (fs.y_bf16) {
                         __bf16 h = (__bf16)v;
                         static_cast<uint16_t *>(fs.Y)[row * fs.ldy + col] =
@@ -763,6 +803,25 @@ SkinnyFn pick_stream(int mt, int ntw, bool resident, bool one, bool idx) {
     }
 }
 
+// dual products: one tile of each weight per wave
+template <int WT>
+SkinnyFn pick_stream_dual(int mt, bool resident, bool one, bool idx) {
+    if constexpr (kEpilogue) {
+        if (resident && idx)
+            return one ? stream_kernel<WT, 1, 2, true, true, true, kEpilogue>
+                       : stream_kernel<WT, 1, 2, true, false, true, kEpilogue>;
+        if (resident)
+            return one ? stream_kernel<WT, 1, 2, true, true, false, kEpilogue>
+                       : stream_kernel<WT, 1, 2, true, false, false, kEpilogue>;
+        switch (mt) {
+        case 1: return stream_kernel<WT, 1, 2, false, false, false, kEpilogue>;
+        case 2: return stream_kernel<WT, 2, 2, false, false, false, kEpilogue>;
+        default: return stream_kernel<WT, 4, 2, false, false, false, kEpilogue>;
+        }
+    }
+    return nullptr;
+}
+
 } // namespace
 
 SkinnyPlan skinny_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t M) {
@@ -785,11 +844,13 @@ SkinnyPlan skinny_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t
         int64_t wg1 = 0;
         for (int i = 0; i < n; ++i)
             wg1 += (items[i].g.Nt + 3) / 4 * p.m_blocks[i];
-        p.ntw = rows > 16 || (rows > 4 && wg1 >= 2048) ? 2 : 1;
+        const bool two = n > 0 && dual(items[0]); // all of a call's items are, or none
+        p.ntw = two || rows > 16 || (rows > 4 && wg1 >= 2048) ? 2 : 1;
         const int bk = stream_bk(wdtype == TSL_Q4G64 ? W_Q4 : W_BF16);
         int64_t base = 0;
         for (int i = 0; i < n; ++i) {
-            p.n_groups[i] = (items[i].g.Nt + 4 * p.ntw - 1) / (4 * p.ntw);
+            const int64_t per = two ? 4 : 4 * p.ntw; // column tiles of a workgroup
+            p.n_groups[i] = (items[i].g.Nt + per - 1) / per;
             base += p.n_groups[i] * p.m_blocks[i];
         }
         const int64_t ks_want = base > 0 ? (512 + base - 1) / base : 1;
@@ -840,7 +901,7 @@ SkinnyPlan skinny_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t
     for (int i = 0; i < n; ++i) {
         p.ws_off[i] = off;
         if (p.ks[i] > 1)
-            off += ((size_t)p.ks[i] * (size_t)items[i].M * (size_t)items[i].g.Ns * sizeof(float) +
+            off += ((size_t)p.ks[i] * (size_t)items[i].M * (size_t)result_columns(items[i]) * sizeof(float) +
                     255) / 256 * 256;
     }
     // sum sets the streaming launch finishes: resident launches (a few token
@@ -901,7 +962,10 @@ hipError_t launch_skinny(const SkinnyPlan &p, const LinearItem *items, int n, ts
         idx = idx || items[i].ridx != nullptr;
     if (idx && (!p.stream || !p.resident))
         return hipErrorInvalidValue;
+    const bool two = n > 0 && dual(items[0]);
     SkinnyFn fn = wdtype == TSL_F32    ? pick_f32(p.mt)
+                  : two ? (wdtype == TSL_BF16 ? pick_stream_dual<W_BF16>(p.mt, p.resident, M == 1, idx)
+                                              : pick_stream_dual<W_Q4>(p.mt, p.resident, M == 1, idx))
                   : wdtype == TSL_BF16 ? pick_stream<W_BF16>(p.mt, p.ntw, p.resident, M == 1, idx)
                                        : pick_stream<W_Q4>(p.mt, p.ntw, p.resident, M == 1, idx);
     if (!fn)
@@ -944,6 +1008,7 @@ hipError_t launch_skinny(const SkinnyPlan &p, const LinearItem *items, int n, ts
         for (int i = 0; i < cn; ++i) {
             const LinearItem &L = items[c0 + i];
             SkinnyItem &a = grp.it[i];
+            grp.set_ep(i, p.fset[c0 + i] >= 0 ? L.fset_ep : L.ep);
             a.B = L.packed;
             a.X = L.X;
             a.ridx = L.ridx;
