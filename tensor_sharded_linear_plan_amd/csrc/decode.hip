@@ -1,0 +1,348 @@
+// Products of a few token rows (up to 16) with an epilogue, in one launch:
+// one rank's Y = act(X W + bias) + residual, a sum set of row shards, or a
+// gated pair act(X W_0) * (X W_1) (mlxcel manual "Tensor parallelism",
+// "Column Parallel" / "Row Parallel").
+//
+// At these sizes a call streams some tens of MB of weights, and its time is
+// the launch and a few memory latencies as much as bytes; a second launch
+// that adds k-partials costs as much as the products.  So the k-range is
+// split inside a workgroup: it owns one 16-column tile (gated: that tile of
+// both weights) and its W waves take consecutive runs of the whole k-range --
+// a sum set's members laid end to end in item order -- which meet in LDS, are
+// added in wave order (so in k order) and go through the epilogue in
+// registers.  Nothing returns to memory but the result; no workspace, no
+// atomics, the same bits every time.  W is 16 for up to 256 tiles, 8 up to
+// 512, else 4: about 4096 waves fill the chip's 1024 SIMDs fourfold.
+//
+// A wave reads its weights as the streaming kernel does (contiguous 1 KB wave
+// loads in MFMA operand order, 4-bit groups applied exactly: skinny.hip),
+// one unit (128 k of 4-bit, 64 k of bf16 weights) ahead, and its activation
+// fragments straight from global memory -- a wave reads only its own k-run of
+// X, from L2, so there is nothing to share through LDS and no barrier before
+// the sum.  Measured: one rank's 4-bit gate and up, 1 row, 3584 -> 2 x 4736
+// (19 MB), 8.0 us a call where the host's enqueue takes as long; 4 ranks'
+// down shards, 4 rows, 18944 -> 3584 (38 MB), 15.2 us (2.5 TB/s; with a
+// separate launch for the k-partials 14.6 and 19.0).  What bounds the larger
+// is the 4-bit expansion's VALU work per record beside 16 waves a CU.
+#include <hip/hip_runtime.h>
+
+#include "device.hpp"
+#include "epilogue.hpp"
+#include "internal.hpp"
+
+namespace tsl {
+namespace {
+
+constexpr int kItems = 64, kMembers = 128;
+
+struct Member {
+    const char *B;       // packed weights
+    const uint16_t *X;
+    const int32_t *ridx; // row m reads X row ridx[m] (zeros outside [0, x_rows)); null: row m
+    int64_t x_rows, ldx;
+    int32_t Ks, units;   // k, and units of it
+    int32_t KC, pad_;    // chunks per column tile in B
+};
+struct Item {
+    void *Y;
+    int64_t ldy;
+    int32_t M, Ns;
+    int32_t first, units; // its members from `first` on; their units together
+    int32_t start, y_bf16;
+};
+struct Group : Epilogues<kItems> {
+    int32_t n, pad_;
+    Item it[kItems];
+    Member mb[kMembers];
+};
+
+template <bool Q4> struct Unit {
+    static constexpr int K = Q4 ? 128 : 64;
+    static constexpr int CHUNKS = Q4 ? 1 : 2;          // 16-byte weight loads per lane
+    static constexpr int64_t CS = Q4 ? kQ4Record : 1024; // bytes per chunk
+    static constexpr int FR = K / 32;                  // activation fragments
+};
+
+template <bool Q4, bool DUAL>
+__global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
+    using C = Unit<Q4>;
+    constexpr int NT = DUAL ? 2 : 1;
+    extern __shared__ __attribute__((aligned(16))) f32x4 red[]; // [waves][NT][64]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int W = blockDim.x >> 6;
+    const int bid = blockIdx.x;
+    int lo = 0, hi = grp.n - 1; // last item whose first workgroup is <= bid
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (grp.it[mid].start <= bid)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const Item &a = grp.it[lo];
+    const int64_t tile = bid - a.start;
+    const int u0 = wave * a.units / W, u1 = (wave + 1) * a.units / W;
+    const int row = lane & 15, kg = lane >> 4;
+    const int64_t up = DUAL ? static_cast<const char *>(grp.ep(lo).up) - grp.mb[a.first].B : 0;
+
+    // where the next unit comes from: unit lu of member r.  Rows past M read
+    // row 0 (finite or not, their results are not stored; masking their lanes
+    // off measured 16.1 against 15.2 us, 4 rows x 18944 x 3584); a row whose
+    // index lies outside X reads row 0 and is masked to zeros.
+    int r = a.first, lu = u0;
+    const char *wp[NT];
+    const uint16_t *xp = nullptr; // this lane's row and k-run
+    uint32_t keep = ~0u;
+    bool masked = false; // some row of the wave may be (uniform)
+    int Ks = 0;
+    auto enter = [&]() __attribute__((always_inline)) {
+        const Member &b = grp.mb[r];
+        Ks = b.Ks;
+        wp[0] = b.B + tile * b.KC * C::CS;
+        if constexpr (DUAL)
+            wp[1] = wp[0] + up;
+        int64_t s = row < a.M ? row : 0;
+        masked = b.ridx != nullptr;
+        if (masked) {
+            s = b.ridx[s];
+            const bool ok = s >= 0 && s < b.x_rows;
+            keep = ok ? ~0u : 0u;
+            s = ok ? s : 0;
+        }
+        xp = b.X + s * b.ldx + 8 * kg;
+    };
+    struct Regs {
+        u32x4 w[NT][C::CHUNKS];
+        u32x2 sb[NT];
+        u32x4 x[C::FR];
+    };
+    auto load = [&](Regs &g) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const char *rec = wp[j] + (int64_t)lu * C::CHUNKS * C::CS;
+#pragma unroll
+            for (int l = 0; l < C::CHUNKS; ++l)
+                g.w[j][l] = *reinterpret_cast<const u32x4 *>(rec + l * C::CS + lane * 16);
+            if constexpr (Q4)
+                g.sb[j] = *reinterpret_cast<const u32x2 *>(rec + kQ4PairsAt + (lane & 15) * 8);
+        }
+        // 4-bit k-ranges are whole 64-k groups and bf16 units 64 k, so that
+        // every condition here is uniform but in a ragged last bf16 unit
+        const uint16_t *x = xp + lu * C::K;
+        const int left = Ks - lu * C::K;
+        if (left >= C::K) {
+#pragma unroll
+            for (int f = 0; f < C::FR; ++f)
+                g.x[f] = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+        } else {
+#pragma unroll
+            for (int f = 0; f < C::FR; ++f) {
+                const int k = 32 * f + 8 * kg;
+                u32x4 v = {0, 0, 0, 0};
+                if (k + 8 <= left) {
+                    v = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+                } else if (k < left) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t l0 = k + 2 * e < left ? x[32 * f + 2 * e] : 0u;
+                        const uint32_t h0 = k + 2 * e + 1 < left ? x[32 * f + 2 * e + 1] : 0u;
+                        v[e] = l0 | (h0 << 16);
+                    }
+                }
+                g.x[f] = v;
+            }
+        }
+        if (masked) {
+#pragma unroll
+            for (int f = 0; f < C::FR; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    g.x[f][e] &= keep;
+        }
+        ++lu;
+    };
+    f32x4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](const Regs &g) __attribute__((always_inline)) {
+        if constexpr (!Q4) {
+#pragma unroll
+            for (int f = 0; f < C::FR; ++f)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[j] = mfma_bf16(__builtin_bit_cast(bf16x8, g.x[f]),
+                                       __builtin_bit_cast(bf16x8, g.w[j][f]), acc[j]);
+        } else {
+            const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u,
+                                                                 0x3F803F80u, 0x3F803F80u});
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            f32x4 xs = zero, ag[NT];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const bf16x8 xa = __builtin_bit_cast(bf16x8, g.x[t]);
+                xs = mfma_bf16(xa, ones, (t & 1) ? xs : zero);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    ag[j] = mfma_bf16(xa, q4_to_bf16_plus128(g.w[j][0][t]), (t & 1) ? ag[j] : zero);
+                if (t & 1) { // end of a group: y += s sum(x (128 + q)) + (b - 128 s) sum(x)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint32_t sbp = g.sb[j][t >> 1];
+                        const float sc = bf16_lo(sbp);
+                        const float cb = __builtin_fmaf(-128.f, sc, bf16_hi(sbp));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            acc[j][q] = __builtin_fmaf(sc, ag[j][q], acc[j][q]);
+                            acc[j][q] = __builtin_fmaf(cb, xs[q], acc[j][q]);
+                        }
+                    }
+                }
+            }
+        }
+    };
+    if (u0 < u1) {
+        while (lu >= grp.mb[r].units) {
+            lu -= grp.mb[r].units;
+            ++r;
+        }
+        enter();
+        auto next = [&](Regs &g) __attribute__((always_inline)) {
+            if (lu == grp.mb[r].units) { // the next member's k-range
+                lu = 0;
+                ++r;
+                enter();
+            }
+            load(g);
+        };
+        Regs g0, g1;
+        load(g0);
+        if constexpr (DUAL) { // a second unit's registers would spill
+            for (int u = u0 + 1; u < u1; ++u) {
+                compute(g0);
+                next(g0);
+            }
+            compute(g0);
+        } else {
+            int u = u0;
+            // steady state: each step's prefetch exists, so that the wait
+            // counts at the loop head are exact
+            for (; u + 2 < u1; u += 2) {
+                next(g1);
+                compute(g0);
+                next(g0);
+                compute(g1);
+            }
+            if (u + 1 < u1) {
+                next(g1);
+                compute(g0);
+                compute(g1);
+            } else {
+                compute(g0);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        red[(wave * NT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        for (int w = 1; w < W; ++w) {
+            const f32x4 v = red[(w * NT + j) * 64 + lane];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[j][q] += v[q];
+        }
+    // lane holds rows 4 (lane / 16) + q of column lane % 16
+    const int64_t col = tile * 16 + (lane & 15);
+    if (col >= a.Ns)
+        return;
+    const Epilogue e = grp.ep(lo);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t m = 4 * kg + q;
+        if (m >= a.M)
+            continue;
+        float v;
+        if constexpr (DUAL)
+            v = ep_gate(e, acc[0][q], acc[1][q], m, col);
+        else
+            v = ep_apply(e, acc[0][q], m, col);
+        ep_put(a.Y, a.y_bf16, m * a.ldy + col, v);
+    }
+}
+
+typedef void (*DecodeFn)(Group);
+
+} // namespace
+
+bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M) {
+    if (wdtype == TSL_F32 || M > kDecodeRows)
+        return false;
+    int64_t tiles = 0;
+    bool any = false;
+    for (const LinearItem &L : items) {
+        any = any || L.ep;
+        if (L.accumulate || L.set_len > kSetParts)
+            return false;
+        if (L.set_len > 0)
+            tiles += L.g.Nt;
+    }
+    return any && tiles <= kDecodeTiles;
+}
+
+hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
+                         hipStream_t stream) {
+    const bool q4 = wdtype == TSL_Q4G64, two = dual(items[0]);
+    const DecodeFn fn = q4 ? (two ? decode_kernel<true, true> : decode_kernel<true, false>)
+                           : (two ? decode_kernel<false, true> : decode_kernel<false, false>);
+    int64_t tiles = 0;
+    for (const LinearItem &L : items)
+        if (L.set_len > 0)
+            tiles += L.g.Nt;
+    const int waves = tiles <= 256 ? 16 : (tiles <= 512 ? 8 : 4);
+    for (size_t i = 0; i < items.size();) {
+        Group grp{};
+        int members = 0;
+        int64_t blocks = 0;
+        for (; i < items.size() && grp.n < kItems && members + items[i].set_len <= kMembers;
+             i += items[i].set_len) {
+            const LinearItem &L = items[i];
+            grp.set_ep(grp.n, L.ep);
+            Item &a = grp.it[grp.n++];
+            a.Y = L.Y;
+            a.ldy = L.ldy;
+            a.M = (int32_t)L.M;
+            a.Ns = (int32_t)L.g.Ns;
+            a.first = members;
+            a.y_bf16 = L.ydtype == TSL_BF16;
+            a.start = (int32_t)blocks;
+            blocks += L.g.Nt;
+            for (int r = 0; r < L.set_len; ++r) {
+                const LinearItem &P = items[i + r];
+                Member &m = grp.mb[members++];
+                m.B = static_cast<const char *>(P.packed);
+                m.X = static_cast<const uint16_t *>(P.X);
+                m.ridx = P.ridx;
+                m.x_rows = P.x_rows;
+                m.ldx = P.ldx;
+                m.Ks = (int32_t)P.g.Ks;
+                m.KC = (int32_t)P.g.KT;
+                m.units = (int32_t)(q4 ? P.g.KT : P.g.KT / 2);
+                a.units += m.units;
+            }
+        }
+        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * waves),
+                           (size_t)waves * (two ? 2 : 1) * 64 * 16, stream, grp);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+} // namespace tsl

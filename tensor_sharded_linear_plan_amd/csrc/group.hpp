@@ -385,6 +385,10 @@ inline size_t plan_row_gathers(std::vector<LinearItem> *items, tsl_dtype wdtype,
 inline size_t group_workspace(const std::vector<LinearItem> &in, tsl_dtype wdtype, int64_t M) {
     if (M == 0 || in.empty())
         return 0;
+    if constexpr (kEpilogue) {
+        if (decode_applies(in, wdtype, M))
+            return 0;
+    }
     std::vector<LinearItem> src = in;
     std::vector<RowGather> jobs;
     const size_t gathered = plan_row_gathers(&src, wdtype, M, nullptr, &jobs);
@@ -400,6 +404,10 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
                      void *workspace, size_t ws_bytes, void *stream) {
     if (M == 0)
         return TSL_OK;
+    if constexpr (kEpilogue) {
+        if (decode_applies(in, wdtype, M))
+            return from_hip(launch_decode(in, wdtype, static_cast<hipStream_t>(stream)));
+    }
     // (a null or short workspace is rejected below, before any launch)
     char *const ws0 = static_cast<char *>(workspace);
     std::vector<LinearItem> src = in;
