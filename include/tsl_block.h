@@ -249,7 +249,8 @@ tsl_status shard_linear_grad_workspace_size(const tsl_shard *shard, tsl_dtype wd
  *   db:       null, or DEVICE binary32 [n_len], summed from the unrounded dZ
  *             in a fixed order.
  * Products accumulate in binary32; with an activation dZ is their operand
- * rounded once to wdtype.  Slope of relu at 0 is 0.  M == 0 writes zero
+ * rounded once to wdtype (BF16 and M * n_len up to 2^16: together with what
+ * that rounding left, so that it does not show).  Slope of relu at 0 is 0.  M == 0 writes zero
  * weight and bias gradients (unless they accumulate).  M, k_len, n_len and
  * input strides below 2^22.  No output may share an element with an input,
  * another output or the workspace.  Errors as shard_linear.
@@ -278,8 +279,8 @@ tsl_status shard_gated_grad_workspace_size(const tsl_shard *gate, const tsl_shar
  *          the size of either buffer.
  *   dW_gate, dW_up: both or neither, with the strides of shard_linear_grad's
  *          dW.
- * dG and dU are the products' operands, rounded once to wdtype; the two
- * terms of dX are added in binary32.  Everything else as shard_linear_grad.
+ * dG and dU are the products' operands, rounded as shard_linear_grad's dZ;
+ * the two terms of dX are added in binary32.  Everything else as shard_linear_grad.
  */
 tsl_status shard_gated_grad(const tsl_shard *gate, const tsl_shard *up, tsl_dtype wdtype,
                             const void *packed_gate_t, const void *packed_up_t,

@@ -543,34 +543,61 @@ struct GradCall {
 // Workspace parts of a call and the products it runs.  Everything but the
 // addresses follows from the shapes and from which outputs are wanted.
 struct GradPlan {
-    size_t row[2] = {}, tr[2] = {}, xt = 0, part = 0, products = 0, total = 0;
+    size_t row[2] = {}, row_lo[2] = {}, tr[2] = {}, xt = 0, part = 0, products = 0, total = 0;
     int64_t K = 0, N = 0, Mp = 0, Np = 0;
-    bool need_row = false, need_tr = false;
+    int64_t Mt = 0; // rows of the transposed copies: Mp, or 2 Mp with split
+    bool need_row = false, need_tr = false, split = false;
 };
 
+// bf16 products read dZ rounded to bf16.  Over many entries those roundings
+// average to the error of the result's own (2^-9 or so of it, together 1.41
+// times); up to this many entries of dZ they need not, and what the rounding
+// left goes along as further operands (the products are bound by latency and
+// the weights' bytes there, not by their operations).  Measured, gated, 3 x
+// 1500 -> 700: error 0.0027 without, 0.0017 with, as one rounding has.
+constexpr int64_t kSplitEntries = int64_t(1) << 16;
+
 bool nk_order(const GradCall &c) { return c.sk == 1 && c.sn != 1; }
+
+// dX and dW share a launch where both take the same kernels.
+bool one_group(const GradCall &c, const GradPlan &p) {
+    return c.dX && c.dW[0] &&
+           use_skinny(c.wdtype, c.M) == use_skinny(c.wdtype, nk_order(c) ? p.N : p.K);
+}
+
+// dX of a few rows alone in its call takes the one-launch form (decode.hip),
+// which products with an epilogue take -- here one that changes nothing.
+const Epilogue kNoEpilogue;
+bool few_rows(const GradCall &c, const GradPlan &p) {
+    return c.M <= kDecodeRows && !one_group(c, p);
+}
 
 // The products of a call: dX (a set of n_w), then dW of each weight, with
 // the operands of `p` at ws (null: sizing).
 void grad_items(const GradCall &c, const GradPlan &p, const PackGeom &gt, char *ws,
                 std::vector<LinearItem> *dx, std::vector<LinearItem> *dw) {
     auto at = [&](size_t off) { return ws ? ws + off : nullptr; };
+    const int len = c.n_w * (p.split ? 2 : 1);
     if (c.dX)
-        for (int q = 0; q < c.n_w; ++q) {
+        for (int s = 0; s < len; ++s) {
+            const int q = p.split ? s / 2 : s;
+            const size_t row = p.split && s % 2 ? p.row_lo[q] : p.row[q];
             LinearItem L;
             L.g = gt;
             L.M = c.M;
             L.packed = c.packed_t[q];
-            L.X = p.need_row ? at(p.row[q]) : c.a;
+            L.X = p.need_row ? at(row) : c.a;
             L.ldx = p.need_row ? p.Np : c.lda;
             // the copy's columns are zero up to Np, as the packed rows are
             if (p.need_row)
                 L.g.Ks = p.Np;
-            L.Y = q == 0 ? c.dX : nullptr;
-            L.ldy = q == 0 ? c.lddx : 0;
+            L.Y = s == 0 ? c.dX : nullptr;
+            L.ldy = s == 0 ? c.lddx : 0;
             L.ydtype = (tsl_dtype)c.dxdtype;
-            L.set_len = q == 0 ? c.n_w : 0;
-            L.set_pos = q;
+            L.set_len = s == 0 ? len : 0;
+            L.set_pos = s;
+            if (s == 0 && few_rows(c, p))
+                L.ep = &kNoEpilogue;
             dx->push_back(L);
         }
     if (!c.dW[0])
@@ -579,26 +606,20 @@ void grad_items(const GradCall &c, const GradPlan &p, const PackGeom &gt, char *
         LinearItem L;
         const bool nk = nk_order(c);
         const int64_t cols = nk ? p.K : p.N;
-        L.g.Ks = L.g.Kpad = p.Mp;
+        L.g.Ks = L.g.Kpad = p.Mt;
         L.g.Ns = cols;
         L.g.Nt = (cols + 15) / 16;
-        L.g.KT = p.Mp / (c.wdtype == TSL_F32 ? 16 : 32);
+        L.g.KT = p.Mt / (c.wdtype == TSL_F32 ? 16 : 32);
         L.M = nk ? p.N : p.K;
         L.X = at(nk ? p.tr[q] : p.xt);
         L.packed = at(nk ? p.xt : p.tr[q]);
-        L.ldx = p.Mp;
+        L.ldx = p.Mt;
         L.Y = c.dW[q];
         L.ldy = nk ? c.sn : c.sk;
         L.ydtype = (tsl_dtype)c.dwdtype;
         L.accumulate = c.accumulate;
         dw->push_back(L);
     }
-}
-
-// dX and dW share a launch where both take the same kernels.
-bool one_group(const GradCall &c, const GradPlan &p) {
-    return c.dX && c.dW[0] &&
-           use_skinny(c.wdtype, c.M) == use_skinny(c.wdtype, nk_order(c) ? p.N : p.K);
 }
 
 // Fills the plan; gt receives the geometry of the packed transposed weight.
@@ -629,6 +650,9 @@ tsl_status plan_grad(const GradCall &c, GradPlan *p, PackGeom *gt) {
     // without an activation dY itself feeds dX
     p->need_row = c.dX && (c.n_w > 1 || c.act != TSL_ACT_NONE);
     p->need_tr = c.dW[0] != nullptr;
+    p->split = c.wdtype == TSL_BF16 && c.M * p->N <= kSplitEntries &&
+               (c.n_w > 1 || (c.act != TSL_ACT_NONE && c.act != TSL_ACT_RELU));
+    p->Mt = p->split ? 2 * p->Mp : p->Mp;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -641,11 +665,13 @@ tsl_status plan_grad(const GradCall &c, GradPlan *p, PackGeom *gt) {
     for (int q = 0; q < c.n_w; ++q) {
         if (p->need_row)
             p->row[q] = take((size_t)c.M * p->Np * e);
+        if (p->need_row && p->split)
+            p->row_lo[q] = take((size_t)c.M * p->Np * e);
         if (p->need_tr)
-            p->tr[q] = take(tr_cols(p->N, !nk_order(c)) * p->Mp * e);
+            p->tr[q] = take(tr_cols(p->N, !nk_order(c)) * p->Mt * e);
     }
     if (p->need_tr)
-        p->xt = take(tr_cols(p->K, nk_order(c)) * p->Mp * e);
+        p->xt = take(tr_cols(p->K, nk_order(c)) * p->Mt * e);
     if (c.db)
         p->part = take((size_t)(p->Mp / 64) * ((p->N + 7) / 8 * 8) * 4);
     p->products = off;
@@ -766,8 +792,10 @@ tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *s
         j.packed = !nk;
         for (int q = 0; q < c.n_w; ++q) {
             j.row[q] = p.need_row ? ws + p.row[q] : nullptr;
+            j.row_lo[q] = p.need_row && p.split ? ws + p.row_lo[q] : nullptr;
             j.tr[q] = p.need_tr ? ws + p.tr[q] : nullptr;
         }
+        j.split = p.split;
         j.part = c.db ? reinterpret_cast<float *>(ws + p.part) : nullptr;
         j.M = M;
         j.N = N;
@@ -777,6 +805,7 @@ tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *s
         j.a = c.X;
         j.lda = c.ldx;
         j.tr[0] = ws + p.xt;
+        j.split = p.split;
         j.packed = nk;
         j.M = M;
         j.N = K;

@@ -13,6 +13,8 @@
 //     runs along the token rows, whole 1 KB tiles of the packed layout;
 //   - the column sums of the unrounded dZ (the bias gradient), one partial per
 //     64 rows.
+// With few entries (split) what the rounding of dZ left is an operand of its
+// own, rows and k-range doubled, so that its error does not show.
 // Bound by bytes: gated, 3 values read and 4 written per element.
 #include "device.hpp"
 #include "epilogue.hpp"
@@ -42,10 +44,10 @@ template <> struct Elem<float> {
 };
 
 // One transposed copy of the tile's values v (rows 2 r, 2 r + 1 of the
-// thread's 8 columns, zero outside the matrix).
+// thread's 8 columns, zero outside the matrix) at rows m0 on of the copy's Mt.
 template <typename T>
 __device__ __forceinline__ void transpose_tile(const GradJob &g, void *out, const f32x8 (&v)[2],
-                                               uint32_t *lds, int64_t m0, int64_t n0) {
+                                               uint32_t *lds, int64_t m0, int64_t Mt, int64_t n0) {
     using E = Elem<T>;
     const int cc = threadIdx.x & 7, r = threadIdx.x >> 3;
     __syncthreads(); // the tile's last readers are done
@@ -62,7 +64,6 @@ __device__ __forceinline__ void transpose_tile(const GradJob &g, void *out, cons
     __syncthreads();
     constexpr int PER = 16 / sizeof(T);      // rows of a 16-byte run
     constexpr int RUNS = kTile / PER;        // runs of a column of the tile
-    const int64_t Mp = (g.M + 63) / 64 * 64; // runs of a whole column: Mp / PER
     const int64_t cols = g.packed ? (g.N + 15) / 16 * 16 : g.N;
 #pragma unroll
     for (int q = 0; q < kTile * RUNS / 256; ++q) {
@@ -85,11 +86,22 @@ __device__ __forceinline__ void transpose_tile(const GradJob &g, void *out, cons
         for (int i = 0; i < 4; ++i)
             w[i] = lds[n * E::LDW + c * 4 + i];
         const int64_t cg = m0 / PER + c, col = n0 + n;
-        const int64_t at = g.packed ? ((col >> 4) * (Mp / PER / 4) + (cg >> 2)) * 64 +
+        const int64_t at = g.packed ? ((col >> 4) * (Mt / PER / 4) + (cg >> 2)) * 64 +
                                           (cg & 3) * 16 + (col & 15)
-                                    : col * (Mp / PER) + cg;
+                                    : col * (Mt / PER) + cg;
         static_cast<u32x4 *>(out)[at] = w;
     }
+}
+
+// What rounding to bf16 left of 8 values (exact; nothing of one that is, or
+// rounds to, an infinity or a NaN).
+__device__ __forceinline__ f32x8 left_of(f32x8 v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float h = (float)(__bf16)v[i];
+        v[i] = __builtin_isfinite(h) ? v[i] - h : 0.f;
+    }
+    return v;
 }
 
 template <typename T>
@@ -103,7 +115,7 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(GradJobs jobs) {
     const int64_t mb = b / g.nblk, m0 = mb * kTile, n0 = (int64_t)(b % g.nblk) * kTile;
     const int cc = threadIdx.x & 7, r = threadIdx.x >> 3;
     const int64_t col = n0 + 8 * cc, N = g.N;
-    f32x8 z[2], y[2]; // dZ (gated: dG, dU) of rows m0 + 2 r and the next
+    f32x8 z[2], y[2] = {}; // dZ (gated: dG, dU) of rows m0 + 2 r and the next
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int64_t m = m0 + 2 * r + q;
@@ -160,10 +172,29 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(GradJobs jobs) {
             g.part[mb * ((N + 7) / 8 * 8) + n] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
         }
     }
+    const int64_t Mp = (g.M + 63) / 64 * 64, Mt = g.split ? 2 * Mp : Mp;
     if (g.tr[0])
-        transpose_tile<T>(g, g.tr[0], z, lds, m0, n0);
+        transpose_tile<T>(g, g.tr[0], z, lds, m0, Mt, n0);
     if (g.tr[1])
-        transpose_tile<T>(g, g.tr[1], y, lds, m0, n0);
+        transpose_tile<T>(g, g.tr[1], y, lds, m0, Mt, n0);
+    if (!E::bf || !g.split)
+        return;
+    if (g.kind != kGradCopy) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            z[q] = left_of(z[q]);
+            y[q] = left_of(y[q]);
+            const int64_t m = m0 + 2 * r + q;
+            if (m < g.M && g.row_lo[0])
+                store8<true>(static_cast<T *>(g.row_lo[0]) + m * g.ld_row, E::bf, col, g.ld_row, z[q]);
+            if (m < g.M && g.row_lo[1])
+                store8<true>(static_cast<T *>(g.row_lo[1]) + m * g.ld_row, E::bf, col, g.ld_row, y[q]);
+        }
+    }
+    if (g.tr[0])
+        transpose_tile<T>(g, g.tr[0], z, lds, Mp + m0, Mt, n0);
+    if (g.tr[1])
+        transpose_tile<T>(g, g.tr[1], y, lds, Mp + m0, Mt, n0);
 }
 
 template <typename T>

@@ -159,10 +159,14 @@ struct GradJob {
     int64_t lda = 0, ldb = 0, ldc = 0;
     // row-major results (null: not wanted), zero columns up to ld_row
     void *row[2] = {};
+    void *row_lo[2] = {}; // split: what rounding left of them
     int64_t ld_row = 0;
-    // transposed results (null: not wanted): [N][Mp] rows, or (packed) the
-    // packed layout of a weight W[Mp][N]; zero from M to Mp = M rounded up to 64
+    // transposed results (null: not wanted): [N][Mt] rows, or (packed) the
+    // packed layout of a weight W[Mt][N]; Mt is Mp = M rounded up to 64 (zero
+    // from M on), and 2 Mp with split: then what rounding left of the first
+    // Mp rows (a copied job: those rows again)
     void *tr[2] = {};
+    int32_t split = 0;
     int32_t packed = 0;
     int32_t kind = kGradCopy, act = 0;
     // binary32 column sums of the result, one row per 64 rows of the job
