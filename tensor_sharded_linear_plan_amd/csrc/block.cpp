@@ -144,7 +144,7 @@ extern "C" tsl_status add_rms_norm(int32_t n_parts, const void *const *parts, ts
 namespace {
 
 size_t norm_grad_bytes(int64_t M, int64_t n) {
-    return (size_t)norm_grad_groups(M, n) * (size_t)((n + 7) / 8 * 8) * 4;
+    return (size_t)norm_grad_partials(M, n) * (size_t)((n + 7) / 8 * 8) * 4;
 }
 
 } // namespace
@@ -215,7 +215,6 @@ extern "C" tsl_status add_rms_norm_grad(int64_t M, int64_t n, const void *dY, ts
         a.ldx = ldx;
         a.ld_dres = ld_dres;
         a.lddx = lddx;
-        a.row_groups = norm_grad_groups(M, n);
         a.eps = eps;
         a.dy_bf16 = dydtype == TSL_BF16;
         a.x_bf16 = xdtype == TSL_BF16;

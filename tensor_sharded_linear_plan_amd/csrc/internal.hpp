@@ -131,16 +131,17 @@ struct NormGradArgs {
     const float *rstd;                  // null: recomputed from X
     void *dX;                           // null: not wanted; dres has its type
     float *part;                        // null: no weight gradient
-    int64_t M, n, lddy, ldx, ld_dres, lddx, row_groups;
+    int64_t M, n, lddy, ldx, ld_dres, lddx;
+    int64_t row_groups; // set by the launcher
     float eps;
     int32_t dy_bf16, x_bf16, w_bf16, dx_bf16;
 };
 // vec: every base is 16-byte aligned and every row stride whole 16 bytes
 // (e4m3: 8 bytes)
 hipError_t launch_norm(const NormArgs &a, bool vec, hipStream_t stream);
-// row groups of a backward launch: its partial weight gradients take
-// row groups x (n rounded up to 8) binary32
-int64_t norm_grad_groups(int64_t M, int64_t n);
+// partial weight gradients of a backward launch: rows of n rounded up to 8
+// binary32
+int64_t norm_grad_partials(int64_t M, int64_t n);
 hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accumulate,
                             hipStream_t stream);
 

@@ -214,70 +214,166 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(NormArgs a)
 }
 
 // ---- backward ----------------------------------------------------------------
-// Row groups walk the rows with the grid's stride; each thread keeps the
-// weight gradient of its own columns over its rows and leaves it in the
-// workspace, [row groups][n rounded up to 8], which column_sum_kernel adds in
-// order.
-template <int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGradArgs a) {
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    __shared__ float red[TPR / 64];
-    const int t = threadIdx.x % TPR;
-    const int64_t g = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; // row group
-    if (g >= a.row_groups)
-        return; // whole waves only (RPB > 1), before any barrier of wider rows
-    const int64_t n = a.n;
-    f32x8 w[NV], dw[NV];
+// Row groups (a wave up to 512 columns, else a workgroup) walk the rows with
+// the grid's stride; each thread keeps the weight gradient of its own columns
+// over its rows.  A workgroup leaves one partial row in the workspace (of its
+// four waves' sums, added in order, where a row is a wave), which
+// column_sum_kernel adds in order.  Aligned bf16 rows (RAW) are loaded one
+// row ahead, as they lie: a row's loads are in flight over the reduction of
+// the row before (8192 x 4096, 268 MB: 110 -> 61 us with
+// the sums, 4.4 TB/s).
+
+// The runs of 8 of a row, still in bf16.
+template <int NV>
+struct RawRow {
+    u32x4 v[NV];
+};
+template <int TPR, int NV>
+__device__ __forceinline__ void raw_load(RawRow<NV> &r, const void *row, int t, int64_t n) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        w[v] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        if (a.weight)
-            w[v] = load8<VEC>(a.weight, a.w_bf16, ((int64_t)v * TPR + t) * 8, n);
+        const int64_t col = ((int64_t)v * TPR + t) * 8;
+        const uint16_t *p = static_cast<const uint16_t *>(row) + col;
+        u32x4 w = {0, 0, 0, 0};
+        if (col + 8 <= n) {
+            w = *reinterpret_cast<const u32x4 *>(p);
+        } else if (col < n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t l0 = col + 2 * e < n ? p[2 * e] : 0u;
+                const uint32_t h0 = col + 2 * e + 1 < n ? p[2 * e + 1] : 0u;
+                w[e] = l0 | (h0 << 16);
+            }
+        }
+        r.v[v] = w;
+    }
+}
+__device__ __forceinline__ f32x8 widen(u32x4 w) {
+    f32x8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+    return v;
+}
+
+template <int TPR, int NV, bool VEC, bool RAW>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGradArgs a) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr int NW = TPR / 64;
+    __shared__ float red[2][2][NW];
+    __shared__ float join[RPB > 1 ? RPB * 512 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t g = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; // row group
+    const int64_t n = a.n;
+    // The weight stays in registers except at the widest rows, which read it
+    // again (from the cache) where they use it, and dres late, so that 1024
+    // threads' registers hold the row.
+    constexpr bool WIDE = TPR > 512;
+    f32x8 w[WIDE ? 1 : NV], dw[NV];
+    auto weight = [&](int v) __attribute__((always_inline)) {
+        if constexpr (WIDE) {
+            if (!a.weight)
+                return f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            return load8<VEC>(a.weight, a.w_bf16, ((int64_t)v * TPR + t) * 8, n);
+        } else {
+            return w[v];
+        }
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if constexpr (!WIDE) {
+            w[v] = f32x8{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            if (a.weight)
+                w[v] = load8<VEC>(a.weight, a.w_bf16, ((int64_t)v * TPR + t) * 8, n);
+        }
         dw[v] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     }
-    for (int64_t m = g; m < a.M; m += a.row_groups) {
-        const char *xp = static_cast<const char *>(a.X) + m * a.ldx * (a.x_bf16 ? 2 : 4);
-        const char *yp = static_cast<const char *>(a.dY) + m * a.lddy * (a.dy_bf16 ? 2 : 4);
-        f32x8 x[NV], dy[NV], dr[NV];
+    RawRow<RAW ? NV : 1> rx, ry, rr; // the next row, RAW only
+    auto fetch = [&](int64_t m) __attribute__((always_inline)) {
+        if constexpr (RAW) {
+            raw_load<TPR, NV>(rx, static_cast<const uint16_t *>(a.X) + m * a.ldx, t, n);
+            raw_load<TPR, NV>(ry, static_cast<const uint16_t *>(a.dY) + m * a.lddy, t, n);
+            if (a.dres)
+                raw_load<TPR, NV>(rr, static_cast<const uint16_t *>(a.dres) + m * a.ld_dres, t, n);
+        }
+    };
+    int odd = 0;
+    if (g < a.M && g < a.row_groups)
+        fetch(g);
+    for (int64_t m = g; m < a.M && g < a.row_groups; m += a.row_groups, odd ^= 1) {
+        f32x8 x[NV], dy[NV], dr[WIDE ? 1 : NV];
+        const char *rp = static_cast<const char *>(a.dres) + m * a.ld_dres * (a.dx_bf16 ? 2 : 4);
+        if constexpr (RAW) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                x[v] = widen(rx.v[v]);
+                dy[v] = widen(ry.v[v]);
+                if (a.dres)
+                    dr[WIDE ? 0 : v] = widen(rr.v[v]);
+            }
+            if (m + a.row_groups < a.M)
+                fetch(m + a.row_groups);
+        } else {
+            const char *xp = static_cast<const char *>(a.X) + m * a.ldx * (a.x_bf16 ? 2 : 4);
+            const char *yp = static_cast<const char *>(a.dY) + m * a.lddy * (a.dy_bf16 ? 2 : 4);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                x[v] = load8<VEC>(xp, a.x_bf16, ((int64_t)v * TPR + t) * 8, n);
+                dy[v] = load8<VEC>(yp, a.dy_bf16, ((int64_t)v * TPR + t) * 8, n);
+            }
+            if (!WIDE && a.dres) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    dr[WIDE ? 0 : v] = load8<VEC>(rp, a.dx_bf16, ((int64_t)v * TPR + t) * 8, n);
+            }
+        }
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            x[v] = load8<VEC>(xp, a.x_bf16, ((int64_t)v * TPR + t) * 8, n);
-            dy[v] = load8<VEC>(yp, a.dy_bf16, ((int64_t)v * TPR + t) * 8, n);
-        }
-        if (a.dres) {
-            const char *rp = static_cast<const char *>(a.dres) + m * a.ld_dres * (a.dx_bf16 ? 2 : 4);
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                dr[v] = load8<VEC>(rp, a.dx_bf16, ((int64_t)v * TPR + t) * 8, n);
-        }
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
+            const f32x8 wv = weight(v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s1 = __builtin_fmaf(x[v][i], x[v][i], s1);
-                s2 = __builtin_fmaf(dy[v][i] * w[v][i], x[v][i], s2);
+                s2 = __builtin_fmaf(dy[v][i] * wv[i], x[v][i], s2);
             }
-        float rstd;
-        if (a.rstd) {
-            rstd = a.rstd[m];
-        } else {
-            s1 = row_sum<TPR>(s1, red);
-            rstd = 1.f / __builtin_sqrtf(s1 / (float)n + a.eps);
         }
-        s2 = row_sum<TPR>(s2, red);
+        // both sums over the row, in one exchange (rows take turns at two
+        // buffers, so that one barrier a row is enough)
+        s2 = wave_sum(s2);
+        if (!a.rstd)
+            s1 = wave_sum(s1);
+        if constexpr (NW > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                red[odd][0][threadIdx.x >> 6] = s1;
+                red[odd][1][threadIdx.x >> 6] = s2;
+            }
+            __syncthreads();
+            s1 = red[odd][0][0];
+            s2 = red[odd][1][0];
+#pragma unroll
+            for (int q = 1; q < NW; ++q) {
+                s1 += red[odd][0][q];
+                s2 += red[odd][1][q];
+            }
+        }
+        const float rstd = a.rstd ? a.rstd[m] : 1.f / __builtin_sqrtf(s1 / (float)n + a.eps);
         const float c = s2 * rstd / (float)n; // mean of t xh
         char *op = a.dX ? static_cast<char *>(a.dX) + m * a.lddx * (a.dx_bf16 ? 2 : 4) : nullptr;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             f32x8 o;
+            const f32x8 wv = weight(v);
+            if (WIDE && a.dres)
+                dr[0] = load8<VEC>(rp, a.dx_bf16, ((int64_t)v * TPR + t) * 8, n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float xh = x[v][i] * rstd;
-                o[i] = rstd * (dy[v][i] * w[v][i] - xh * c);
+                o[i] = rstd * (dy[v][i] * wv[i] - xh * c);
                 dw[v][i] = __builtin_fmaf(dy[v][i], xh, dw[v][i]);
                 if (a.dres)
-                    o[i] += dr[v][i];
+                    o[i] += dr[WIDE ? 0 : v][i];
             }
             if (op)
                 store8<VEC>(op, a.dx_bf16, ((int64_t)v * TPR + t) * 8, n, o);
@@ -285,13 +381,30 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGr
     }
     if (!a.part)
         return;
+    float *const out = a.part + (int64_t)blockIdx.x * ((n + 7) / 8 * 8);
+    if constexpr (RPB > 1) { // the waves' sums in order (a wave without rows has zeros)
+        const int q = threadIdx.x / TPR;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-        store8<true>(a.part + g * ((n + 7) / 8 * 8), false, ((int64_t)v * TPR + t) * 8, n, dw[v]);
+        for (int i = 0; i < 8; ++i)
+            join[q * 512 + t * 8 + i] = dw[0][i];
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += 256) {
+            float s = join[j];
+#pragma unroll
+            for (int k = 1; k < RPB; ++k)
+                s += join[k * 512 + j];
+            out[j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            store8<true>(out, false, ((int64_t)v * TPR + t) * 8, n, dw[v]);
+    }
 }
 
-// dW[j] (+)= sum over the row groups' partials, 16 columns per workgroup:
-// 16 threads per column take every 16th partial, then add up in order.
+// out[j] (+)= sum over the partial rows, 16 columns per workgroup: 16 threads
+// per column take every 16th partial (eight loads in flight), then add up in
+// order.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict__ part, int64_t groups,
                                                       int64_t n, float *__restrict__ dW,
                                                       int accumulate) {
@@ -300,9 +413,20 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict
     const int64_t j = (int64_t)blockIdx.x * 16 + c;
     const int64_t ld = (n + 7) / 8 * 8;
     float s = 0.f;
-    if (j < n)
-        for (int64_t g = q; g < groups; g += 16)
+    if (j < n) {
+        int64_t g = q;
+        for (; g + 7 * 16 < groups; g += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = part[(g + 16 * i) * ld + j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s += v[i];
+        }
+        for (; g < groups; g += 16)
             s += part[g * ld + j];
+    }
     red[q][c] = s;
     __syncthreads();
     if (q != 0 || j >= n)
@@ -316,6 +440,10 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict
 // (threads per row, runs of 8 per thread) for a width
 #define TSL_NORM_SHAPES(X)                                                                         \
     X(64, 1, 512) X(256, 1, 2048) X(256, 2, 4096) X(256, 4, 8192) X(1024, 2, 16384) X(1024, 4, 32768)
+
+// ... of the backward pass, whose rows hold three operands at once
+#define TSL_NORM_GRAD_SHAPES(X)                                                                    \
+    X(64, 1, 512) X(256, 1, 2048) X(256, 2, 4096) X(512, 2, 8192) X(1024, 2, 16384) X(1024, 4, 32768)
 
 inline int rows_per_group(int64_t n) { return n <= 512 ? 4 : 1; }
 
@@ -338,11 +466,19 @@ hipError_t launch_norm(const NormArgs &a, bool vec, hipStream_t stream) {
     return hipErrorInvalidValue;
 }
 
-// Row groups of a backward launch: enough workgroups to fill the chip, few
-// enough that their weight-gradient partials stay small beside the rows.
-int64_t norm_grad_groups(int64_t M, int64_t n) {
-    const int64_t most = (n <= 4096 ? 1024 : 512) * rows_per_group(n);
-    return M < most ? M : most;
+// Row groups of a backward launch: enough workgroups to fill the chip, and at
+// least four rows each once there are 256 workgroups, so that their partial
+// weight gradients stay small beside the rows.
+static int64_t grad_row_groups(int64_t M, int64_t n) {
+    const int64_t rpb = rows_per_group(n), most = (n <= 4096 ? 1024 : 512) * rpb;
+    const int64_t want = (M + 3) / 4 > 256 * rpb ? (M + 3) / 4 : 256 * rpb;
+    const int64_t groups = want < most ? want : most;
+    return M < groups ? M : groups;
+}
+
+int64_t norm_grad_partials(int64_t M, int64_t n) {
+    const int64_t rpb = rows_per_group(n);
+    return (grad_row_groups(M, n) + rpb - 1) / rpb;
 }
 
 hipError_t launch_column_sum(const float *part, int64_t groups, int64_t n, float *out,
@@ -352,30 +488,37 @@ hipError_t launch_column_sum(const float *part, int64_t groups, int64_t n, float
     return hipGetLastError();
 }
 
-hipError_t launch_norm_grad(const NormGradArgs &a, bool vec, float *dW, int accumulate,
+hipError_t launch_norm_grad(const NormGradArgs &args, bool vec, float *dW, int accumulate,
                             hipStream_t stream) {
+    NormGradArgs a = args;
+    a.row_groups = grad_row_groups(a.M, a.n);
+    const int64_t parts = norm_grad_partials(a.M, a.n);
+    const bool raw = vec && a.x_bf16 && a.dy_bf16 && a.dx_bf16;
     if (a.M > 0) {
-        const int64_t rpb = rows_per_group(a.n);
-        const dim3 grid((unsigned)((a.row_groups + rpb - 1) / rpb));
+        const dim3 grid((unsigned)parts);
         hipError_t e = hipErrorInvalidValue;
 #define TSL_CASE(TPR_, NV_, MAX_)                                                                  \
     if (e == hipErrorInvalidValue && a.n <= MAX_) {                                                \
         const dim3 block(TPR_ < 256 ? 256 : TPR_);                                                 \
-        if (vec)                                                                                   \
-            hipLaunchKernelGGL((norm_grad_kernel<TPR_, NV_, true>), grid, block, 0, stream, a);    \
+        if (raw && TPR_ <= 512)                                                                    \
+            hipLaunchKernelGGL((norm_grad_kernel<TPR_, NV_, true, (TPR_ <= 512)>), grid, block, 0, \
+                               stream, a);                                                         \
+        else if (vec)                                                                              \
+            hipLaunchKernelGGL((norm_grad_kernel<TPR_, NV_, true, false>), grid, block, 0, stream, \
+                               a);                                                                 \
         else                                                                                       \
-            hipLaunchKernelGGL((norm_grad_kernel<TPR_, NV_, false>), grid, block, 0, stream, a);   \
+            hipLaunchKernelGGL((norm_grad_kernel<TPR_, NV_, false, false>), grid, block, 0,        \
+                               stream, a);                                                         \
         e = hipGetLastError();                                                                     \
         if (e != hipSuccess)                                                                       \
             return e;                                                                              \
     }
-        TSL_NORM_SHAPES(TSL_CASE)
+        TSL_NORM_GRAD_SHAPES(TSL_CASE)
 #undef TSL_CASE
         if (e != hipSuccess)
             return e;
     }
-    return dW ? launch_column_sum(a.part, a.M > 0 ? a.row_groups : 0, a.n, dW, accumulate, stream)
-              : hipSuccess;
+    return dW ? launch_column_sum(a.part, parts, a.n, dW, accumulate, stream) : hipSuccess;
 }
 
 } // namespace tsl
