@@ -336,6 +336,50 @@ inline size_t split_sets(std::vector<LinearItem> *items, char *ws) {
     return off;
 }
 
+// The last columns of a lone product as a piece of its own where the GEMM
+// plan wants that (prefill.hip, tail_choice): *items becomes the two pieces.
+// eps receives the second's epilogue, which the caller keeps until the launch.
+inline void split_tail(std::vector<LinearItem> *items, tsl_dtype wdtype, int64_t M, Epilogue *ep) {
+    if constexpr (kEpilogue) {
+        if (items->size() != 1 || use_skinny(wdtype, M))
+            return;
+        const int64_t n0 = tail_columns((*items)[0], wdtype);
+        if (n0 == 0)
+            return;
+        LinearItem a = (*items)[0], b = a;
+        const size_t ye = a.ydtype == TSL_F32 ? 4 : 2;
+        auto past = [](auto *p, int64_t bytes) {
+            typedef decltype(p) P;
+            return p ? reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p) + bytes) : p;
+        };
+        a.g.Ns = n0;
+        b.g.Ns -= n0;
+        b.tail = true;
+        b.Y = past(b.Y, n0 * ye);
+        const int64_t bytes = n0 / 16 * (a.g.KT / a.cat) * 1024; // of the columns before
+        if (wdtype == TSL_Q4G64) {
+            b.tile_off = n0 / 16; // the column exponents lie behind all the records
+        } else {
+            a.g.Nt = n0 / 16;
+            b.g.Nt -= n0 / 16;
+            b.packed = past(b.packed, bytes);
+            for (int r = 0; r < b.cat; ++r)
+                b.seg_packed[r] = past(b.seg_packed[r], bytes);
+        }
+        if (b.ep) {
+            *ep = *b.ep;
+            ep->bias = past(ep->bias, n0 * (ep->flags & kEpBiasBf16 ? 2 : 4));
+            ep->res = past(ep->res, n0 * (ep->flags & kEpResBf16 ? 2 : 4));
+            ep->pre = past(ep->pre, n0 * (ep->flags & kEpPreBf16 ? 2 : 4));
+            ep->pre2 = past(ep->pre2, n0 * (ep->flags & kEpPreBf16 ? 2 : 4));
+            if (wdtype != TSL_Q4G64)
+                ep->up = past(ep->up, bytes);
+            b.ep = ep;
+        }
+        items->assign({a, b});
+    }
+}
+
 // Rows read through an index.  The 4-bit activation pass (GEMM regime) and
 // the resident streaming kernel (a few decode rows, bf16 and 4-bit
 // weights) read them where they lie; the other kernels read X rows at
@@ -393,6 +437,8 @@ inline size_t group_workspace(const std::vector<LinearItem> &in, tsl_dtype wdtyp
     std::vector<RowGather> jobs;
     const size_t gathered = plan_row_gathers(&src, wdtype, M, nullptr, &jobs);
     std::vector<LinearItem> items = launch_order(concat_sets(src, wdtype, M));
+    Epilogue tail_ep;
+    split_tail(&items, wdtype, M, &tail_ep);
     const size_t parts = split_sets(&items, nullptr);
     if (use_skinny(wdtype, M))
         return gathered + parts + skinny_plan(items.data(), (int)items.size(), wdtype, M).ws_bytes;
@@ -414,7 +460,9 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
     std::vector<RowGather> gathers;
     const size_t gathered = plan_row_gathers(&src, wdtype, M, ws0, &gathers);
     char *ws = ws0 ? ws0 + gathered : nullptr; // the rank partials, then the plan's
-    const std::vector<LinearItem> ordered = launch_order(concat_sets(src, wdtype, M));
+    std::vector<LinearItem> ordered = launch_order(concat_sets(src, wdtype, M));
+    Epilogue tail_ep;
+    split_tail(&ordered, wdtype, M, &tail_ep);
     std::vector<LinearItem> items = ordered;
     const size_t parts = split_sets(&items, ws);
     const int n = (int)items.size();

@@ -227,6 +227,10 @@ struct LinearItem {
     // both results (ep->up: the second packed weight, of the same geometry)
     const Epilogue *ep = nullptr;
     const Epilogue *fset_ep = nullptr; // of the sum set it is a member of
+    // the second of a lone product's two pieces (its activations are the
+    // first's), and the first 16-column tile of a piece of 4-bit weights
+    bool tail = false;
+    int64_t tile_off = 0;
     // member fset_pos of a sum set of fset_len products that split_sets
     // turned into lone items (0: none), and the set's own output
     int fset_len = 0, fset_pos = 0;
@@ -362,6 +366,9 @@ struct PrefillPlan {
     size_t ws_bytes = 0;
 };
 bool prefill_supported(tsl_dtype wdtype);
+// First column of the piece that a lone product's last columns run as (0: it
+// runs whole); libtsl_block.so only.
+int64_t tail_columns(const LinearItem &L, tsl_dtype wdtype);
 PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t M);
 // most workgroups any one launch of the group takes (bounded by the host)
 int64_t prefill_blocks(const PrefillPlan &p, const LinearItem *items, int n, int64_t M);

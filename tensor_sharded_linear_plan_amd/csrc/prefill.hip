@@ -797,13 +797,8 @@ double chunk_cost(const Variant &v, double pen, const LinearItem *items, int c0,
 // tiles otherwise ends with most CUs idle.
 constexpr int64_t kSplitSearchBelow = 1024;
 
-// Modelled cost of a variant over a group, each launch (kPrefillGroupMax items;
-// every launch drains before the next starts) with its k-splits, which
-// *ks receives per item: a launch of fewer than kSplitBelow tiles splits
-// its long products toward one tile per CU; a launch of fewer than
-// kSplitSearchBelow tiles takes the modelled best factor.
-double variant_cost(const Variant &v, const LinearItem *items, int n, std::vector<int> *ks,
-                    bool q4) {
+// A variant's per-CU penalty relative to the MFMAs' own time.
+double variant_penalty(const Variant &v, bool q4) {
     const double TM = v.bm / v.wm, TN = v.bn / v.wn;
     const double flops = 2.0 * v.bm * v.bn; // per k
     double pen;
@@ -828,6 +823,17 @@ double variant_cost(const Variant &v, const LinearItem *items, int n, std::vecto
         pen += 120.0 / ((v.bm / 32) * (v.bn / 4 / 32) * 32.0) / (waves > 1 ? 2.0 : 1.0);
     }
     pen = pen > 1.0 ? pen : 1.0;
+    return pen;
+}
+
+// Modelled cost of a variant over a group, each launch (kPrefillGroupMax items;
+// every launch drains before the next starts) with its k-splits, which
+// *ks receives per item: a launch of fewer than kSplitBelow tiles splits
+// its long products toward one tile per CU; a launch of fewer than
+// kSplitSearchBelow tiles takes the modelled best factor.
+double variant_cost(const Variant &v, const LinearItem *items, int n, std::vector<int> *ks,
+                    bool q4) {
+    const double pen = variant_penalty(v, q4);
     double total = 0.0;
     ks->assign(n, 1);
     for (int c0 = 0; c0 < n;) {
@@ -875,6 +881,7 @@ double variant_cost(const Variant &v, const LinearItem *items, int n, std::vecto
 struct PlanChoice {
     Variant v;
     std::vector<int> ks;
+    int64_t n_main = 0; // > 0: a lone product in two pieces, ks[0] and ks[1] (tail_columns)
 };
 std::mutex g_plan_mu;
 std::unordered_map<std::string, PlanChoice> g_plans;
@@ -902,9 +909,54 @@ std::string plan_key(const LinearItem *items, int n, tsl_dtype wdtype) {
 
 bool prefill_supported(tsl_dtype wdtype) { return wdtype == TSL_BF16 || wdtype == TSL_Q4G64; }
 
-PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t M) {
-    (void)M;
-    PrefillPlan best;
+namespace {
+
+// A lone product of somewhat more tiles than whole rounds over the chip (272
+// of 256 x 256 over 256 CUs, say) leaves most CUs idle through its last
+// round.  Its last column tiles may instead run along k in pieces of that
+// round: the columns [n_main, Ns) split ks[1] ways, the rest unsplit, in one
+// launch.  Kept when the model finds it shorter than *best; 10000 clocks
+// stand for the launch that adds the pieces.  Only in tiles no smaller than
+// the whole product's: the model flatters small tiles over long k (2048 x
+// 17408 -> 5120, 4-bit: 409 us in 256 x 256 tiles split 3 ways along k, 480
+// in 128 x 256 tiles with a tail).  Measured, 2048 x 5120 -> 2 x 4352 4-bit:
+// 269 us whole in 128 x 256 tiles (3 rounds of 544), 201 us as 256 tiles of
+// 256 x 256 and 16 split 8 ways.
+void tail_choice(const LinearItem &L, const Variant *vs, int nv, bool q4, double best_cost,
+                 PlanChoice *best) {
+    if (L.accumulate || L.no_split || L.set_len != 1)
+        return;
+    const int64_t stages = kpad64(L.g.Ks) / 64, per_col = dual(L) ? 2 : 1;
+    const int least = best->v.bm * best->v.bn;
+    for (int vi = 0; vi < nv; ++vi) {
+        const Variant &v = vs[vi];
+        const int per_cu = q4 ? q4_per_cu(v) : 1;
+        const int64_t slots = 256 * per_cu, mb = (L.M + v.bm - 1) / v.bm;
+        const int64_t nb = (result_columns(L) + v.bn - 1) / v.bn, rem = mb * nb % slots;
+        if (v.bm * v.bn < least || mb * nb < slots || mb * nb > 16 * slots || rem == 0)
+            continue;
+        const int64_t ct = (rem + mb - 1) / mb; // column tiles of the tail
+        int64_t ks = slots / (ct * mb);
+        ks = ks < stages / 8 ? ks : stages / 8;
+        ks = ks < 8 ? ks : 8;
+        if (ct >= nb || ks < 2)
+            continue;
+        LinearItem two[2] = {L, L};
+        const int64_t n_main = (nb - ct) * v.bn / per_col;
+        two[0].g.Ns = n_main;
+        two[1].g.Ns = L.g.Ns - n_main;
+        const int kk[2] = {1, (int)ks};
+        const double cost = chunk_cost(v, variant_penalty(v, q4), two, 0, 2, kk, per_cu) + 32.0e4;
+        if (cost < best_cost * 0.97) {
+            best_cost = cost;
+            best->v = v;
+            best->ks.assign(kk, kk + 2);
+            best->n_main = n_main;
+        }
+    }
+}
+
+PlanChoice choose_plan(const LinearItem *items, int n, tsl_dtype wdtype) {
     const bool q4 = wdtype == TSL_Q4G64;
     const std::string key = plan_key(items, n, wdtype);
     PlanChoice choice;
@@ -936,10 +988,32 @@ PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64
                 choice.ks = ks;
             }
         }
+        if (kEpilogue && n == 1)
+            tail_choice(items[0], vs, nv, q4, best_cost, &choice);
         std::lock_guard<std::mutex> lock(g_plan_mu);
         if (g_plans.size() >= kPlanCacheMax)
             g_plans.clear();
         g_plans.emplace(key, choice);
+    }
+    return choice;
+}
+
+} // namespace
+
+int64_t tail_columns(const LinearItem &L, tsl_dtype wdtype) {
+    return choose_plan(&L, 1, wdtype).n_main;
+}
+
+PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64_t M) {
+    (void)M;
+    PrefillPlan best;
+    PlanChoice choice;
+    if (n == 2 && items[1].tail) { // the two pieces of a lone product
+        LinearItem whole = items[0];
+        whole.g.Ns += items[1].g.Ns;
+        choice = choose_plan(&whole, 1, wdtype);
+    } else {
+        choice = choose_plan(items, n, wdtype);
     }
     best.bm = choice.v.bm;
     best.bn = choice.v.bn;
@@ -962,6 +1036,8 @@ PrefillPlan prefill_plan(const LinearItem *items, int n, tsl_dtype wdtype, int64
         const bool q4 = wdtype == TSL_Q4G64;
         if (q4 || g.Ks % 64 != 0) {
             int first = i;
+            if (items[i].tail)
+                first = best.x_first[i - 1];
             for (int j = 0; j < i && items[i].X; ++j)
                 if (items[j].X == items[i].X && items[j].ldx == items[i].ldx &&
                     items[j].ridx == items[i].ridx && items[j].x_rows == items[i].x_rows &&

@@ -59,7 +59,7 @@ struct Q4Item {
     int32_t KBm;       // 128-k records per column tile of one member
     int32_t nst;       // 32-k activation stages of the whole k-range
     int32_t MB, NB;    // tile grid
-    int32_t pad0_, start; // first workgroup
+    int32_t t_off, start; // first 16-column tile in the records; first workgroup
     int32_t flags, ks; // flags: bit 0 bf16 output, bit 1 accumulate, bit 2 an epilogue
     int32_t seg, R;    // joined sum set: member table row (-1: none) and member count
 };
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
     if (threadIdx.x < kSetParts)
         mtab[threadIdx.x] = a.R > 1 ? grp.segw[a.seg][threadIdx.x < a.R ? threadIdx.x : 0] : a.W;
     __syncthreads();
-    const int t0 = (int)(n0 >> 4);
+    const int t0 = (int)(n0 >> 4) + (kEpilogue ? a.t_off : 0);
     // where block b's records start: the member holding global block
     // blk0 + b and the block's index within it
     auto block_src = [&](int b, int &lb) __attribute__((always_inline)) {
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(64 * WM * WN)
 #pragma unroll
         for (int j = 0; j < C::NT; ++j) {
             int64_t n = n0 + (DUAL ? C::TN / 2 * wn + 32 * (j >> 1) : C::TN * wn + 32 * j) + (lane & 31);
+            n += kEpilogue ? (int64_t)a.t_off * 16 : 0;
             n = n < (int64_t)a.Nt16 * 16 ? n : (int64_t)a.Nt16 * 16 - 1;
             int f = -1000;
             for (int r = 0; r < a.R; ++r) {
@@ -665,6 +666,7 @@ hipError_t launch_q4_gemm(const PrefillPlan &p, const LinearItem *items, int n, 
             a.M = (int32_t)L.M;
             a.Ns = (int32_t)g.Ns;
             a.Nt16 = (int32_t)g.Nt;
+            a.t_off = (int32_t)L.tile_off;
             a.KBm = (int32_t)(g.KT / L.cat);
             a.nst = (int32_t)(g.Ks / 32);
             a.MB = (int32_t)((L.M + p.bm - 1) / p.bm);
