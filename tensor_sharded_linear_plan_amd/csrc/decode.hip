@@ -1,4 +1,4 @@
-// Products of a few token rows (up to 16) with an epilogue, in one launch:
+// Products of a few token rows (up to 64) with an epilogue, in one launch:
 // one rank's Y = act(X W + bias) + residual, a sum set of row shards, or a
 // gated pair act(X W_0) * (X W_1) (mlxcel manual "Tensor parallelism",
 // "Column Parallel" / "Row Parallel").
@@ -11,8 +11,9 @@
 // a sum set's members laid end to end in item order -- which meet in LDS, are
 // added in wave order (so in k order) and go through the epilogue in
 // registers.  Nothing returns to memory but the result; no workspace, no
-// atomics, the same bits every time.  W is 16 for up to 256 tiles, 8 up to
-// 512, else 4: about 4096 waves fill the chip's 1024 SIMDs fourfold.
+// atomics, the same bits every time.  W is 16 for up to 256 tiles (and 16
+// rows: more need the registers of 8 waves), 8 up to 512, else 4: about 4096
+// waves fill the chip's 1024 SIMDs fourfold.
 //
 // A wave reads its weights as the streaming kernel does (contiguous 1 KB wave
 // loads in MFMA operand order, 4-bit groups applied exactly: skinny.hip),
@@ -63,11 +64,12 @@ template <bool Q4> struct Unit {
     static constexpr int FR = K / 32;                  // activation fragments
 };
 
-template <bool Q4, bool DUAL>
-__global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
+// MT 16-row tiles; more than one needs the registers of 8 waves.
+template <bool Q4, bool DUAL, int MT>
+__global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp) {
     using C = Unit<Q4>;
     constexpr int NT = DUAL ? 2 : 1;
-    extern __shared__ __attribute__((aligned(16))) f32x4 red[]; // [waves][NT][64]
+    extern __shared__ __attribute__((aligned(16))) f32x4 red[]; // [waves][MT][NT][64]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int W = blockDim.x >> 6;
@@ -92,8 +94,8 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
     // index lies outside X reads row 0 and is masked to zeros.
     int r = a.first, lu = u0;
     const char *wp[NT];
-    const uint16_t *xp = nullptr; // this lane's row and k-run
-    uint32_t keep = ~0u;
+    const uint16_t *xp[MT]; // this lane's rows and k-run
+    uint32_t keep[MT];
     bool masked = false; // some row of the wave may be (uniform)
     int Ks = 0;
     auto enter = [&]() __attribute__((always_inline)) {
@@ -102,20 +104,24 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
         wp[0] = b.B + tile * b.KC * C::CS;
         if constexpr (DUAL)
             wp[1] = wp[0] + up;
-        int64_t s = row < a.M ? row : 0;
         masked = b.ridx != nullptr;
-        if (masked) {
-            s = b.ridx[s];
-            const bool ok = s >= 0 && s < b.x_rows;
-            keep = ok ? ~0u : 0u;
-            s = ok ? s : 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            int64_t s = 16 * i + row < a.M ? 16 * i + row : 0;
+            keep[i] = ~0u;
+            if (masked) {
+                s = b.ridx[s];
+                const bool ok = s >= 0 && s < b.x_rows;
+                keep[i] = ok ? ~0u : 0u;
+                s = ok ? s : 0;
+            }
+            xp[i] = b.X + s * b.ldx + 8 * kg;
         }
-        xp = b.X + s * b.ldx + 8 * kg;
     };
     struct Regs {
         u32x4 w[NT][C::CHUNKS];
         u32x2 sb[NT];
-        u32x4 x[C::FR];
+        u32x4 x[MT][C::FR];
     };
     auto load = [&](Regs &g) __attribute__((always_inline)) {
 #pragma unroll
@@ -129,63 +135,78 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
         }
         // 4-bit k-ranges are whole 64-k groups and bf16 units 64 k, so that
         // every condition here is uniform but in a ragged last bf16 unit
-        const uint16_t *x = xp + lu * C::K;
         const int left = Ks - lu * C::K;
-        if (left >= C::K) {
 #pragma unroll
-            for (int f = 0; f < C::FR; ++f)
-                g.x[f] = *reinterpret_cast<const u32x4 *>(x + 32 * f);
-        } else {
+        for (int i = 0; i < MT; ++i) {
+            const uint16_t *x = xp[i] + lu * C::K;
+            if (left >= C::K) {
 #pragma unroll
-            for (int f = 0; f < C::FR; ++f) {
-                const int k = 32 * f + 8 * kg;
-                u32x4 v = {0, 0, 0, 0};
-                if (k + 8 <= left) {
-                    v = *reinterpret_cast<const u32x4 *>(x + 32 * f);
-                } else if (k < left) {
+                for (int f = 0; f < C::FR; ++f)
+                    g.x[i][f] = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t l0 = k + 2 * e < left ? x[32 * f + 2 * e] : 0u;
-                        const uint32_t h0 = k + 2 * e + 1 < left ? x[32 * f + 2 * e + 1] : 0u;
-                        v[e] = l0 | (h0 << 16);
+                for (int f = 0; f < C::FR; ++f) {
+                    const int k = 32 * f + 8 * kg;
+                    u32x4 v = {0, 0, 0, 0};
+                    if (k + 8 <= left) {
+                        v = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+                    } else if (k < left) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t l0 = k + 2 * e < left ? x[32 * f + 2 * e] : 0u;
+                            const uint32_t h0 = k + 2 * e + 1 < left ? x[32 * f + 2 * e + 1] : 0u;
+                            v[e] = l0 | (h0 << 16);
+                        }
                     }
+                    g.x[i][f] = v;
                 }
-                g.x[f] = v;
             }
-        }
-        if (masked) {
+            if (masked) {
 #pragma unroll
-            for (int f = 0; f < C::FR; ++f)
+                for (int f = 0; f < C::FR; ++f)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    g.x[f][e] &= keep;
+                    for (int e = 0; e < 4; ++e)
+                        g.x[i][f][e] &= keep[i];
+            }
         }
         ++lu;
     };
-    f32x4 acc[NT];
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const Regs &g) __attribute__((always_inline)) {
         if constexpr (!Q4) {
 #pragma unroll
             for (int f = 0; f < C::FR; ++f)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    acc[j] = mfma_bf16(__builtin_bit_cast(bf16x8, g.x[f]),
-                                       __builtin_bit_cast(bf16x8, g.w[j][f]), acc[j]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        acc[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, g.x[i][f]),
+                                              __builtin_bit_cast(bf16x8, g.w[j][f]), acc[i][j]);
         } else {
             const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u,
                                                                  0x3F803F80u, 0x3F803F80u});
             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            f32x4 xs = zero, ag[NT];
+            f32x4 xs[MT], ag[MT][NT];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const bf16x8 xa = __builtin_bit_cast(bf16x8, g.x[t]);
-                xs = mfma_bf16(xa, ones, (t & 1) ? xs : zero);
+                bf16x8 xa[MT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    ag[j] = mfma_bf16(xa, q4_to_bf16_plus128(g.w[j][0][t]), (t & 1) ? ag[j] : zero);
+                for (int i = 0; i < MT; ++i) {
+                    xa[i] = __builtin_bit_cast(bf16x8, g.x[i][t]);
+                    xs[i] = mfma_bf16(xa[i], ones, (t & 1) ? xs[i] : zero);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const bf16x8 bq = q4_to_bf16_plus128(g.w[j][0][t]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        ag[i][j] = mfma_bf16(xa[i], bq, (t & 1) ? ag[i][j] : zero);
+                }
                 if (t & 1) { // end of a group: y += s sum(x (128 + q)) + (b - 128 s) sum(x)
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -193,10 +214,12 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
                         const float sc = bf16_lo(sbp);
                         const float cb = __builtin_fmaf(-128.f, sc, bf16_hi(sbp));
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            acc[j][q] = __builtin_fmaf(sc, ag[j][q], acc[j][q]);
-                            acc[j][q] = __builtin_fmaf(cb, xs[q], acc[j][q]);
-                        }
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                acc[i][j][q] = __builtin_fmaf(sc, ag[i][j][q], acc[i][j][q]);
+                                acc[i][j][q] = __builtin_fmaf(cb, xs[i][q], acc[i][j][q]);
+                            }
                     }
                 }
             }
@@ -218,7 +241,7 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
         };
         Regs g0, g1;
         load(g0);
-        if constexpr (DUAL) { // a second unit's registers would spill
+        if constexpr (MT == 1 ? DUAL : Q4 && MT * NT > 2) { // a second unit's registers would spill
             for (int u = u0 + 1; u < u1; ++u) {
                 compute(g0);
                 next(g0);
@@ -244,42 +267,66 @@ __global__ void __launch_bounds__(1024) decode_kernel(Group grp) {
         }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        red[(wave * NT + j) * 64 + lane] = acc[j];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            red[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    if (wave != 0)
-        return;
+    // wave i adds up and stores row tile i
+    for (int i = wave; i < MT; i += W) {
+        f32x4 v[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        for (int w = 1; w < W; ++w) {
-            const f32x4 v = red[(w * NT + j) * 64 + lane];
+        for (int j = 0; j < NT; ++j) {
+            v[j] = red[(i * NT + j) * 64 + lane];
+            for (int w = 1; w < W; ++w) {
+                const f32x4 p = red[((w * MT + i) * NT + j) * 64 + lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                acc[j][q] += v[q];
+                for (int q = 0; q < 4; ++q)
+                    v[j][q] += p[q];
+            }
         }
-    // lane holds rows 4 (lane / 16) + q of column lane % 16
-    const int64_t col = tile * 16 + (lane & 15);
-    if (col >= a.Ns)
-        return;
-    const Epilogue e = grp.ep(lo);
+        // lane holds rows 16 i + 4 (lane / 16) + q of column lane % 16
+        const int64_t col = tile * 16 + (lane & 15);
+        if (col >= a.Ns)
+            return;
+        const Epilogue e = grp.ep(lo);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int64_t m = 4 * kg + q;
-        if (m >= a.M)
-            continue;
-        float v;
-        if constexpr (DUAL)
-            v = ep_gate(e, acc[0][q], acc[1][q], m, col);
-        else
-            v = ep_apply(e, acc[0][q], m, col);
-        ep_put(a.Y, a.y_bf16, m * a.ldy + col, v);
+        for (int q = 0; q < 4; ++q) {
+            const int64_t m = 16 * i + 4 * kg + q;
+            if (m >= a.M)
+                continue;
+            float y;
+            if constexpr (DUAL)
+                y = ep_gate(e, v[0][q], v[1][q], m, col);
+            else
+                y = ep_apply(e, v[0][q], m, col);
+            ep_put(a.Y, a.y_bf16, m * a.ldy + col, y);
+        }
     }
 }
 
 typedef void (*DecodeFn)(Group);
 
+template <bool Q4, bool DUAL> DecodeFn pick(int mt) {
+    return mt == 1   ? decode_kernel<Q4, DUAL, 1>
+           : mt == 2 ? decode_kernel<Q4, DUAL, 2>
+           : mt == 3 ? decode_kernel<Q4, DUAL, 3>
+                     : decode_kernel<Q4, DUAL, 4>;
+}
+
 } // namespace
 
+// Each tile's waves read the call's X again (from L2), which the streaming
+// kernel's workgroups share among four or eight tiles, so this form is for
+// calls of few tiles or few rows: with T tiles (of one weight) and M rows,
+// up to 32 rows T M <= 9472 (gated: twice that, for a tile of X serves both
+// weights), and T <= 1200.  Either side of it, K 3584, this form / the other:
+// 4-bit lone T 592: M 16 15.1 / 14.9 us, M 32 25.7 / 22.2; T 1184: M 8 17.1 /
+// 17.8, M 16 22.2 / 18.4; T 2048: M 1 16.5 / 15.3; gated T 1184: M 16 24.2 /
+// 25.7, M 32 39.7 / 36.9; bf16 lone T 592: M 16 16.5 / 17.9, M 32 25.2 / 22.4.
+// From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 / 63, gated 57 /
+// 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles (T 224, K
+// 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 / 15.5).
 bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M) {
     if (wdtype == TSL_F32 || M > kDecodeRows)
         return false;
@@ -292,19 +339,26 @@ bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int6
         if (L.set_len > 0)
             tiles += L.g.Nt;
     }
-    return any && tiles <= kDecodeTiles;
+    if (!any || tiles > 1200)
+        return false;
+    const bool two = dual(items[0]);
+    if (M <= 32)
+        return tiles * M <= (two ? 18944 : 9472);
+    return wdtype == TSL_Q4G64 || (two && tiles * M <= 14336);
 }
 
-hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
+hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M,
                          hipStream_t stream) {
     const bool q4 = wdtype == TSL_Q4G64, two = dual(items[0]);
-    const DecodeFn fn = q4 ? (two ? decode_kernel<true, true> : decode_kernel<true, false>)
-                           : (two ? decode_kernel<false, true> : decode_kernel<false, false>);
+    const int mt = (int)((M + 15) / 16);
+    const DecodeFn fn = q4 ? (two ? pick<true, true>(mt) : pick<true, false>(mt))
+                           : (two ? pick<false, true>(mt) : pick<false, false>(mt));
     int64_t tiles = 0;
     for (const LinearItem &L : items)
         if (L.set_len > 0)
             tiles += L.g.Nt;
-    const int waves = tiles <= 256 ? 16 : (tiles <= 512 ? 8 : 4);
+    const int waves = tiles <= 256 && mt == 1 ? 16 : (tiles <= 512 ? 8 : 4);
+    const size_t lds = (size_t)waves * mt * (two ? 2 : 1) * 64 * 16;
     for (size_t i = 0; i < items.size();) {
         Group grp{};
         int members = 0;
@@ -336,8 +390,7 @@ hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
                 a.units += m.units;
             }
         }
-        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * waves),
-                           (size_t)waves * (two ? 2 : 1) * 64 * 16, stream, grp);
+        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * waves), lds, stream, grp);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;

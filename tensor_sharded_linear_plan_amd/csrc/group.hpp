@@ -452,7 +452,7 @@ inline tsl_status run_group(const std::vector<LinearItem> &in, tsl_dtype wdtype,
         return TSL_OK;
     if constexpr (kEpilogue) {
         if (decode_applies(in, wdtype, M))
-            return from_hip(launch_decode(in, wdtype, static_cast<hipStream_t>(stream)));
+            return from_hip(launch_decode(in, wdtype, M, static_cast<hipStream_t>(stream)));
     }
     // (a null or short workspace is rejected below, before any launch)
     char *const ws0 = static_cast<char *>(workspace);

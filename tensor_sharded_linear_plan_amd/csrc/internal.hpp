@@ -341,12 +341,11 @@ hipError_t launch_skinny(const SkinnyPlan &p, const LinearItem *items, int n, ts
                          int64_t M, void *workspace, hipStream_t stream);
 
 // ---- decode.hip (libtsl_block.so): a few rows with an epilogue, one launch ----
-constexpr int64_t kDecodeRows = 16;    // one 16-row MFMA tile
-constexpr int64_t kDecodeTiles = 2048; // column tiles of a call
+constexpr int64_t kDecodeRows = 64; // rows of a call, at most
 // Whether a call (sets still whole) runs that way; its rows may be read
 // through an index, and it needs no workspace.
 bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M);
-hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
+hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M,
                          hipStream_t stream);
 
 // ---- prefill.hip: 32x32x16 MFMA GEMM, operands copied straight into LDS ----
