@@ -234,7 +234,8 @@ static_assert(sizeof(tsl_gated_item) == 120 && offsetof(tsl_gated_item, hdtype) 
 
 namespace {
 
-// The items of a size query (shards, set links, rows, whether indexed).
+// The items of a size query (shards, set links, rows, accumulation, whether
+// indexed).
 tsl_status sized_items(int32_t n_items, const tsl_linear_item *items, tsl_dtype wdtype, int64_t M,
                        std::vector<LinearItem> *out) {
     out->resize(n_items);
@@ -250,7 +251,10 @@ tsl_status sized_items(int32_t n_items, const tsl_linear_item *items, tsl_dtype 
         L.M = items[i].rows ? items[i].rows : M;
         L.ridx = items[i].row_index;
         L.x_rows = 1;
+        L.accumulate = items[i].accumulate; // of a set's first item
         L.set_pos = i - first;
+        if (L.set_pos > 0)
+            L.accumulate = 0;
         if (!items[i].sum_next || i == n_items - 1) {
             (*out)[first].set_len = i - first + 1;
             for (int32_t r = first + 1; r <= i; ++r)
@@ -796,6 +800,10 @@ tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *s
         }
         j.split = p.split;
         j.part = c.db ? reinterpret_cast<float *>(ws + p.part) : nullptr;
+        if (c.db && p.Mp == 64) { // one partial row: the sums themselves
+            j.part = c.db;
+            j.add = c.accumulate;
+        }
         j.M = M;
         j.N = N;
     }
@@ -815,7 +823,7 @@ tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *s
     if (blocks > kMaxBlocks)
         return TSL_ERR_UNSUPPORTED;
     hipError_t he = launch_grad_rows(jobs, n_jobs, !f32, s);
-    if (he == hipSuccess && c.db)
+    if (he == hipSuccess && c.db && p.Mp > 64)
         he = launch_column_sum(reinterpret_cast<const float *>(ws + p.part), p.Mp / 64, N, c.db,
                                c.accumulate, s);
     if (he != hipSuccess)

@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(GradJobs jobs) {
         const int64_t n = n0 + threadIdx.x;
         if (threadIdx.x < kTile && n < N) {
             const int t = threadIdx.x;
-            g.part[mb * ((N + 7) / 8 * 8) + n] = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
+            float *const p = g.part + mb * ((N + 7) / 8 * 8) + n;
+            const float v = ((red[0][t] + red[1][t]) + red[2][t]) + red[3][t];
+            *p = g.add ? *p + v : v;
         }
     }
     const int64_t Mp = (g.M + 63) / 64 * 64, Mt = g.split ? 2 * Mp : Mp;

@@ -171,8 +171,10 @@ struct GradJob {
     int32_t packed = 0;
     int32_t kind = kGradCopy, act = 0;
     // binary32 column sums of the result, one row per 64 rows of the job
-    // (row stride N rounded up to 8); null: not wanted
+    // (row stride N rounded up to 8); null: not wanted.  add: added to what
+    // is there
     float *part = nullptr;
+    int32_t add = 0;
     int64_t M = 0, N = 0;
     int32_t nblk = 0, start = 0; // set by the launcher
 };

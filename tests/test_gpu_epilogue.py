@@ -260,3 +260,43 @@ def test_captured_and_replayed(wk, M, tp):
         run(items, eps, wk, M)
         t.cuda.synchronize()
     del keep
+
+
+@pytest.mark.parametrize("wk,M,T", [("f32", 4, 3), ("bf16", 5, 9), ("bf16", 20, 50), ("bf16", 70, 40),
+                                    ("q4", 3, 7), ("q4", 30, 9), ("q4", 66, 200)])
+def test_sum_set_read_through_row_indices(wk, M, T):
+    """The members of a set read different rows of different matrices."""
+    t = torch()
+    K, N = 256, 72
+    e, b, r, p, _ = epilogue(M, N, "silu", "f32", "f32", "f32")
+    Y = out(M, N, "f32")[1]
+    items, want = [], f64(b)[None, :]
+    for i in range(2):
+        W = Weight(wk, K, N, 140 + i)
+        x = ints(150 + i, (T, K))
+        idx = rng(160 + i).integers(-1, T + 1, size=M).astype(np.int32)
+        sh = tsl.plan_linear(K, N, 1, tsl.ROW, 64 if wk == "q4" else 0)[0]
+        buf, nb = W.pack(sh)
+        X = put(x, xkind(wk))
+        items.append(dict(shard=sh, packed=buf, packed_bytes=nb, X=X, ldx=X.stride(0), Y=Y,
+                          ldy=Y.stride(0), ydtype=tsl.F32, sum_next=1 - i,
+                          row_index=t.from_numpy(idx).to(DEV), x_rows=T))
+        want = want + np.where(((idx >= 0) & (idx < T))[:, None], x[np.clip(idx, 0, T - 1)], 0) @ W.w
+    run(items, [e, None], wk, M)
+    assert np.array_equal(f64(p), want)
+    v, _, err = act(want, "silu")
+    close(f64(Y), v + f64(r), err + U * np.abs(v + f64(r)), "f32")
+
+
+@pytest.mark.parametrize("wk,M", [("f32", 3), ("bf16", 4), ("bf16", 40), ("q4", 4), ("q4", 70)])
+def test_accumulating_items_beside_epilogues(wk, M):
+    """A plain accumulating product and one with an epilogue in one call, in
+    the workspace the size query asks for."""
+    K, N = 1024, 96
+    W, X, (a,) = problem(wk, M, K, N, seed=171)
+    Y1, Y2 = out(M, N, "f32", fill=2.0)[1], out(M, N, "f32")[1]
+    items = [dict(a, Y=Y1, ldy=Y1.stride(0), ydtype=tsl.F32, accumulate=1),
+             dict(a, Y=Y2, ldy=Y2.stride(0), ydtype=tsl.F32)]
+    run(items, [None, dict(act=tsl.ACT_RELU)], wk, M)
+    z = f64(X) @ W.w
+    assert np.array_equal(f64(Y1), z + 2) and np.array_equal(f64(Y2), np.maximum(z, 0))

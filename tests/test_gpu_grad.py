@@ -285,3 +285,16 @@ def test_repeat_gives_the_same_bits_and_replays():
         assert all(t.equal(a, b) for a, b in zip(outs, want))
         step()
         t.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [1, 64, 65])
+@pytest.mark.parametrize("acc", [0, 1])
+def test_bias_gradient_alone(M, acc):
+    """The sums of one and of several blocks of rows, with no product at all."""
+    N = 100
+    W = Weight("bf16", 64, N, 1)
+    sh = tsl.plan_linear(64, N, 1, tsl.COLUMN)[0]
+    dy = ints(2, (M, N))
+    X = put(ints(1, (M, 64)), "bf16")
+    db = linear_grad("bf16", W, sh, X, "none", None, put(dy, "bf16"), want="b", acc=acc, fill=5.0)[2]
+    assert np.array_equal(f64(db), dy.sum(0) + 5 * acc)
