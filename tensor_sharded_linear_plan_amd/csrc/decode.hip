@@ -314,6 +314,11 @@ template <bool Q4, bool DUAL> DecodeFn pick(int mt) {
                      : decode_kernel<Q4, DUAL, 4>;
 }
 
+// Waves of a workgroup.
+int wave_count(int64_t tiles, int64_t M) {
+    return tiles <= 256 && M <= 16 ? 16 : (tiles <= 512 ? 8 : 4);
+}
+
 } // namespace
 
 // Each tile's waves read the call's X again (from L2), which the streaming
@@ -327,12 +332,19 @@ template <bool Q4, bool DUAL> DecodeFn pick(int mt) {
 // From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 / 63, gated 57 /
 // 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles (T 224, K
 // 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 / 15.5).
+// Few tiles of a long k leave a 4-bit wave of more than one row tile, which
+// holds no second unit, a chain of loads that only the split over workgroups
+// shortens: with less than half the chip's waves, up to 8 units a wave (T 46,
+// 106 units over 8 waves, M 42: 39.2 / 23.9 us; 64 units, M 24: 17.0 / 15.4;
+// one row tile, 256 units over 16 waves, M 1: 16.5 / 21.3).
 bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M) {
     if (wdtype == TSL_F32 || M > kDecodeRows)
         return false;
-    int64_t tiles = 0;
+    int64_t tiles = 0, units = 0, set = 0; // units: the longest set's
     bool any = false;
     for (const LinearItem &L : items) {
+        set = (L.set_pos == 0 ? 0 : set) + (wdtype == TSL_Q4G64 ? L.g.KT : L.g.KT / 2);
+        units = set > units ? set : units;
         any = any || L.ep;
         if (L.accumulate || L.set_len > kSetParts)
             return false;
@@ -340,6 +352,9 @@ bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int6
             tiles += L.g.Nt;
     }
     if (!any || tiles > 1200)
+        return false;
+    const int waves = wave_count(tiles, M);
+    if (wdtype == TSL_Q4G64 && M > 16 && tiles * waves < 2048 && units > 8 * waves)
         return false;
     const bool two = dual(items[0]);
     if (M <= 32)
@@ -357,7 +372,7 @@ hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
     for (const LinearItem &L : items)
         if (L.set_len > 0)
             tiles += L.g.Nt;
-    const int waves = tiles <= 256 && mt == 1 ? 16 : (tiles <= 512 ? 8 : 4);
+    const int waves = wave_count(tiles, M);
     const size_t lds = (size_t)waves * mt * (two ? 2 : 1) * 64 * 16;
     for (size_t i = 0; i < items.size();) {
         Group grp{};
