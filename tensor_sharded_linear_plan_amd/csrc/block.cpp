@@ -295,6 +295,7 @@ tsl_status check_epilogue(const tsl_epilogue &e, int64_t n, Epilogue *out) {
 // (kept pre-activations, biases, residuals) against every output and input.
 bool epilogue_clash(const std::vector<LinearItem> &v, size_t xe) {
     std::vector<Mat> kept, read; // outputs and inputs of the epilogues
+    std::vector<const LinearItem *> reader; // whose input read[i] is
     for (const LinearItem &L : v) {
         if (!L.ep)
             continue;
@@ -308,6 +309,7 @@ bool epilogue_clash(const std::vector<LinearItem> &v, size_t xe) {
             read.push_back(Mat{e.bias, 1, L.g.Ns, L.g.Ns, (size_t)(e.flags & kEpBiasBf16 ? 2 : 4)});
         if (e.res)
             read.push_back(Mat{e.res, L.M, L.g.Ns, e.ldr, re});
+        reader.resize(read.size(), &L);
     }
     if (kept.empty() && read.empty())
         return false;
@@ -320,9 +322,11 @@ bool epilogue_clash(const std::vector<LinearItem> &v, size_t xe) {
         for (const Mat &k : kept)
             if (clash(k, x) || clash(k, ix) || clash(k, y))
                 return true;
-        for (const Mat &r : read) {
-            const bool own = L.ep && L.ep->res == r.p && r.p == L.Y && L.ep->ldr == L.ldy &&
-                             y.e == r.e && r.ld == y.ld && r.rows == y.rows && r.cols == y.cols;
+        for (size_t i = 0; i < read.size(); ++i) {
+            const Mat &r = read[i];
+            // the residual of the item itself, updated in place
+            const bool own = reader[i] == &L && r.p == L.ep->res && r.p == L.Y && r.ld == y.ld &&
+                             r.e == y.e && r.rows == y.rows && r.cols == y.cols;
             if (!own && clash(y, r))
                 return true;
         }
