@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(64 * WM * WN)
     // entry), so the block loop never reads the kernel arguments (a scalar
     // load there would drain the LDS reads in flight); the copies address
     // records with full 64-bit per-lane addresses.
-    int KBm = a.KBm, tmax = a.Nt16 - 1;
+    // The entries are the tile's own first records (a 64-bit step: a packed
+    // weight may pass 4 GiB), so that the copies' offsets stay below 2^30.
+    const int t0 = (int)(n0 >> 4) + (kEpilogue ? a.t_off : 0);
+    int KBm = a.KBm, tmax = a.Nt16 - 1 - t0;
     asm volatile("" : "+s"(KBm), "+s"(tmax));
     // DUAL: from the first weight's records to the second's
     int64_t to_up = 0;
@@ -201,9 +204,9 @@ __global__ void __launch_bounds__(64 * WM * WN)
         to_up = static_cast<const char *>(grp.ep(lo).up) - a.W;
     }
     if (threadIdx.x < kSetParts)
-        mtab[threadIdx.x] = a.R > 1 ? grp.segw[a.seg][threadIdx.x < a.R ? threadIdx.x : 0] : a.W;
+        mtab[threadIdx.x] = (a.R > 1 ? grp.segw[a.seg][threadIdx.x < a.R ? threadIdx.x : 0] : a.W) +
+                            (int64_t)t0 * KBm * kQ4Record;
     __syncthreads();
-    const int t0 = (int)(n0 >> 4) + (kEpilogue ? a.t_off : 0);
     // where block b's records start: the member holding global block
     // blk0 + b and the block's index within it
     auto block_src = [&](int b, int &lb) __attribute__((always_inline)) {
@@ -224,14 +227,14 @@ __global__ void __launch_bounds__(64 * WM * WN)
         if (c < C::CCW) {
             const int rr = wave + C::NW * c;
             const int rc = DUAL ? 2 * (rr >> 2) + (rr & 1) : rr; // 16-column tile of its weight
-            const int nt = t0 + rc < tmax ? t0 + rc : tmax;
+            const int nt = rc < tmax ? rc : tmax;
             const uint32_t off = (uint32_t)((nt * KBm + lb) * kQ4Record) + 16 * (uint32_t)lane;
             dma16_at((DUAL && (rr >> 1 & 1) ? base + to_up : base) + off, dst + rr * 1024);
         } else {
             const int p = wave + C::NW * (c - C::CCW);
             const int rr = 2 * p + (lane >> 5);
             const int rc = DUAL ? 2 * (p >> 1) + (lane >> 5) : rr;
-            const int nt = t0 + rc < tmax ? t0 + rc : tmax;
+            const int nt = rc < tmax ? rc : tmax;
             const uint32_t off = (uint32_t)((nt * KBm + lb) * kQ4Record) + kQ4PairsAt +
                                  4 * (uint32_t)(lane & 31);
             dma4_at((DUAL && (p & 1) ? base + to_up : base) + off, dst + C::NR * 1024 + p * 256);
