@@ -150,7 +150,10 @@ tsl_status shard_linear_group_epilogue_workspace_size(int32_t n_items,
  *              product).  Of a sum set the first item's applies, once, to the
  *              set's sum -- bias and residual of a row-parallel layer are
  *              added after the ranks' partials ([mlxcel] "Row Parallel") --
- *              and those of its other members must be null.
+ *              and those of its other members must be null.  A set's products
+ *              are added in binary32 over the members' k-ranges in item
+ *              order; equal calls give equal bits, but not those of separate
+ *              products added afterwards.
  * accumulate must be 0 for an item with an epilogue.  No output (Y, pre) may
  * share an element with another output or with any X, bias or residual
  * (except a residual that is its own item's Y).
@@ -250,7 +253,8 @@ tsl_status shard_linear_grad_workspace_size(const tsl_shard *shard, tsl_dtype wd
  *             in a fixed order.
  * Products accumulate in binary32; with an activation dZ is their operand
  * rounded once to wdtype (BF16 and M * n_len up to 2^16: together with what
- * that rounding left, so that it does not show).  Slope of relu at 0 is 0.  M == 0 writes zero
+ * that rounding left, so that it does not show; an infinity in X or the weight
+ * may then give NaN).  Slope of relu at 0 is 0.  M == 0 writes zero
  * weight and bias gradients (unless they accumulate).  M, k_len, n_len and
  * input strides below 2^22.  No output may share an element with an input,
  * another output or the workspace.  Errors as shard_linear.

@@ -1,12 +1,13 @@
 """One rank's share of tensor-parallel linear layers on one MI355X.
 
-The compute lives in ``libtsl.so`` (hand-written HIP kernels for gfx950
-behind a C ABI declared in ``include/tsl.h``).  ``binding`` is a thin ctypes
-layer over it with the same entry-point names; it raises ImportError when
-the library has not been built -- there is no fallback.
+The compute lives in ``libtsl.so`` and ``libtsl_block.so`` (hand-written HIP
+kernels for gfx950 behind the C ABIs of ``include/tsl.h`` and
+``include/tsl_block.h``).  ``binding`` is a thin ctypes layer over them with
+the same entry-point names; it raises ImportError when one has not been
+built -- there is no fallback.
 
 ``synth`` (seeded input generators), ``configs`` (workload sizes) and
-``build`` (the compiler driver) do not need the library.
+``build`` (the compiler driver) do not need the libraries.
 """
 import importlib
 
@@ -16,7 +17,7 @@ __all__ = ["binding", "synth", "configs"]
 def __getattr__(name):
     if name in ("binding", "synth", "configs", "build"):
         return importlib.import_module("." + name, __name__)
-    # entry points re-exported from the binding: loading it loads libtsl.so
+    # entry points re-exported from the binding: loading it loads both libraries
     binding = importlib.import_module(".binding", __name__)
     if hasattr(binding, name):
         return getattr(binding, name)

@@ -1,6 +1,7 @@
 """ctypes binding of libtsl.so and libtsl_block.so -- the entry points of
-include/tsl.h and include/tsl_block.h under the same names, argument marshalling only.  Every step of the compute runs in
-the library's HIP kernels; nothing here computes.
+include/tsl.h and include/tsl_block.h under the same names, argument
+marshalling only.  Every step of the compute runs in the libraries' HIP
+kernels; nothing here computes.
 
 Pointer arguments take either an integer device address or any object with
 a ``data_ptr()`` method (a torch tensor).  ``stream=None`` means the current
@@ -364,6 +365,8 @@ def _items(items):
             continue
         get = it.get
         sh = it["shard"]
+        if not isinstance(sh, Shard):
+            sh = Shard(*sh.as_tuple())
         keep.append(sh)
         arr[i] = LinearItem(ctypes.pointer(sh), _ptr(it["packed"]), it["packed_bytes"],
                             _ptr(it["X"]), it["ldx"], _ptr(get("Y")), get("ldy", 0),

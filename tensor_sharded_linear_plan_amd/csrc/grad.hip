@@ -15,7 +15,8 @@
 //     64 rows.
 // With few entries (split) what the rounding of dZ left is an operand of its
 // own, rows and k-range doubled, so that its error does not show.
-// Bound by bytes: gated, 3 values read and 4 written per element.
+// Bound by bytes: gated, 3 values read and 4 written per element (4096 rows,
+// 3584 columns, with the copy of X of 4096: 272 MB in 54 us, 5.0 TB/s).
 #include "device.hpp"
 #include "epilogue.hpp"
 #include "internal.hpp"

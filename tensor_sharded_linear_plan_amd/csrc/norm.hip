@@ -10,8 +10,10 @@
 // the TPR threads that own it (NV runs of 8 columns each) from its only read
 // to its only write, so every input is read once and every output written
 // once.  A row's threads are one wave up to 512 columns (four rows share a
-// workgroup), a workgroup of four waves up to 8192 and of sixteen up to
-// 32768.  All sums are binary32.
+// workgroup), a workgroup of four waves up to 8192 (backward, three operands
+// a row: up to 4096, eight waves up to 8192) and of sixteen up to 32768.  All
+// sums are binary32.  Measured, forward, four partials and a residual to e4m3,
+// 2048 x 5120: 52 us, 221 MB, 4.3 TB/s, where a copy reaches 4.9.
 #include "device.hpp"
 #include "internal.hpp"
 #include "rows.hpp"
