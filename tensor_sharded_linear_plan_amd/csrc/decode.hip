@@ -20,11 +20,12 @@
 // one unit (128 k of 4-bit, 64 k of bf16 weights) ahead, and its activation
 // fragments straight from global memory -- a wave reads only its own k-run of
 // X, from L2, so there is nothing to share through LDS and no barrier before
-// the sum.  Measured: one rank's 4-bit gate and up, 1 row, 3584 -> 2 x 4736
-// (19 MB), 8.0 us a call where the host's enqueue takes as long; 4 ranks'
-// down shards, 4 rows, 18944 -> 3584 (38 MB), 15.2 us (2.5 TB/s; with a
-// separate launch for the k-partials 14.6 and 19.0).  What bounds the larger
-// is the 4-bit expansion's VALU work per record beside 16 waves a CU.
+// the sum.  Most of those loads are activations (16 rows of 32 k are 1 KB, as
+// the weights of 128 k), so calls of up to 8 rows pack several k-slices into
+// one operand (RG below).  Measured: one rank's 4-bit gate and up, 1 row, 3584
+// -> 2 x 4736 (19 MB), 8.2 us; 4 ranks' down shards, 4 rows, 18944 -> 3584 (38
+// MB), 14.5 us with whole operands, 11.5 with packed ones (3.3 TB/s; with whole
+// ones and a separate launch for the k-partials 19.0).
 #include <hip/hip_runtime.h>
 
 #include "device.hpp"
@@ -64,10 +65,20 @@ template <bool Q4> struct Unit {
     static constexpr int FR = K / 32;                  // activation fragments
 };
 
-// MT 16-row tiles; more than one needs the registers of 8 waves.
-template <bool Q4, bool DUAL, int MT>
+// MT 16-row tiles; more than one needs the registers of 8 waves.  RG: rows of
+// a call of few rows (4 or 8; 4-bit weights), else 16.  Of the 16 rows an MFMA
+// takes, rows RG s .. RG s + RG - 1 are then the call's rows at 32-k slice s of
+// 16 / RG, so that one load holds several slices' activations.  Against the
+// weights of slice t the results in slice t's rows are its product (the others
+// mean nothing): each lane keeps its own slice's and adds them up, and the
+// lanes of one row meet at the end.
+template <bool Q4, bool DUAL, int MT, int RG>
 __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp) {
+    constexpr bool FEW = RG < 16;
+    static_assert(!FEW || (Q4 && MT == 1), "one tile of slices");
     using C = Unit<Q4>;
+    constexpr int NS = 16 / RG;       // slices of a load
+    constexpr int XR = C::FR / NS;    // activation loads per unit
     constexpr int NT = DUAL ? 2 : 1;
     extern __shared__ __attribute__((aligned(16))) f32x4 red[]; // [waves][MT][NT][64]
     const int lane = threadIdx.x & 63;
@@ -85,7 +96,10 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
     const Item &a = grp.it[lo];
     const int64_t tile = bid - a.start;
     const int u0 = wave * a.units / W, u1 = (wave + 1) * a.units / W;
-    const int row = lane & 15, kg = lane >> 4;
+    const int kg = lane >> 4;
+    const int row = lane & (RG - 1);      // this lane's activation row
+    const int slice = (lane & 15) / RG;   // and slice of a load; its results':
+    const int rslice = kg * 4 / RG;
     const int64_t up = DUAL ? static_cast<const char *>(grp.ep(lo).up) - grp.mb[a.first].B : 0;
 
     // where the next unit comes from: unit lu of member r.  Rows past M read
@@ -120,8 +134,8 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
     };
     struct Regs {
         u32x4 w[NT][C::CHUNKS];
-        u32x2 sb[NT];
-        u32x4 x[MT][C::FR];
+        u32x2 sb[NT]; // (RG 4: the one pair of this lane's results)
+        u32x4 x[MT][XR];
     };
     auto load = [&](Regs &g) __attribute__((always_inline)) {
 #pragma unroll
@@ -130,7 +144,10 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
 #pragma unroll
             for (int l = 0; l < C::CHUNKS; ++l)
                 g.w[j][l] = *reinterpret_cast<const u32x4 *>(rec + l * C::CS + lane * 16);
-            if constexpr (Q4)
+            if constexpr (RG == 4)
+                g.sb[j].x = *reinterpret_cast<const uint32_t *>(rec + kQ4PairsAt + (lane & 15) * 8 +
+                                                                (rslice >> 1) * 4);
+            else if constexpr (Q4)
                 g.sb[j] = *reinterpret_cast<const u32x2 *>(rec + kQ4PairsAt + (lane & 15) * 8);
         }
         // 4-bit k-ranges are whole 64-k groups and bf16 units 64 k, so that
@@ -138,23 +155,23 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
         const int left = Ks - lu * C::K;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const uint16_t *x = xp[i] + lu * C::K;
+            const uint16_t *x = xp[i] + lu * C::K + 32 * slice;
             if (left >= C::K) {
 #pragma unroll
-                for (int f = 0; f < C::FR; ++f)
-                    g.x[i][f] = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+                for (int f = 0; f < XR; ++f)
+                    g.x[i][f] = *reinterpret_cast<const u32x4 *>(x + 32 * NS * f);
             } else {
 #pragma unroll
-                for (int f = 0; f < C::FR; ++f) {
-                    const int k = 32 * f + 8 * kg;
+                for (int f = 0; f < XR; ++f) {
+                    const int k = 32 * (NS * f + slice) + 8 * kg;
                     u32x4 v = {0, 0, 0, 0};
                     if (k + 8 <= left) {
-                        v = *reinterpret_cast<const u32x4 *>(x + 32 * f);
+                        v = *reinterpret_cast<const u32x4 *>(x + 32 * NS * f);
                     } else if (k < left) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t l0 = k + 2 * e < left ? x[32 * f + 2 * e] : 0u;
-                            const uint32_t h0 = k + 2 * e + 1 < left ? x[32 * f + 2 * e + 1] : 0u;
+                            const uint32_t l0 = k + 2 * e < left ? x[32 * NS * f + 2 * e] : 0u;
+                            const uint32_t h0 = k + 2 * e + 1 < left ? x[32 * NS * f + 2 * e + 1] : 0u;
                             v[e] = l0 | (h0 << 16);
                         }
                     }
@@ -163,7 +180,7 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
             }
             if (masked) {
 #pragma unroll
-                for (int f = 0; f < C::FR; ++f)
+                for (int f = 0; f < XR; ++f)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         g.x[i][f][e] &= keep[i];
@@ -178,7 +195,37 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
         for (int j = 0; j < NT; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const Regs &g) __attribute__((always_inline)) {
-        if constexpr (!Q4) {
+        if constexpr (FEW) {
+            const bf16x8 ones = __builtin_bit_cast(
+                bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < XR; ++f) {
+                const bf16x8 xa = __builtin_bit_cast(bf16x8, g.x[0][f]);
+                const f32x4 xs = mfma_bf16(xa, ones, zero); // of the slice of each lane's results
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    f32x4 ag[NS];
+#pragma unroll
+                    for (int t = 0; t < NS; ++t)
+                        ag[t] = mfma_bf16(xa, q4_to_bf16_plus128(g.w[j][0][NS * f + t]), zero);
+                    // as below: s sum(x (128 + q)) + (b - 128 s) sum(x)
+                    const uint32_t sbp = g.sb[j][f];
+                    const float sc = bf16_lo(sbp);
+                    const float cb = __builtin_fmaf(-128.f, sc, bf16_hi(sbp));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float v = rslice & 1 ? ag[1][q] : ag[0][q];
+                        if constexpr (NS == 4) {
+                            const float v1 = rslice & 1 ? ag[3][q] : ag[2][q];
+                            v = rslice & 2 ? v1 : v;
+                        }
+                        acc[0][j][q] = __builtin_fmaf(sc, v, acc[0][j][q]);
+                        acc[0][j][q] = __builtin_fmaf(cb, xs[q], acc[0][j][q]);
+                    }
+                }
+            }
+        } else if constexpr (!Q4) {
 #pragma unroll
             for (int f = 0; f < C::FR; ++f)
 #pragma unroll
@@ -285,15 +332,31 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
                     v[j][q] += p[q];
             }
         }
-        // lane holds rows 16 i + 4 (lane / 16) + q of column lane % 16
+        if constexpr (FEW) { // the slices' sums
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[j][q] += __shfl_xor(v[j][q], 32, 64);
+                    if constexpr (RG == 4)
+                        v[j][q] += __shfl_xor(v[j][q], 16, 64);
+                }
+                if constexpr (RG == 4) { // each lane's one row to its first place
+                    const float a0 = kg & 1 ? v[j][1] : v[j][0], a1 = kg & 1 ? v[j][3] : v[j][2];
+                    v[j][0] = kg & 2 ? a1 : a0;
+                }
+            }
+        }
+        // lane holds rows 16 i + 4 (lane / 16) + q (RG 4: row lane / 16; RG 8:
+        // lanes from 32 on repeat the others) of column lane % 16
         const int64_t col = tile * 16 + (lane & 15);
         if (col >= a.Ns)
             return;
         const Epilogue e = grp.ep(lo);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t m = 16 * i + 4 * kg + q;
-            if (m >= a.M)
+        for (int q = 0; q < (RG == 4 ? 1 : 4); ++q) {
+            const int64_t m = RG == 4 ? kg : 16 * i + 4 * kg + q;
+            if (m >= a.M) // (RG 8: so are the repeated lanes' rows)
                 continue;
             float y;
             if constexpr (DUAL)
@@ -307,11 +370,15 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
 
 typedef void (*DecodeFn)(Group);
 
-template <bool Q4, bool DUAL> DecodeFn pick(int mt) {
-    return mt == 1   ? decode_kernel<Q4, DUAL, 1>
-           : mt == 2 ? decode_kernel<Q4, DUAL, 2>
-           : mt == 3 ? decode_kernel<Q4, DUAL, 3>
-                     : decode_kernel<Q4, DUAL, 4>;
+template <bool Q4, bool DUAL> DecodeFn pick(int64_t M) {
+    if constexpr (Q4) {
+        if (M <= 8)
+            return M <= 4 ? decode_kernel<true, DUAL, 1, 4> : decode_kernel<true, DUAL, 1, 8>;
+    }
+    return M <= 16   ? decode_kernel<Q4, DUAL, 1, 16>
+           : M <= 32 ? decode_kernel<Q4, DUAL, 2, 16>
+           : M <= 48 ? decode_kernel<Q4, DUAL, 3, 16>
+                     : decode_kernel<Q4, DUAL, 4, 16>;
 }
 
 // Waves of a workgroup.
@@ -326,9 +393,12 @@ int wave_count(int64_t tiles, int64_t M) {
 // calls of few tiles or few rows: with T tiles (of one weight) and M rows,
 // up to 32 rows T M <= 9472 (gated: twice that, for a tile of X serves both
 // weights), and T <= 1200.  Either side of it, K 3584, this form / the other:
-// 4-bit lone T 592: M 16 15.1 / 14.9 us, M 32 25.7 / 22.2; T 1184: M 8 17.1 /
-// 17.8, M 16 22.2 / 18.4; T 2048: M 1 16.5 / 15.3; gated T 1184: M 16 24.2 /
-// 25.7, M 32 39.7 / 36.9; bf16 lone T 592: M 16 16.5 / 17.9, M 32 25.2 / 22.4.
+// 4-bit lone T 592: M 16 15.1 / 14.9 us, M 32 25.7 / 22.2; T 1184: M 16 22.2 /
+// 18.4; T 1280: M 8 15.0 / 16.6; T 2048: M 6 23.8 / 20.8; gated T 1184: M 16
+// 24.2 / 25.7, M 32 39.7 / 36.9; bf16 lone T 592: M 16 16.5 / 17.9, M 32 25.2 /
+// 22.4.  Up to 4 rows of 4-bit weights, whose activations are one load a unit,
+// always: T 1280: M 1 10.1 / 14.1, M 4 10.2 / 15.8; T 2048: M 1 17.6 / 16.5, M 4
+// 18.6 / 20.9; T 9504: M 1 55.8 / 57.6, M 4 63.4 / 65.7.
 // From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 / 63, gated 57 /
 // 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles (T 224, K
 // 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 / 15.5).
@@ -351,6 +421,8 @@ bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int6
         if (L.set_len > 0)
             tiles += L.g.Nt;
     }
+    if (any && wdtype == TSL_Q4G64 && M <= 4 && tiles < (1 << 20)) // (workgroups of a launch)
+        return true;
     if (!any || tiles > 1200)
         return false;
     const int waves = wave_count(tiles, M);
@@ -366,8 +438,8 @@ hipError_t launch_decode(const std::vector<LinearItem> &items, tsl_dtype wdtype,
                          hipStream_t stream) {
     const bool q4 = wdtype == TSL_Q4G64, two = dual(items[0]);
     const int mt = (int)((M + 15) / 16);
-    const DecodeFn fn = q4 ? (two ? pick<true, true>(mt) : pick<true, false>(mt))
-                           : (two ? pick<false, true>(mt) : pick<false, false>(mt));
+    const DecodeFn fn = q4 ? (two ? pick<true, true>(M) : pick<true, false>(M))
+                           : (two ? pick<false, true>(M) : pick<false, false>(M));
     int64_t tiles = 0;
     for (const LinearItem &L : items)
         if (L.set_len > 0)
