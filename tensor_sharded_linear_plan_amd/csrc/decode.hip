@@ -397,8 +397,11 @@ int wave_count(int64_t tiles, int64_t M) {
 // 18.4; T 1280: M 8 15.0 / 16.6; T 2048: M 6 23.8 / 20.8; gated T 1184: M 16
 // 24.2 / 25.7, M 32 39.7 / 36.9; bf16 lone T 592: M 16 16.5 / 17.9, M 32 25.2 /
 // 22.4.  Up to 4 rows of 4-bit weights, whose activations are one load a unit,
-// always: T 1280: M 1 10.1 / 14.1, M 4 10.2 / 15.8; T 2048: M 1 17.6 / 16.5, M 4
-// 18.6 / 20.9; T 9504: M 1 55.8 / 57.6, M 4 63.4 / 65.7.
+// where one launch holds the call's items: T <= 1536, and any T (a launch's
+// workgroups countable) from 3 rows on: T 1280: M 1 10.1 / 14.1, M 4 10.2 /
+// 15.8; T 2048: M 1 17.6 / 16.5, M 4 18.6 / 20.9; T 9504: M 4 63.4 / 65.7;
+// experts of 2048 -> 768, rows through an index: 32 of them, M 2 10.1 / 14.7,
+// 64, M 1 17.5 / 15.6, M 4 18.0 / 19.1, in two launches 128, M 4 34.3 / 30.4.
 // From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 / 63, gated 57 /
 // 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles (T 224, K
 // 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 / 15.5).
@@ -410,7 +413,7 @@ int wave_count(int64_t tiles, int64_t M) {
 bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M) {
     if (wdtype == TSL_F32 || M > kDecodeRows)
         return false;
-    int64_t tiles = 0, units = 0, set = 0; // units: the longest set's
+    int64_t tiles = 0, sets = 0, units = 0, set = 0; // units: the longest set's
     bool any = false;
     for (const LinearItem &L : items) {
         set = (L.set_pos == 0 ? 0 : set) + (wdtype == TSL_Q4G64 ? L.g.KT : L.g.KT / 2);
@@ -418,11 +421,13 @@ bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int6
         any = any || L.ep;
         if (L.accumulate || L.set_len > kSetParts)
             return false;
-        if (L.set_len > 0)
+        if (L.set_len > 0) {
             tiles += L.g.Nt;
+            ++sets;
+        }
     }
-    if (any && wdtype == TSL_Q4G64 && M <= 4 && tiles < (1 << 20)) // (workgroups of a launch)
-        return true;
+    if (any && wdtype == TSL_Q4G64 && M <= 4 && sets <= kItems)
+        return tiles <= 1536 || (M > 2 && tiles < (1 << 20));
     if (!any || tiles > 1200)
         return false;
     const int waves = wave_count(tiles, M);
