@@ -849,7 +849,11 @@ tsl_status run_grad(const GradCall &c, void *workspace, size_t ws_bytes, void *s
     return run_group(dw, c.wdtype, rows, gws, gbytes, stream);
 }
 
-// A size query's call: every output wanted, an activation in between.
+// The most a call needs over everything the size query does not know: the
+// order of the weight gradients, the outputs wanted, the activation (none, one
+// with the rounding's remainders as operands, one without) and accumulation
+// (an accumulating product is not split along k, and another of its launch may
+// then be split further).
 tsl_status size_grad(const GradCall &in, size_t *bytes) {
     if (in.M < 0 || !bytes)
         return TSL_ERR_INVALID_ARG;
@@ -858,22 +862,30 @@ tsl_status size_grad(const GradCall &in, size_t *bytes) {
     static char any[1];
     GradCall c = in;
     size_t most = 0;
+    // silu, and where it splits its operands relu, which never does; a gated
+    // pair's operands are the same for every activation
+    const int acts[3] = {TSL_ACT_SILU, TSL_ACT_NONE, TSL_ACT_RELU};
     for (int order = 0; order < 2; ++order)
         for (int mask = 1; mask < 4; ++mask)
-            for (int act = 0; act < 2; ++act) {
-                c.act = act ? TSL_ACT_SILU : TSL_ACT_NONE;
-                c.dX = mask & 1 ? any : nullptr;
-                c.dW[0] = mask & 2 ? any : nullptr;
-                c.dW[1] = c.n_w == 2 ? c.dW[0] : nullptr;
-                c.db = c.n_w == 1 ? reinterpret_cast<float *>(any) : nullptr;
-                c.sk = order ? 1 : 2;
-                c.sn = order ? 2 : 1;
-                GradPlan p;
-                PackGeom gt;
-                tsl_status st = plan_grad(c, &p, &gt);
-                if (st != TSL_OK)
-                    return st;
-                most = p.total > most ? p.total : most;
+            for (int acc = 0; acc < (mask & 2 ? 2 : 1); ++acc) {
+                bool split = false;
+                for (int k = 0; k < (c.n_w == 2 ? 1 : (split ? 3 : 2)); ++k) {
+                    c.act = acts[k];
+                    c.accumulate = acc;
+                    c.dX = mask & 1 ? any : nullptr;
+                    c.dW[0] = mask & 2 ? any : nullptr;
+                    c.dW[1] = c.n_w == 2 ? c.dW[0] : nullptr;
+                    c.db = c.n_w == 1 ? reinterpret_cast<float *>(any) : nullptr;
+                    c.sk = order ? 1 : 2;
+                    c.sn = order ? 2 : 1;
+                    GradPlan p;
+                    PackGeom gt;
+                    tsl_status st = plan_grad(c, &p, &gt);
+                    if (st != TSL_OK)
+                        return st;
+                    split = split || p.split;
+                    most = p.total > most ? p.total : most;
+                }
             }
     *bytes = most;
     return TSL_OK;
