@@ -410,10 +410,13 @@ typedef struct {
 
 /*
  * shard_linear_group_workspace_size -- workspace bytes shard_linear_group
- * needs for these items (only their shards, sum_next, rows and whether
- * row_index is null are read), weight type and M.  An upper bound: a call
- * whose items read the same X (same pointer, ldx, k_len and row_index)
- * shares one activation copy and uses less.
+ * needs for these items (only their shards, sum_next, rows, accumulate and
+ * whether row_index is null are read), weight type and M.  An upper bound: a
+ * call whose items read the same X (same pointer, ldx, k_len and row_index)
+ * shares one activation copy and uses less, and what is asked for with
+ * accumulate 1 serves the same items all with 0.  (Not the other way round: a
+ * product that accumulates is not split along k, and the others of its call
+ * may then be split further.)
  */
 tsl_status shard_linear_group_workspace_size(int32_t n_items, const tsl_linear_item *items,
                                              tsl_dtype wdtype, int64_t M, size_t *bytes);

@@ -134,8 +134,8 @@ typedef struct tsl_epilogue {
 
 /* shard_linear_group_epilogue_workspace_size -- workspace bytes
  * shard_linear_group_epilogue needs (items as for
- * shard_linear_group_workspace_size, and their accumulate; of the epilogues
- * only whether one is null is read).  0 for most calls of up to 64 rows. */
+ * shard_linear_group_workspace_size; of the epilogues only whether one is
+ * null is read).  0 for most calls of up to 64 rows. */
 tsl_status shard_linear_group_epilogue_workspace_size(int32_t n_items,
                                                       const tsl_linear_item *items,
                                                       const tsl_epilogue *const *epilogues,

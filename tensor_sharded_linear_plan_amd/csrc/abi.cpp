@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cstddef>
 #include <vector>
 
@@ -107,6 +108,7 @@ extern "C" tsl_status shard_linear_group_workspace_size(int32_t n_items,
         return TSL_ERR_INVALID_ARG;
     std::vector<LinearItem> v(n_items);
     int32_t first = 0;
+    bool accumulates = false;
     for (int32_t i = 0; i < n_items; ++i) {
         if (!items[i].shard || (items[i].sum_next != 0 && items[i].sum_next != 1) ||
             items[i].rows < 0 || items[i].rows > M)
@@ -118,6 +120,9 @@ extern "C" tsl_status shard_linear_group_workspace_size(int32_t n_items,
         v[i].ridx = items[i].row_index; // only whether it is null matters here
         v[i].x_rows = 1;
         v[i].set_pos = i - first;
+        // part of the plan (a set's items do not accumulate)
+        v[i].accumulate = v[i].set_pos == 0 && items[i].accumulate == 1;
+        accumulates = accumulates || v[i].accumulate;
         if (!items[i].sum_next || i == n_items - 1) {
             v[first].set_len = i - first + 1;
             for (int32_t r = first + 1; r <= i; ++r)
@@ -126,6 +131,11 @@ extern "C" tsl_status shard_linear_group_workspace_size(int32_t n_items,
         }
     }
     *bytes = group_workspace(v, wdtype, M);
+    if (accumulates) { // the same items storing their products fit too
+        for (LinearItem &L : v)
+            L.accumulate = 0;
+        *bytes = std::max(*bytes, group_workspace(v, wdtype, M));
+    }
     return TSL_OK;
 }
 

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cstddef>
 #include <vector>
 
@@ -358,6 +359,13 @@ extern "C" tsl_status shard_linear_group_epilogue_workspace_size(
             if (epilogues[i])
                 v[i].ep = &none;
         *bytes = group_workspace(v, wdtype, M);
+        bool accumulates = false;
+        for (LinearItem &L : v) {
+            accumulates = accumulates || L.accumulate;
+            L.accumulate = 0;
+        }
+        if (accumulates) // the same items storing their products fit too
+            *bytes = std::max(*bytes, group_workspace(v, wdtype, M));
         return TSL_OK;
     });
 }
