@@ -47,9 +47,13 @@ extern "C" {
  *             once), or E4M3: 8-bit values q with binary32 scales, y = s q,
  *             one s per run of `group` columns (group 32, 64 or 128; the
  *             last run of a row may be short) or per row (group 0):
- *             s = max |y| / 448 over the run and q = y / s rounded to nearest
- *             even; a run of zeros has s = 0, a run with a value that is not
- *             finite an s that is not finite and q NaN.
+ *             s = max |y| / 448 over the run, and q the quotient y / s (both
+ *             divisions in binary32) rounded to nearest even; a run of zeros
+ *             (or of values up to 224 * 2^-149, whose s rounds to 0) has
+ *             s = 0 and q = 0, a run with a value that is not finite an s
+ *             that is not finite and q NaN.  The products of these headers
+ *             read F32 and BF16; the 8-bit form is for a consumer of the
+ *             caller's.
  *   scales:   DEVICE binary32 [M][ceil(n / group)] ([M] for group 0) for
  *             E4M3, else null (and group 0).
  *   rstd:     null, or DEVICE binary32 [M]: receives rstd (for the backward

@@ -72,19 +72,22 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float *red) {
 
 constexpr float kE4M3Max = 448.f;
 
-// 8 values times 1 / scale as e4m3 (nearest, ties to even; gfx950 converts
-// a pair per instruction).  Every |v| is at most the scale times 448 up to
-// rounding, and clamped to it; a scale of zero has only zeros.
+// 8 values over their scale as e4m3 (nearest, ties to even; gfx950 converts a
+// pair per instruction).  The quotient is a division: a product with the rounded
+// reciprocal falls on the other side of a tie now and then (2 codes of 13
+// million), and the pass is bound by memory either way (2048 x 5120, four
+// partials: 51.2 us with the reciprocal, 51.7 divided; one bf16 part 23.0 and
+// 23.6).  Every |v| is at most the scale times 448 up to the scale's rounding,
+// and clamped to it.  A scale of zero (the largest |v| over 448 rounds to zero)
+// has only zeros.
 __device__ __forceinline__ u32x2 quant8(f32x8 v, float scale) {
-    const float inv = scale > 0.f ? 1.f / scale : 0.f;
+    const float d = scale == 0.f ? 1.f : scale; // |v| < 2^-140 there: codes of zero
+    const bool bad = !__builtin_isfinite(scale);
     u32x2 w = {0, 0};
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // a scale below 2^-128 has an infinite reciprocal: divide instead
-        float x = __builtin_isinf(inv) ? v[i] / scale : v[i] * inv;
-        if (scale != scale || __builtin_isinf(scale))
-            x = __builtin_nanf("");
+        const float x = bad ? __builtin_nanf("") : v[i] / d;
         q[i] = x > kE4M3Max ? kE4M3Max : (x < -kE4M3Max ? -kE4M3Max : x);
     }
 #pragma unroll
