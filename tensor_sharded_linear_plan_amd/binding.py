@@ -351,10 +351,15 @@ def shard_linear(shard, wdtype, packed, packed_bytes, xdtype, X, ldx, M, ydtype,
                              ws_bytes, _stream(stream)), "shard_linear")
 
 
+def _shard(sh):
+    """A Shard, or a copy of any object with its as_tuple."""
+    return sh if isinstance(sh, Shard) else Shard(*sh.as_tuple())
+
+
 def _items(items):
     """items: sequence of dicts (or LinearItem) with the tsl_linear_item
     fields (ydtype defaults to F32, accumulate, sum_next and rows to 0,
-    row_index to None); shard is a Shard; a set member's Y may be None.
+    row_index to None); shard as _shard; a set member's Y may be None.
     Returns the ctypes array (which keeps the shards alive) and its length."""
     n = len(items)
     arr = (LinearItem * (n or 1))()
@@ -364,9 +369,7 @@ def _items(items):
             arr[i] = it
             continue
         get = it.get
-        sh = it["shard"]
-        if not isinstance(sh, Shard):
-            sh = Shard(*sh.as_tuple())
+        sh = _shard(it["shard"])
         keep.append(sh)
         arr[i] = LinearItem(ctypes.pointer(sh), _ptr(it["packed"]), it["packed_bytes"],
                             _ptr(it["X"]), it["ldx"], _ptr(get("Y")), get("ldy", 0),
@@ -473,7 +476,8 @@ def shard_linear_group_epilogue(items, epilogues, wdtype, xdtype, M, workspace=N
 
 def _gated(items):
     """items: sequence of dicts (or GatedItem) with the tsl_gated_item fields
-    (hdtype defaults to F32, rows to 0, G, U and row_index to None)."""
+    (gate and up as _shard; hdtype defaults to F32, rows to 0, G, U and
+    row_index to None)."""
     n = len(items)
     arr = (GatedItem * (n or 1))()
     keep = []
@@ -481,7 +485,7 @@ def _gated(items):
         if isinstance(it, GatedItem):
             arr[i] = it
             continue
-        get, g, u = it.get, it["gate"], it["up"]
+        get, g, u = it.get, _shard(it["gate"]), _shard(it["up"])
         keep += [g, u]
         arr[i] = GatedItem(ctypes.pointer(g), ctypes.pointer(u), _ptr(it["packed_gate"]),
                            _ptr(it["packed_up"]), it["packed_bytes"], _ptr(it["X"]), it["ldx"],
@@ -507,14 +511,14 @@ def shard_gated_group(items, act, wdtype, xdtype, M, workspace=None, ws_bytes=0,
 
 
 def transpose_shard(shard):
-    out = Shard()
-    _check(_block.transpose_shard(ctypes.byref(shard), ctypes.byref(out)), "transpose_shard")
+    sh, out = _shard(shard), Shard()
+    _check(_block.transpose_shard(ctypes.byref(sh), ctypes.byref(out)), "transpose_shard")
     return out
 
 
 def shard_linear_grad_workspace_size(shard, wdtype, M):
-    b = _sz(0)
-    _check(_block.shard_linear_grad_workspace_size(ctypes.byref(shard), wdtype, M, ctypes.byref(b)),
+    sh, b = _shard(shard), _sz(0)
+    _check(_block.shard_linear_grad_workspace_size(ctypes.byref(sh), wdtype, M, ctypes.byref(b)),
            "shard_linear_grad_workspace_size")
     return b.value
 
@@ -522,7 +526,8 @@ def shard_linear_grad_workspace_size(shard, wdtype, M):
 def shard_linear_grad(shard, wdtype, packed_t, packed_t_bytes, M, X, ldx, act, Z, ldz, dY, lddy,
                       dxdtype, dX, lddx, dwdtype, dW, dw_stride_k, dw_stride_n, accumulate_dw=0,
                       db=None, workspace=None, ws_bytes=0, stream=None):
-    _check(_block.shard_linear_grad(ctypes.byref(shard), wdtype, _ptr(packed_t), packed_t_bytes, M,
+    sh = _shard(shard)
+    _check(_block.shard_linear_grad(ctypes.byref(sh), wdtype, _ptr(packed_t), packed_t_bytes, M,
                                     _ptr(X), ldx, act, _ptr(Z), ldz, _ptr(dY), lddy, dxdtype,
                                     _ptr(dX), lddx, dwdtype, _ptr(dW), dw_stride_k, dw_stride_n,
                                     accumulate_dw, _ptr(db), _ptr(workspace), ws_bytes,
@@ -530,8 +535,8 @@ def shard_linear_grad(shard, wdtype, packed_t, packed_t_bytes, M, X, ldx, act, Z
 
 
 def shard_gated_grad_workspace_size(gate, up, wdtype, M):
-    b = _sz(0)
-    _check(_block.shard_gated_grad_workspace_size(ctypes.byref(gate), ctypes.byref(up), wdtype, M,
+    g, u, b = _shard(gate), _shard(up), _sz(0)
+    _check(_block.shard_gated_grad_workspace_size(ctypes.byref(g), ctypes.byref(u), wdtype, M,
                                                   ctypes.byref(b)),
            "shard_gated_grad_workspace_size")
     return b.value
@@ -540,7 +545,8 @@ def shard_gated_grad_workspace_size(gate, up, wdtype, M):
 def shard_gated_grad(gate, up, wdtype, packed_gate_t, packed_up_t, packed_t_bytes, M, X, ldx, act, G,
                      U, ld_gu, dH, lddh, dxdtype, dX, lddx, dwdtype, dW_gate, dW_up, dw_stride_k,
                      dw_stride_n, accumulate_dw=0, workspace=None, ws_bytes=0, stream=None):
-    _check(_block.shard_gated_grad(ctypes.byref(gate), ctypes.byref(up), wdtype, _ptr(packed_gate_t),
+    g, u = _shard(gate), _shard(up)
+    _check(_block.shard_gated_grad(ctypes.byref(g), ctypes.byref(u), wdtype, _ptr(packed_gate_t),
                                    _ptr(packed_up_t), packed_t_bytes, M, _ptr(X), ldx, act, _ptr(G),
                                    _ptr(U), ld_gu, _ptr(dH), lddh, dxdtype, _ptr(dX), lddx, dwdtype,
                                    _ptr(dW_gate), _ptr(dW_up), dw_stride_k, dw_stride_n,
