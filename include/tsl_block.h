@@ -158,9 +158,9 @@ tsl_status shard_linear_group_epilogue_workspace_size(int32_t n_items,
  *              are added in binary32 over the members' k-ranges in item
  *              order; equal calls give equal bits, but not those of separate
  *              products added afterwards.
- * accumulate must be 0 for an item with an epilogue.  No output (Y, pre) may
- * share an element with another output or with any X, bias or residual
- * (except a residual that is its own item's Y).
+ * accumulate must be 0 for an item with an epilogue; ld_res and ld_pre are
+ * below 2^31.  No output (Y, pre) may share an element with another output or
+ * with any X, bias or residual (except a residual that is its own item's Y).
  */
 tsl_status shard_linear_group_epilogue(int32_t n_items, const tsl_linear_item *items,
                                        const tsl_epilogue *const *epilogues, tsl_dtype wdtype,
@@ -179,7 +179,8 @@ tsl_status shard_linear_group_epilogue(int32_t n_items, const tsl_linear_item *i
  * (F32 or BF16), formed in binary32 from the two products and rounded once.
  * G, U: null, or DEVICE [rows][n_len], row stride ld_gu, type hdtype: receive
  * X W_gate and X W_up (rounded once) for the backward pass; either both or
- * none.
+ * none, ld_gu below 2^31.  They have H's type, and shard_gated_grad reads the
+ * weights': keep them from a call whose hdtype is the weights' type.
  */
 typedef struct tsl_gated_item {
     const tsl_shard *gate, *up;
@@ -259,9 +260,11 @@ tsl_status shard_linear_grad_workspace_size(const tsl_shard *shard, tsl_dtype wd
  * rounded once to wdtype (BF16 and M * n_len up to 2^16: together with what
  * that rounding left, so that it does not show; an infinity in X or the weight
  * may then give NaN).  Slope of relu at 0 is 0.  M == 0 writes zero
- * weight and bias gradients (unless they accumulate).  M, k_len, n_len and
- * input strides below 2^22.  No output may share an element with an input,
- * another output or the workspace.  Errors as shard_linear.
+ * weight and bias gradients (unless they accumulate).  M, k_len and n_len
+ * below 2^22 - 64, the product of any two of them at most 2^34 (F32: 2^32);
+ * input strides below 2^22, output strides below 2^31.  No output may share an
+ * element with an input, another output or the workspace.  Errors as
+ * shard_linear.
  */
 tsl_status shard_linear_grad(const tsl_shard *shard, tsl_dtype wdtype, const void *packed_t,
                              size_t packed_t_bytes, int64_t M, const void *X, int64_t ldx,

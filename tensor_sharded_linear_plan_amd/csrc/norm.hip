@@ -11,9 +11,11 @@
 // to its only write, so every input is read once and every output written
 // once.  A row's threads are one wave up to 512 columns (four rows share a
 // workgroup), a workgroup of four waves up to 8192 (backward, three operands
-// a row: up to 4096, eight waves up to 8192) and of sixteen up to 32768.  All
-// sums are binary32.  Measured, forward, four partials and a residual to e4m3,
-// 2048 x 5120: 52 us, 221 MB, 4.3 TB/s, where a copy reaches 4.9.
+// a row: up to 4096, eight waves up to 8192) and of sixteen up to 32768 -- where
+// the backward pass does not fit: see norm_grad_kernel.  All sums are binary32.
+// Measured, forward, four partials and a residual to e4m3, 2048 x 5120: 52 us,
+// 221 MB, 4.3 TB/s, where a copy reaches 4.9; 2048 x 16384, one bf16 part, 59 us,
+// 4.0 TB/s.
 #include "device.hpp"
 #include "internal.hpp"
 #include "rows.hpp"
@@ -226,7 +228,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(NormArgs a)
 // column_sum_kernel adds in order.  Aligned bf16 rows (RAW) are loaded one
 // row ahead, as they lie: a row's loads are in flight over the reduction of
 // the row before (8192 x 4096, 268 MB: 110 -> 61 us with
-// the sums, 4.4 TB/s).
+// the sums, 4.4 TB/s; 1024 x 8192 20.7 us, 3.2 TB/s).  Above 8192 columns a
+// thread's 16 or 32 columns of a row and of the weight gradient pass the 128
+// registers that sixteen waves leave it: 100 to 110 of them spill up to 16384
+// columns, 236 to 258 up to 32768, and the pass is bound by that traffic (1024 x
+// 16384 74 us, 1.8 TB/s; 1024 x 32768 219 us, 1.2 TB/s).
 
 // The runs of 8 of a row, still in bf16.
 template <int NV>
@@ -273,8 +279,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel(NormGr
     const int64_t g = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; // row group
     const int64_t n = a.n;
     // The weight stays in registers except at the widest rows, which read it
-    // again (from the cache) where they use it, and dres late, so that 1024
-    // threads' registers hold the row.
+    // again (from the cache) where they use it, and dres late, so that fewer of
+    // the 1024 threads' registers spill.
     constexpr bool WIDE = TPR > 512;
     f32x8 w[WIDE ? 1 : NV], dw[NV];
     auto weight = [&](int v) __attribute__((always_inline)) {
