@@ -408,23 +408,25 @@ int wave_count(int64_t tiles, int64_t M) {
 // 4-bit lone T 592: M 16 15.1 / 14.9 us, M 32 25.7 / 22.2; T 1184: M 16 22.2 /
 // 18.4; T 1280: M 8 15.0 / 16.6; T 2048: M 6 23.8 / 20.8; gated T 1184: M 16
 // 24.2 / 25.7, M 32 39.7 / 36.9; bf16 lone T 592: M 16 16.5 / 17.9, M 32 25.2
-// / 22.4.  Up to 4 rows of 4-bit weights, whose activations are one load a
-// unit, and up to 64 lone items or sets (of up to 8 members): T <= 1536, and
-// any T (a launch's workgroups countable) from 3 rows on: T 1280: M 1 10.1 /
-// 14.1, M 4 10.2 / 15.8; T 2048: M 1 17.6 / 16.5, M 4 18.6 / 20.9; T 9504: M 4
-// 63.4 / 65.7; experts of 2048 -> 768, rows through an index: 32 of them, M 2
-// 10.1 / 14.7, 64, M 1 17.5 / 15.6, M 4 18.0 / 19.1, 128, M 4 34.3 / 30.4.  A
-// launch closes at 128 members too, but sets gain more than its end costs: 48
-// sets of 4 shards of 192 -> 2048 (two launches), M 4 24.0 / 60.7; 40 of 4,
-// 192 -> 512, M 1 9.8 / 24.5; 64 of 8, 512 -> 256 (four launches), M 4 34.8 /
-// 91.0. From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 / 63, gated
-// 57 / 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles (T 224, K
-// 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 / 15.5). Few
-// tiles of a long k leave a 4-bit wave of more than one row tile a chain of
-// loads that only the split over workgroups shortens: with less than half the
-// chip's waves, up to 8 units a wave (T 46, 106 units over 8 waves, M 42: 39.2
-// / 23.9 us; 64 units, M 24: 17.0 / 15.4; one row tile, 256 units over 16
-// waves, M 1: 16.5 / 21.3).
+// / 22.4.  (The rule does not read k; along others the border lies elsewhere:
+// 4-bit lone T 592, M 16, K 1024 6.3 / 8.5, K 8192 27.6 / 19.0, bf16 7.2 /
+// 10.4 and 38.1 / 36.8.)  Up to 4 rows of 4-bit weights, whose activations are
+// one load a unit, and up to 64 lone items or sets (of up to 8 members): T <=
+// 1536, and any T (a launch's workgroups countable) from 3 rows on: T 1280: M
+// 1 10.1 / 14.1, M 4 10.2 / 15.8; T 2048: M 1 17.6 / 16.5, M 4 18.6 / 20.9; T
+// 9504: M 4 63.4 / 65.7; experts of 2048 -> 768, rows through an index: 32 of
+// them, M 2 10.1 / 14.7, 64, M 1 17.5 / 15.6, M 4 18.0 / 19.1, 128, M 4 34.3 /
+// 30.4.  A launch closes at 128 members too, but sets gain more than its end
+// costs: 48 sets of 4 shards of 192 -> 2048 (two launches), M 4 24.0 / 60.7;
+// 40 of 4, 192 -> 512, M 1 9.8 / 24.5; 64 of 8, 512 -> 256 (four launches), M
+// 4 34.8 / 91.0.  From 33 to 64 rows 4-bit weights always (T 1184: M 48 53 /
+// 63, gated 57 / 78; T 2048: M 48 82 / 75), bf16 only gated pairs of few tiles
+// (T 224, K 4096: M 64 20.8 / 23.1; T 592: 52.9 / 40.8; lone T 256: 20.1 /
+// 15.5).  Few tiles of a long k leave a 4-bit wave of more than one row tile a
+// chain of loads that only the split over workgroups shortens: with less than
+// half the chip's waves, up to 8 units a wave (T 46, 106 units over 8 waves, M
+// 42: 39.2 / 23.9 us; 64 units, M 24: 17.0 / 15.4; one row tile, 256 units
+// over 16 waves, M 1: 16.5 / 21.3).
 bool decode_applies(const std::vector<LinearItem> &items, tsl_dtype wdtype, int64_t M) {
     if (wdtype == TSL_F32 || M > kDecodeRows)
         return false;

@@ -14,7 +14,7 @@
 // a row: up to 4096, eight waves up to 8192) and of sixteen up to 32768 -- where
 // the backward pass does not fit: see norm_grad_kernel.  All sums are binary32.
 // Measured, forward, four partials and a residual to e4m3, 2048 x 5120: 52 us,
-// 221 MB, 4.3 TB/s, where a copy reaches 4.9; 2048 x 16384, one bf16 part, 59 us,
+// 221 MB, 4.2 TB/s, where a copy reaches 4.9; 2048 x 16384, one bf16 part, 59 us,
 // 4.0 TB/s.
 #include "device.hpp"
 #include "internal.hpp"
