@@ -23,14 +23,13 @@
 // the sum.  Products of one weight (4-bit: up to 32 rows) and bf16 pairs of
 // more than 16 rows hold a second unit, whose loads are in flight while the
 // first is computed; the other pairs and 4-bit calls of more rows load the
-// next unit once the one before is in the matrix cores, and their other waves
-// fill the gap (what bounds the one-row pair below).  Most of those loads are
-// activations (16 rows of 32 k are 1 KB, as the weights of 128 k), so calls of
-// up to 8 rows pack several k-slices into one operand (RG below).  Measured:
-// one rank's 4-bit gate and up, 1 row, 3584 -> 2 x 4736 (19 MB), 8.2 us; 4
-// ranks' down shards, 4 rows, 18944 -> 3584 (38 MB), 14.5 us with whole
-// operands, 11.5 with packed ones (3.3 TB/s; with whole ones and a separate
-// launch for the k-partials 19.0).
+// next unit once the one before is in the matrix cores, and the SIMD's other
+// waves fill the gap.  Most of those loads are activations (16 rows of 32 k
+// are 1 KB, as the weights of 128 k), so calls of up to 8 rows pack several
+// k-slices into one operand (RG below).  Measured: one rank's 4-bit gate and
+// up, 1 row, 3584 -> 2 x 4736 (19 MB), 8.2 us; 4 ranks' down shards, 4 rows,
+// 18944 -> 3584 (38 MB), 14.5 us with whole operands, 11.5 with packed ones
+// (3.3 TB/s; with whole ones and a separate launch for the k-partials 19.0).
 #include <hip/hip_runtime.h>
 
 #include "device.hpp"
@@ -293,13 +292,11 @@ __global__ void __launch_bounds__(MT == 1 ? 1024 : 512) decode_kernel(Group grp)
         };
         Regs g0, g1;
         load(g0);
-        // One unit at a time where a second one's registers spill (4-bit: pairs
-        // of 5 to 16 rows, three or four row tiles of pairs, four of one
-        // weight), and in their neighbours, which hold one without spilling
-        // (pairs of up to 4 rows 110 registers of 128, 4-bit pairs of two row
-        // tiles 217 and three tiles of one weight 236 of 256, bf16 pairs of one
-        // row tile 91 of 128) but were measured only where it spills (one-row
-        // pair with whole operands: 14.6 us one at a time, 23.7 two).
+        // One unit at a time where a second one's registers spill or leave a SIMD
+        // fewer waves, whose loads overlap as well (one at a time / two, 3584 ->
+        // 2 x 4736, 4-bit: M 1 8.3 / 8.7 us, 77 and 110 registers; M 8 9.7 / 10.2,
+        // spills; M 32 19.8 / 22.0; one weight, M 48 24.8 / 26.3; bf16 pairs, M 1
+        // 16.2 / 15.8)
         if constexpr (MT == 1 ? DUAL : Q4 && MT * NT > 2) {
             for (int u = u0 + 1; u < u1; ++u) {
                 compute(g0);
