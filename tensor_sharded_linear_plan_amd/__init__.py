@@ -1,8 +1,8 @@
 """One rank's share of tensor-parallel linear layers on one MI355X.
 
-The compute lives in ``libtsl.so`` and ``libtsl_block.so`` (hand-written HIP
-kernels for gfx950 behind the C ABIs of ``include/tsl.h`` and
-``include/tsl_block.h``).  ``binding`` is a thin ctypes layer over them with
+The compute lives in ``libtsl.so``, ``libtsl_block.so`` and ``libtsl_attn.so``
+(hand-written HIP kernels for gfx950 behind the C ABIs of ``include/tsl.h``,
+``include/tsl_block.h`` and ``include/tsl_attn.h``).  ``binding`` is a thin ctypes layer over them with
 the same entry-point names; it raises ImportError when one has not been
 built -- there is no fallback.
 

@@ -1,6 +1,6 @@
-"""ctypes binding of libtsl.so and libtsl_block.so -- the entry points of
-include/tsl.h and include/tsl_block.h under the same names, argument
-marshalling only.  Every step of the compute runs in the libraries' HIP
+"""ctypes binding of libtsl.so, libtsl_block.so and libtsl_attn.so -- the entry
+points of include/tsl.h, include/tsl_block.h and include/tsl_attn.h under the
+same names, argument marshalling only.  Every step of the compute runs in the libraries' HIP
 kernels; nothing here computes.
 
 Pointer arguments take either an integer device address or any object with
@@ -8,7 +8,7 @@ a ``data_ptr()`` method (a torch tensor).  ``stream=None`` means the current
 torch stream when torch has a GPU, else the null stream.  A non-OK status
 raises TslError carrying the status code.
 
-Importing this module loads both libraries; when one has not been built the
+Importing this module loads the libraries; when one has not been built the
 import fails with ImportError -- there is no fallback path.
 
 PyTorch wheels for ROCm carry their own HIP runtime, which torch's libraries
@@ -39,6 +39,11 @@ if not os.path.exists(BLOCK_LIBRARY):
     raise ImportError("libtsl_block.so is not built: run __graft_entry__.build() or "
                       "python tensor_sharded_linear_plan_amd/build.py")
 _block = ctypes.CDLL(BLOCK_LIBRARY)
+ATTN_LIBRARY = os.path.join(_PKG, "libtsl_attn.so")
+if not os.path.exists(ATTN_LIBRARY):
+    raise ImportError("libtsl_attn.so is not built: run __graft_entry__.build() or "
+                      "python tensor_sharded_linear_plan_amd/build.py")
+_attn = ctypes.CDLL(ATTN_LIBRARY)
 
 # ---- enums (include/tsl.h) ----
 OK = 0
@@ -57,6 +62,7 @@ EMBED, LM_HEAD = 8, 9
 F32, BF16, Q4G64, E4M3 = 0, 1, 2, 3
 ALL_REDUCE, REDUCE_SCATTER, ALL_GATHER = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+ROTARY_HALVES, ROTARY_PAIRS = 0, 1
 MAX_PARTS = 64
 
 
@@ -66,6 +72,7 @@ class TslError(RuntimeError):
         msg = _lib.tsl_status_string(status).decode()
         if status == ERR_HIP:
             last = _block.tsl_block_last_hip_error_string if where in BLOCK_EXPORTS else \
+                _attn.tsl_attn_last_hip_error_string if where in ATTN_EXPORTS else \
                 _lib.tsl_last_hip_error_string
             msg += " [%s]" % last().decode()
         super().__init__("%s: %s (%d)" % (where, msg, status))
@@ -129,6 +136,38 @@ class GatedItem(ctypes.Structure):
                 ("G", ctypes.c_void_p), ("U", ctypes.c_void_p), ("ld_gu", ctypes.c_int64),
                 ("row_index", ctypes.c_void_p), ("x_rows", ctypes.c_int64),
                 ("hdtype", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
+class Rotary(ctypes.Structure):
+    """Positions and frequencies of rotate_heads (tsl_rotary)."""
+    _fields_ = [("positions", ctypes.c_void_p), ("ld_pos", ctypes.c_int64),
+                ("freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("style", ctypes.c_int32)]
+
+
+class RotateItem(ctypes.Structure):
+    """One operand of rotate_heads (tsl_rotate_item)."""
+    _fields_ = [("X", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_head", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("xdtype", ctypes.c_int32),
+                ("ydtype", ctypes.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    """A paged 4-bit cache of keys and values (tsl_cache)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class Seqs(ctypes.Structure):
+    """The sequences of a cache call (tsl_seqs)."""
+    _fields_ = [("row_start", ctypes.c_void_p), ("context", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_context", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
@@ -219,6 +258,27 @@ BLOCK_EXPORTS = ("add_rms_norm", "add_rms_norm_grad_workspace_size", "add_rms_no
                  "tsl_block_last_hip_error_string")
 for _f in BLOCK_EXPORTS[:-1]:
     getattr(_block, _f).restype = ctypes.c_int
+
+_P_CACHE, _P_SEQS = ctypes.POINTER(Cache), ctypes.POINTER(Seqs)
+_attn.rotate_heads.argtypes = [_i32, ctypes.POINTER(RotateItem), _i64, ctypes.POINTER(Rotary),
+                               ctypes.c_int, _vp]
+_attn.cache_size.argtypes = [_P_CACHE, ctypes.POINTER(_sz)]
+for _f in ("cache_append", "cache_read"):
+    getattr(_attn, _f).argtypes = [_P_CACHE, _P_SEQS, ctypes.c_int, _vp, _i64, _i64, _vp, _i64, _i64,
+                                   _vp]
+_attn.cache_attention_workspace_size.argtypes = [_P_CACHE, _P_SEQS, _i32, _i32, _i32,
+                                                 ctypes.POINTER(_sz)]
+_attn.cache_attention.argtypes = [_P_CACHE, _P_SEQS, _i32, _vp, _i64, _i64, ctypes.c_float, _i32,
+                                  _i32, ctypes.c_int, _vp, _i64, _i64, _vp, _sz, _vp]
+_attn.tsl_attn_last_hip_error_string.argtypes = []
+_attn.tsl_attn_last_hip_error_string.restype = ctypes.c_char_p
+
+# the entry points of include/tsl_attn.h
+ATTN_EXPORTS = ("rotate_heads", "cache_size", "cache_append", "cache_read",
+                "cache_attention_workspace_size", "cache_attention",
+                "tsl_attn_last_hip_error_string")
+for _f in ATTN_EXPORTS[:-1]:
+    getattr(_attn, _f).restype = ctypes.c_int
 
 
 def _check(status, where):
@@ -552,3 +612,79 @@ def shard_gated_grad(gate, up, wdtype, packed_gate_t, packed_up_t, packed_t_byte
                                    _ptr(dW_gate), _ptr(dW_up), dw_stride_k, dw_stride_n,
                                    accumulate_dw, _ptr(workspace), ws_bytes, _stream(stream)),
            "shard_gated_grad")
+
+
+def _rotary(r):
+    """r: a dict (or Rotary) with the tsl_rotary fields; pair_axis a sequence of
+    axes or None (style defaults to ROTARY_HALVES, axes to 1, ld_pos to 0)."""
+    if isinstance(r, Rotary):
+        return r
+    axis = r.get("pair_axis")
+    if axis is not None:
+        if len(axis) != r["rot_dim"] // 2:
+            raise ValueError("one axis per pair")
+        axis = (ctypes.c_uint8 * max(len(axis), 1))(*axis)
+    out = Rotary(_ptr(r["positions"]), r.get("ld_pos", 0), _ptr(r["freq"]),
+                 ctypes.cast(axis, ctypes.c_void_p) if axis is not None else None,
+                 r.get("axes", 1), r["rot_dim"], r["head_dim"], r.get("style", ROTARY_HALVES))
+    out._keep = axis
+    return out
+
+
+def rotate_heads(items, M, rotary, inverse=0, stream=None):
+    """items: sequence of dicts (or RotateItem) with the tsl_rotate_item fields."""
+    n = len(items)
+    arr = (RotateItem * max(n, 1))()
+    for i, it in enumerate(items):
+        arr[i] = it if isinstance(it, RotateItem) else \
+            RotateItem(_ptr(it["X"]), it["ldx"], it["x_head"], _ptr(it["Y"]), it["ldy"],
+                       it["y_head"], it["n_heads"], it["xdtype"], it["ydtype"])
+    r = _rotary(rotary)
+    _check(_attn.rotate_heads(n, arr, M, ctypes.byref(r), inverse, _stream(stream)), "rotate_heads")
+
+
+def _cache(c):
+    """c: a dict (or Cache) with the tsl_cache fields."""
+    return c if isinstance(c, Cache) else Cache(_ptr(c.get("pages")), c["n_pages"], c["page_tokens"],
+                                                c["n_kv_heads"], c["head_dim"])
+
+
+def _seqs(q):
+    """q: a dict (or Seqs) with the tsl_seqs fields (the arrays default to
+    None, for size queries)."""
+    return q if isinstance(q, Seqs) else Seqs(_ptr(q.get("row_start")), _ptr(q.get("context")),
+                                              _ptr(q.get("page_table")), q.get("ld_table", 0),
+                                              q["rows"], q["n_seqs"], q["max_rows"],
+                                              q["max_context"], q["max_pages"])
+
+
+def cache_size(cache):
+    b = _sz(0)
+    _check(_attn.cache_size(ctypes.byref(_cache(cache)), ctypes.byref(b)), "cache_size")
+    return b.value
+
+
+def cache_append(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, stream=None):
+    _check(_attn.cache_append(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), dtype, _ptr(K),
+                              ldk, k_head, _ptr(V), ldv, v_head, _stream(stream)), "cache_append")
+
+
+def cache_read(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, stream=None):
+    _check(_attn.cache_read(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), dtype, _ptr(K),
+                            ldk, k_head, _ptr(V), ldv, v_head, _stream(stream)), "cache_read")
+
+
+def cache_attention_workspace_size(cache, seqs, n_q_heads, window=0, sinks=0):
+    b = _sz(0)
+    _check(_attn.cache_attention_workspace_size(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)),
+                                                n_q_heads, window, sinks, ctypes.byref(b)),
+           "cache_attention_workspace_size")
+    return b.value
+
+
+def cache_attention(cache, seqs, n_q_heads, Q, ldq, q_head, scale, window, sinks, odtype, O, ldo,
+                    o_head, workspace=None, ws_bytes=0, stream=None):
+    _check(_attn.cache_attention(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), n_q_heads,
+                                 _ptr(Q), ldq, q_head, scale, window, sinks, odtype, _ptr(O), ldo,
+                                 o_head, _ptr(workspace), ws_bytes, _stream(stream)),
+           "cache_attention")

@@ -1,9 +1,10 @@
-"""Build libtsl.so and libtsl_block.so: the gfx950 HIP kernels and their C
-ABIs, in-tree.
+"""Build libtsl.so, libtsl_block.so and libtsl_attn.so: the gfx950 HIP kernels
+and their C ABIs, in-tree.
 
 libtsl.so is the shard products and joins of include/tsl.h; libtsl_block.so
 the layer-block operators of include/tsl_block.h, whose products are the same
-GEMM and streaming sources compiled with an epilogue (TSL_EPILOGUE=1).
+GEMM and streaming sources compiled with an epilogue (TSL_EPILOGUE=1);
+libtsl_attn.so the attention operators of include/tsl_attn.h.
 
 Every translation unit is compiled by hipcc for gfx950 only; packed FP32
 instructions are switched off for the device code (they are never needed
@@ -24,12 +25,14 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libtsl.so")
 BLOCK_LIBRARY = os.path.join(PKG, "libtsl_block.so")
+ATTN_LIBRARY = os.path.join(PKG, "libtsl_attn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["abi.cpp", "plan.cpp", "pack.hip", "combine.hip", "embed.hip", "moe.hip", "skinny.hip", "prefill.hip", "q4gemm.hip",
            "noalloc.hip"]
 BLOCK_SOURCES = ["block.cpp", "norm.hip", "grad.hip", "decode.hip", "combine.hip", "skinny.hip",
                  "prefill.hip", "q4gemm.hip"]
+ATTN_SOURCES = ["attn.cpp", "rotary.hip", "kvcache.hip", "attend.hip"]
 BLOCK_FLAGS = ["-DTSL_EPILOGUE=1"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-mcode-object-version=5", "-Wall",
          # only the C ABI of include/tsl.h is exported (it sets default visibility)
@@ -80,9 +83,10 @@ def _link(library, header, objs):
 
 
 def build(verbose=False, jobs=None):
-    """Compile all sources and link both libraries; returns libtsl.so's path."""
+    """Compile all sources and link the libraries; returns libtsl.so's path."""
     os.makedirs(OBJDIR, exist_ok=True)
-    todo = [(s, "", []) for s in SOURCES] + [(s, "_block", BLOCK_FLAGS) for s in BLOCK_SOURCES]
+    todo = [(s, "", []) for s in SOURCES] + [(s, "_block", BLOCK_FLAGS) for s in BLOCK_SOURCES] + \
+        [(s, "", []) for s in ATTN_SOURCES]
     jobs = jobs or min(len(todo), int(os.environ.get("MAX_JOBS", "8")))
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
         results = list(ex.map(_compile, todo))
@@ -92,7 +96,9 @@ def build(verbose=False, jobs=None):
                 print(err, file=sys.stderr)
     objs = [o for o, _ in results]
     _link(LIBRARY, "tsl.h", objs[:len(SOURCES)])
-    _link(BLOCK_LIBRARY, "tsl_block.h", objs[len(SOURCES):])
+    block = len(SOURCES) + len(BLOCK_SOURCES)
+    _link(BLOCK_LIBRARY, "tsl_block.h", objs[len(SOURCES):block])
+    _link(ATTN_LIBRARY, "tsl_attn.h", objs[block:])
     return LIBRARY
 
 

@@ -1,0 +1,423 @@
+// The C ABI of tsl_attn.h.  Checks run before anything is enqueued; no exception leaves an
+// entry point.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <cstddef>
+
+#include "attn.hpp"
+#include "group.hpp"
+#include "tsl_attn.h"
+
+using namespace tsl;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 22;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokens = int64_t(1) << 30; // of a page table's row
+constexpr int kMaxSeqs = 65535;
+constexpr int kMaxHeads = 1024;
+
+bool dense_type(int d) { return d == TSL_F32 || d == TSL_BF16; }
+size_t elem(int d) { return d == TSL_F32 ? 4 : 2; }
+
+// A [rows][heads][cols] operand (tsl_attn.h, "Heads").
+struct Heads {
+    const void *p;
+    int64_t rows, heads, cols, ld, head;
+    size_t e;
+
+    // strides that keep its elements apart, in either nesting
+    bool sound() const {
+        if (ld >= kMaxStride || head >= kMaxStride)
+            return false;
+        if (rows <= 1 && heads <= 1)
+            return true;
+        if (rows <= 1)
+            return head >= cols;
+        if (heads <= 1)
+            return ld >= cols;
+        return (head >= cols && ld >= (heads - 1) * head + cols) ||
+               (ld >= cols && head >= (rows - 1) * ld + cols);
+    }
+    size_t bytes() const {
+        return (size_t)((rows - 1) * ld + (heads - 1) * head + cols) * e;
+    }
+    bool wide() const { // 16-byte aligned runs throughout
+        const int64_t run = 16 / (int64_t)e;
+        return aligned(p, 16) && (rows <= 1 || ld % run == 0) && (heads <= 1 || head % run == 0);
+    }
+};
+
+// Whether two operands share a byte: their spans, and where those meet (slices
+// of one array) the rows of each pair of heads.
+bool clash(const Heads &a, const Heads &b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || !overlaps(a.p, a.bytes(), b.p, b.bytes()))
+        return false;
+    // a lone row's stride says nothing
+    const int64_t la = a.rows > 1 ? a.ld : a.cols, lb = b.rows > 1 ? b.ld : b.cols;
+    for (int64_t i = 0; i < a.heads; ++i)
+        for (int64_t j = 0; j < b.heads; ++j)
+            if (matrices_overlap(static_cast<const char *>(a.p) + i * a.head * (int64_t)a.e, a.rows,
+                                 a.cols, la, a.e,
+                                 static_cast<const char *>(b.p) + j * b.head * (int64_t)b.e, b.rows,
+                                 b.cols, lb, b.e))
+                return true;
+    return false;
+}
+
+tsl_status cache_check(const tsl_cache *c, bool with_pages) {
+    if (!c || c->n_pages < 1 || c->page_tokens < 1 || c->n_kv_heads < 1 || c->head_dim < 1 ||
+        (with_pages && !c->pages))
+        return TSL_ERR_INVALID_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) ||
+        c->page_tokens < kBlock || c->page_tokens > 4096 ||
+        (c->page_tokens & (c->page_tokens - 1)) || c->n_kv_heads > kMaxHeads ||
+        c->n_pages > INT32_MAX)
+        return TSL_ERR_UNSUPPORTED;
+    if (with_pages && !aligned(c->pages, 256))
+        return TSL_ERR_MISALIGNED;
+    return TSL_OK;
+}
+
+size_t page_size(const tsl_cache &c) {
+    return (size_t)c.n_kv_heads * (size_t)(c.page_tokens / kBlock) * record_bytes(c.head_dim);
+}
+
+tsl_status seqs_check(const tsl_cache &c, const tsl_seqs *q, bool with_arrays) {
+    if (!q || q->n_seqs < 0 || q->rows < 0 || q->max_rows < 0 || q->max_context < 0 ||
+        q->max_pages < 0)
+        return TSL_ERR_INVALID_ARG;
+    if (with_arrays && q->n_seqs > 0) {
+        if (!q->row_start || !q->context || (q->max_pages > 0 && !q->page_table))
+            return TSL_ERR_INVALID_ARG;
+        if (q->n_seqs > 1 && q->ld_table < q->max_pages)
+            return TSL_ERR_INVALID_ARG;
+    }
+    if (q->n_seqs > kMaxSeqs || q->rows >= kMaxRows || q->ld_table >= kMaxStride ||
+        (int64_t)q->max_pages * c.page_tokens > kMaxTokens)
+        return TSL_ERR_UNSUPPORTED;
+    if (with_arrays &&
+        (!aligned(q->row_start, 4) || !aligned(q->context, 4) || !aligned(q->page_table, 4)))
+        return TSL_ERR_MISALIGNED;
+    return TSL_OK;
+}
+
+bool nothing(const tsl_seqs &q) { return q.n_seqs == 0 || q.rows == 0 || q.max_rows == 0; }
+
+CacheArgs cache_args(const tsl_cache &c, const tsl_seqs &q) {
+    CacheArgs a{};
+    a.pages = static_cast<char *>(c.pages);
+    a.page_bytes = (int64_t)page_size(c);
+    a.head_bytes = a.page_bytes / c.n_kv_heads;
+    a.n_pages = (int32_t)c.n_pages;
+    a.shift = 0;
+    while ((kBlock << a.shift) < c.page_tokens)
+        ++a.shift;
+    a.n_kv_heads = c.n_kv_heads;
+    a.row_start = q.row_start;
+    a.context = q.context;
+    a.page_table = q.page_table;
+    a.ld_table = q.n_seqs > 1 ? q.ld_table : 0;
+    a.rows = (int32_t)q.rows;
+    a.n_seqs = q.n_seqs;
+    a.max_rows = (int32_t)std::min<int64_t>(q.max_rows, q.rows);
+    a.max_pages = q.max_pages;
+    return a;
+}
+
+// Whether an operand of the caller's touches the cache or the arrays that
+// the kernels read.
+bool meets_cache(const Heads &h, const tsl_cache &c, const tsl_seqs &q, bool arrays) {
+    if (!h.p)
+        return false;
+    const size_t pages = page_size(c) * (size_t)c.n_pages;
+    if (overlaps(h.p, h.bytes(), c.pages, pages))
+        return true;
+    if (!arrays)
+        return false;
+    return overlaps(h.p, h.bytes(), q.row_start, 4 * ((size_t)q.n_seqs + 1)) ||
+           overlaps(h.p, h.bytes(), q.context, 4 * (size_t)q.n_seqs) ||
+           (q.max_pages > 0 &&
+            overlaps(h.p, h.bytes(), q.page_table,
+                     4 * ((size_t)(q.n_seqs - 1) * (size_t)(q.n_seqs > 1 ? q.ld_table : 0) +
+                          (size_t)q.max_pages)));
+}
+
+// Checks and arguments that cache_append and cache_read share.
+tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dtype, const void *K,
+                     int64_t ldk, int64_t k_head, const void *V, int64_t ldv, int64_t v_head,
+                     bool read, MoveArgs *out) {
+    tsl_status st = cache_check(cache, true);
+    if (st != TSL_OK)
+        return st;
+    if ((st = seqs_check(*cache, seqs, true)) != TSL_OK)
+        return st;
+    if (!dense_type(dtype) || (read ? !K && !V : !K || !V))
+        return TSL_ERR_INVALID_ARG;
+    const size_t e = elem(dtype);
+    const Heads k = {K, seqs->rows, cache->n_kv_heads, cache->head_dim, ldk, k_head, e};
+    const Heads v = {V, seqs->rows, cache->n_kv_heads, cache->head_dim, ldv, v_head, e};
+    for (const Heads *h : {&k, &v}) {
+        if (!h->p)
+            continue;
+        if (h->ld < 0 || h->head < 0 || !h->sound())
+            return TSL_ERR_INVALID_ARG;
+        if (!h->wide())
+            return TSL_ERR_MISALIGNED;
+    }
+    MoveArgs a{};
+    a.c = cache_args(*cache, *seqs);
+    // a run of n rows touches at most so many records, wherever it starts
+    a.seq_blocks = a.c.max_rows > 0 ? (a.c.max_rows + kBlock - 2) / kBlock + 1 : 0;
+    if ((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks > kMaxBlocks)
+        return TSL_ERR_UNSUPPORTED;
+    if (!nothing(*seqs) &&
+        (meets_cache(k, *cache, *seqs, read) || meets_cache(v, *cache, *seqs, read) ||
+         (read && clash(k, v))))
+        return TSL_ERR_INVALID_ARG;
+    a.K = const_cast<void *>(K);
+    a.V = const_cast<void *>(V);
+    a.ldk = ldk;
+    a.k_head = k_head;
+    a.ldv = ldv;
+    a.v_head = v_head;
+    a.bf16 = dtype == TSL_BF16;
+    *out = a;
+    return TSL_OK;
+}
+
+// How cache_attention divides its work; a function of sizes alone.
+struct AttendPlan {
+    int32_t tiles, splits, min_share;
+    size_t bytes;
+};
+
+// Workgroups that a call of few rows is divided into at least, where its
+// tokens allow it: three for each of the 256 CUs.
+constexpr int64_t kAttendUnits = 768;
+// Records that are worth a range of their own: two for each wave.
+constexpr int kAttendShare = 8;
+
+tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
+                       int32_t sinks, AttendPlan *p) {
+    const int64_t group = n_q_heads / c.n_kv_heads;
+    const int64_t max_rows = std::min<int64_t>(q.max_rows, q.rows);
+    int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
+    if (window)
+        seen = std::min<int64_t>(seen, (int64_t)window + sinks + kTileRows + 2 * kBlock);
+    const int64_t records = (seen + kBlock - 1) / kBlock;
+    p->tiles = (int32_t)((max_rows * group + kTileRows - 1) / kTileRows);
+    const int64_t units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
+    int64_t splits = units > 0 ? (kAttendUnits + units - 1) / units : 1;
+    splits = std::max<int64_t>(1, std::min(splits, (records + kAttendShare - 1) / kAttendShare));
+    p->splits = (int32_t)splits;
+    p->min_share = kAttendShare;
+    if (units * splits > kMaxBlocks || units * (kTileRows / 4) > kMaxBlocks)
+        return TSL_ERR_UNSUPPORTED;
+    p->bytes = splits > 1 ? (size_t)(units * splits) * kTileRows * (size_t)(c.head_dim + 2) * 4 : 0;
+    return TSL_OK;
+}
+
+tsl_status attend_check(const tsl_cache *cache, const tsl_seqs *seqs, int32_t n_q_heads,
+                        int32_t window, int32_t sinks, bool run) {
+    tsl_status st = cache_check(cache, run);
+    if (st != TSL_OK)
+        return st;
+    if ((st = seqs_check(*cache, seqs, run)) != TSL_OK)
+        return st;
+    if (n_q_heads < 1 || window < 0 || sinks < 0)
+        return TSL_ERR_INVALID_ARG;
+    if (n_q_heads % cache->n_kv_heads)
+        return TSL_ERR_NOT_DIVISIBLE;
+    if (n_q_heads > kMaxHeads || window > kMaxContext || sinks > kMaxContext)
+        return TSL_ERR_UNSUPPORTED;
+    return TSL_OK;
+}
+
+} // namespace
+
+extern "C" tsl_status rotate_heads(int32_t n_items, const tsl_rotate_item *items, int64_t M,
+                                   const tsl_rotary *rotary, int inverse, void *stream) {
+    if (!items || !rotary || n_items < 1 || M < 0 || (inverse != 0 && inverse != 1))
+        return TSL_ERR_INVALID_ARG;
+    const tsl_rotary &r = *rotary;
+    if (!r.positions || !r.freq || r.axes < 1 || r.head_dim < 2 || r.rot_dim < 2 ||
+        r.rot_dim % 2 || r.rot_dim > r.head_dim ||
+        (r.style != TSL_ROTARY_HALVES && r.style != TSL_ROTARY_PAIRS))
+        return TSL_ERR_INVALID_ARG;
+    if (n_items > kMaxRotateItems || r.axes > 4 || r.head_dim > kMaxHeadDim || M >= kMaxRows)
+        return TSL_ERR_UNSUPPORTED;
+    if (r.axes > 1 && (r.ld_pos < M || r.ld_pos >= kMaxStride))
+        return TSL_ERR_INVALID_ARG;
+    if (!aligned(r.positions, 4) || !aligned(r.freq, 4))
+        return TSL_ERR_MISALIGNED;
+    RotateArgs a{};
+    for (int p = 0; p < r.rot_dim / 2 && r.pair_axis; ++p) {
+        if (r.pair_axis[p] >= r.axes)
+            return TSL_ERR_INVALID_ARG;
+        a.axis[p >> 4] |= (uint32_t)r.pair_axis[p] << (2 * (p & 15));
+    }
+    const int half = r.rot_dim / 2;
+    bool wide = r.head_dim % 8 == 0 &&
+                (r.style == TSL_ROTARY_HALVES ? half % 8 == 0 : r.rot_dim % 8 == 0);
+    int64_t heads = 0;
+    Heads x[kMaxRotateItems], y[kMaxRotateItems];
+    for (int i = 0; i < n_items; ++i) {
+        const tsl_rotate_item &it = items[i];
+        if (!it.X || !it.Y || it.n_heads < 1 || !dense_type(it.xdtype) || !dense_type(it.ydtype) ||
+            it.ldx < 0 || it.x_head < 0 || it.ldy < 0 || it.y_head < 0)
+            return TSL_ERR_INVALID_ARG;
+        if (it.n_heads > kMaxHeads)
+            return TSL_ERR_UNSUPPORTED;
+        x[i] = Heads{it.X, M, it.n_heads, r.head_dim, it.ldx, it.x_head, elem(it.xdtype)};
+        y[i] = Heads{it.Y, M, it.n_heads, r.head_dim, it.ldy, it.y_head, elem(it.ydtype)};
+        if (!x[i].sound() || !y[i].sound())
+            return TSL_ERR_INVALID_ARG;
+        if (!aligned(it.X, x[i].e) || !aligned(it.Y, y[i].e))
+            return TSL_ERR_MISALIGNED;
+        wide = wide && x[i].wide() && y[i].wide();
+        heads += it.n_heads;
+        a.item[i] = RotateArgs::Item{it.X,       it.Y,      it.ldx, it.x_head,
+                                     it.ldy,     it.y_head, it.n_heads, it.xdtype == TSL_BF16,
+                                     it.ydtype == TSL_BF16, 0};
+    }
+    if (M == 0)
+        return TSL_OK;
+    const Heads pos = {r.positions, r.axes, 1, M, r.axes > 1 ? r.ld_pos : M, 0, 4};
+    const Heads freq = {r.freq, 1, 1, half, half, 0, 4};
+    for (int i = 0; i < n_items; ++i) {
+        if (clash(y[i], pos) || clash(y[i], freq))
+            return TSL_ERR_INVALID_ARG;
+        for (int j = 0; j < n_items; ++j) {
+            const bool own = i == j && y[i].p == x[i].p && y[i].e == x[i].e &&
+                             (M == 1 || y[i].ld == x[i].ld) &&
+                             (y[i].heads == 1 || y[i].head == x[i].head);
+            if ((!own && clash(y[i], x[j])) || (i < j && clash(y[i], y[j])))
+                return TSL_ERR_INVALID_ARG;
+        }
+    }
+    a.positions = r.positions;
+    a.freq = r.freq;
+    a.ld_pos = r.ld_pos;
+    a.M = M;
+    a.n_items = n_items;
+    a.heads = (int32_t)heads;
+    a.rot_dim = r.rot_dim;
+    a.head_dim = r.head_dim;
+    a.pairs = r.style == TSL_ROTARY_PAIRS;
+    a.inverse = inverse;
+    a.wide = wide;
+    return from_hip(launch_rotate(a, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" tsl_status cache_size(const tsl_cache *cache, size_t *bytes) {
+    if (!bytes)
+        return TSL_ERR_INVALID_ARG;
+    const tsl_status st = cache_check(cache, false);
+    if (st == TSL_OK)
+        *bytes = page_size(*cache) * (size_t)cache->n_pages;
+    return st;
+}
+
+extern "C" tsl_status cache_append(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dtype,
+                                   const void *K, int64_t ldk, int64_t k_head, const void *V,
+                                   int64_t ldv, int64_t v_head, void *stream) {
+    MoveArgs a;
+    const tsl_status st =
+        move_args(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, false, &a);
+    if (st != TSL_OK || nothing(*seqs))
+        return st;
+    return from_hip(launch_cache_append(cache->head_dim, a, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" tsl_status cache_read(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dtype,
+                                 void *K, int64_t ldk, int64_t k_head, void *V, int64_t ldv,
+                                 int64_t v_head, void *stream) {
+    MoveArgs a;
+    const tsl_status st = move_args(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, true, &a);
+    if (st != TSL_OK || nothing(*seqs))
+        return st;
+    return from_hip(launch_cache_read(cache->head_dim, a, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs *seqs,
+                                                     int32_t n_q_heads, int32_t window,
+                                                     int32_t sinks, size_t *bytes) {
+    if (!bytes)
+        return TSL_ERR_INVALID_ARG;
+    tsl_status st = attend_check(cache, seqs, n_q_heads, window, sinks, false);
+    AttendPlan p;
+    if (st == TSL_OK && (st = attend_plan(*cache, *seqs, n_q_heads, window, sinks, &p)) == TSL_OK)
+        *bytes = p.bytes;
+    return st;
+}
+
+extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *seqs,
+                                      int32_t n_q_heads, const void *Q, int64_t ldq, int64_t q_head,
+                                      float scale, int32_t window, int32_t sinks, tsl_dtype odtype,
+                                      void *O, int64_t ldo, int64_t o_head, void *workspace,
+                                      size_t ws_bytes, void *stream) {
+    tsl_status st = attend_check(cache, seqs, n_q_heads, window, sinks, true);
+    if (st != TSL_OK)
+        return st;
+    if (!Q || !O || !dense_type(odtype) || !isfinite(scale) || ldq < 0 || q_head < 0 || ldo < 0 ||
+        o_head < 0)
+        return TSL_ERR_INVALID_ARG;
+    const Heads q = {Q, seqs->rows, n_q_heads, cache->head_dim, ldq, q_head, 2};
+    const Heads o = {O, seqs->rows, n_q_heads, cache->head_dim, ldo, o_head, elem(odtype)};
+    if (!q.sound() || !o.sound())
+        return TSL_ERR_INVALID_ARG;
+    if (!q.wide() || !o.wide())
+        return TSL_ERR_MISALIGNED;
+    AttendPlan p;
+    if ((st = attend_plan(*cache, *seqs, n_q_heads, window, sinks, &p)) != TSL_OK)
+        return st;
+    if (nothing(*seqs))
+        return TSL_OK;
+    if (p.bytes) {
+        if (!workspace || ws_bytes < p.bytes)
+            return TSL_ERR_BUFFER_TOO_SMALL;
+        if (!aligned(workspace, 256))
+            return TSL_ERR_MISALIGNED;
+        const Heads ws = {workspace, 1, 1, (int64_t)p.bytes, (int64_t)p.bytes, 0, 1};
+        if (clash(ws, q) || clash(ws, o) || meets_cache(ws, *cache, *seqs, true))
+            return TSL_ERR_INVALID_ARG;
+    }
+    if (clash(o, q) || meets_cache(o, *cache, *seqs, true))
+        return TSL_ERR_INVALID_ARG;
+    AttendArgs a{};
+    a.c = cache_args(*cache, *seqs);
+    a.Q = static_cast<const uint16_t *>(Q);
+    a.O = O;
+    a.ldq = ldq;
+    a.q_head = q_head;
+    a.ldo = ldo;
+    a.o_head = o_head;
+    a.scale = scale * 1.44269504088896340736f;
+    a.group = n_q_heads / cache->n_kv_heads;
+    a.window = window;
+    a.sinks = sinks;
+    a.o_bf16 = odtype == TSL_BF16;
+    a.tiles = p.tiles;
+    a.splits = p.splits;
+    a.min_share = p.min_share;
+    if (p.bytes) {
+        a.part = static_cast<float *>(workspace);
+        a.part_ml = a.part + (int64_t)a.c.n_seqs * a.c.n_kv_heads * p.tiles * p.splits *
+                                 kTileRows * cache->head_dim;
+    }
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    hipError_t e = launch_attend_decode(cache->head_dim, a, hs);
+    if (e == hipSuccess && p.splits > 1)
+        e = launch_attend_join(cache->head_dim, kTileRows, a, hs);
+    return from_hip(e);
+}
+
+extern "C" const char *tsl_attn_last_hip_error_string(void) {
+    return hipGetErrorString(g_last_hip);
+}

@@ -1,0 +1,166 @@
+// Internal interface between the C ABI of tsl_attn.h (attn.cpp) and its HIP
+// kernels, and what those kernels share on the device: where a token of the
+// cache lies and which tokens a tile of query rows sees.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.hpp"
+#include "tsl_attn.h"
+
+namespace tsl {
+
+constexpr int kMaxRotateItems = 8;
+constexpr int kMaxHeadDim = 512; // of rotate_heads
+
+struct RotateArgs {
+    struct Item {
+        const void *X;
+        void *Y;
+        int64_t ldx, x_head, ldy, y_head;
+        int32_t n_heads, x_bf16, y_bf16, vec;
+    } item[kMaxRotateItems];
+    const int32_t *positions;
+    const float *freq;
+    int64_t ld_pos, M;
+    int32_t n_items, heads; // heads of all items
+    int32_t rot_dim, head_dim, pairs, inverse;
+    int32_t wide; // every item takes the vector form
+    uint32_t axis[kMaxHeadDim / 2 / 16]; // two bits a pair
+};
+
+hipError_t launch_rotate(const RotateArgs &a, hipStream_t stream);
+
+// One record holds kBlock tokens of one head (tsl_attn.h, tsl_cache).
+constexpr int kBlock = 32;
+constexpr int record_bytes(int head_dim) { return 36 * head_dim; }
+
+// Longest context; windows and first tokens are no longer either, so that
+// positions and their differences fit 32 bits.
+constexpr int kMaxContext = 1 << 30;
+
+struct CacheArgs {
+    char *pages;
+    int64_t page_bytes, head_bytes;
+    int32_t n_pages, shift; // records of a page and head: 1 << shift
+    int32_t n_kv_heads;
+    // sequences
+    const int32_t *row_start, *context, *page_table;
+    int64_t ld_table;
+    int32_t rows, n_seqs, max_rows, max_pages;
+};
+
+struct MoveArgs {
+    CacheArgs c;
+    void *K, *V;
+    int64_t ldk, k_head, ldv, v_head;
+    int32_t bf16;
+    int32_t seq_blocks; // records a sequence's rows may span
+};
+
+hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream);
+hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream);
+
+struct AttendArgs {
+    CacheArgs c;
+    const uint16_t *Q;
+    void *O;
+    int64_t ldq, q_head, ldo, o_head;
+    float scale; // times log2 e
+    int32_t group, window, sinks, o_bf16;
+    int32_t tiles;     // row tiles of a sequence and K/V head
+    int32_t splits;    // ranges of tokens a tile is divided into at most
+    int32_t min_share; // records of a range at least
+    float *part;       // [seq][head][tile][split][tile rows][head_dim], splits > 1
+    float *part_ml;    // ... [tile rows][2]: reference exponent and sum
+};
+
+constexpr int kTileRows = 16; // query rows of a tile of attend_decode
+
+hipError_t launch_attend_decode(int head_dim, const AttendArgs &a, hipStream_t stream);
+hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
+
+// ---- where tokens lie and which are seen ------------------------------------------
+// (host code too, for tests without a GPU)
+
+// A sequence's rows, clamped to what the operands have.
+struct SeqRows {
+    int row0, n, ctx;
+};
+__host__ __device__ __forceinline__ SeqRows seq_rows(const CacheArgs &c, int s) {
+    SeqRows r;
+    const int a = c.row_start[s], b = c.row_start[s + 1];
+    r.row0 = a < 0 ? 0 : (a > c.rows ? c.rows : a);
+    const int end = b < r.row0 ? r.row0 : (b > c.rows ? c.rows : b);
+    r.n = end - r.row0;
+    const int ctx = c.context[s];
+    r.ctx = ctx < 0 ? 0 : (ctx > kMaxContext ? kMaxContext : ctx);
+    return r;
+}
+
+// The record of a sequence's tokens 32 blk .. 32 blk + 31 (blk >= 0), or null
+// where they are not there.
+__host__ __device__ __forceinline__ char *record_of(const CacheArgs &c, int s, int head, int blk,
+                                           int rec_bytes) {
+    const int page = blk >> c.shift;
+    if (page >= c.max_pages)
+        return nullptr;
+    const int p = c.page_table[s * c.ld_table + page];
+    if (p < 0 || p >= c.n_pages)
+        return nullptr;
+    return c.pages + p * c.page_bytes + head * c.head_bytes +
+           (int64_t)(blk & ((1 << c.shift) - 1)) * rec_bytes;
+}
+
+// What a tile of query rows sees: positions first .. last (of its rows), and
+// the records that hold a visible token of any row, as a list: `lead` records
+// from 0 on (first tokens that stay visible), then those from `from` on.
+struct TileView {
+    int first, last;
+    int lead, from, count;
+    int share, used; // records of a range, ranges with any
+};
+__host__ __device__ __forceinline__ TileView tile_view(const AttendArgs &a, int first, int last) {
+    TileView v;
+    v.first = first;
+    v.last = last;
+    const int64_t cap = (int64_t)a.c.max_pages << (a.c.shift + 5);
+    const int end = last + 1 < cap ? last + 1 : (int)cap; // tokens below it
+    v.lead = v.from = v.count = 0;
+    if (end > 0) {
+        int lo = a.window && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
+        lo = lo < end ? lo : end;
+        const int keep = a.sinks < end ? a.sinks : end;
+        v.from = lo >> 5;
+        const int lead = (keep + 31) >> 5;
+        v.lead = lead < v.from ? lead : v.from;
+        v.count = v.lead + ((end + 31) >> 5) - v.from;
+    }
+    v.share = (v.count + a.splits - 1) / a.splits;
+    v.share = v.share > a.min_share ? v.share : a.min_share;
+    v.used = (v.count + v.share - 1) / v.share;
+    return v;
+}
+__host__ __device__ __forceinline__ int view_block(const TileView &v, int i) {
+    return i < v.lead ? i : v.from + i - v.lead;
+}
+// Whether every row of the tile sees all tokens of a record.
+__host__ __device__ __forceinline__ bool sees_all(const AttendArgs &a, const TileView &v, int blk) {
+    const int lo = blk * kBlock, hi = lo + kBlock - 1;
+    return hi <= v.first && (!a.window || lo > v.last - a.window || hi < a.sinks);
+}
+// Whether a row at position pos (its window starting at lo) sees token j.
+__host__ __device__ __forceinline__ bool sees(const AttendArgs &a, int pos, int lo, int j) {
+    return j <= pos && (j >= lo || j < a.sinks);
+}
+__host__ __device__ __forceinline__ int window_start(const AttendArgs &a, int pos) {
+    return a.window ? pos - a.window + 1 : 0;
+}
+
+// Where no running maximum was set yet; its exponentials of it are zero.
+constexpr float kNoMax = -3.0e38f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+} // namespace tsl

@@ -1,0 +1,235 @@
+// Keys and values into and out of the paged 4-bit cache (layout: tsl_attn.h,
+// tsl_cache).  A run x of 64 columns of a head of a token becomes
+//     b = bf16(min x),  s = bf16((max x - b) / 15),  c = round((x - b) / s).
+// Bound by bytes: 2 or 4 read and 0.5625 written a value (append), the
+// reverse (read).  One workgroup takes one record (32 tokens of one head), so
+// the words that tokens share have one writer.
+#include "attn.hpp"
+#include "rows.hpp"
+
+namespace tsl {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The record, and the tokens of it that the call's rows are (lo .. hi - 1),
+// of one workgroup; row is that of token 0 (it may lie before the rows).
+struct Span {
+    char *rec;
+    int lo, hi;
+    int64_t row;
+    int head;
+    int row0, before; // the sequence's first row; rows before position 0 (of the first workgroup)
+};
+template <int D>
+__device__ __forceinline__ Span span_of(const MoveArgs &a) {
+    const int blk_i = blockIdx.x % a.seq_blocks, rest = blockIdx.x / a.seq_blocks;
+    Span w;
+    w.head = rest % a.c.n_kv_heads;
+    const int s = rest / a.c.n_kv_heads;
+    const SeqRows q = seq_rows(a.c, s);
+    const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
+    const int start = q.ctx - q.n; // position of row 0
+    w.row0 = q.row0;
+    w.before = blk_i > 0 || start >= 0 ? 0 : (n < -start ? n : -start);
+    const int first = start > 0 ? start : 0;
+    const int64_t end = (int64_t)start + n;
+    const int blk = (first >> 5) + blk_i;
+    const int64_t t0 = (int64_t)blk * kBlock;
+    w.lo = t0 < first ? (int)(first - t0) : 0;
+    w.hi = end - t0 < kBlock ? (int)(end - t0 > 0 ? end - t0 : 0) : kBlock;
+    w.row = q.row0 + t0 - start;
+    w.rec = w.hi > w.lo ? record_of(a.c, s, w.head, blk, record_bytes(D)) : nullptr;
+    return w;
+}
+
+// Index of 32-bit word n of a lane in a record's codes.
+__device__ __forceinline__ int word_at(int n, int lane) { return (n >> 2) * 256 + lane * 4 + (n & 3); }
+// Place of a token in the 32 scales (or biases) of a record.
+__device__ __forceinline__ int scale_at(int t) {
+    return ((t & 15) >> 2) * 8 + (t >> 4) * 4 + (t & 3);
+}
+__device__ __forceinline__ int nibble_at(int i) { return 4 * ((i >> 1) + 4 * (i & 1)); }
+
+// Codes of 8 columns of a run whose other columns the 8 lanes of this
+// lane's group hold; s and b are the run's.
+__device__ __forceinline__ void quantise(f32x8 x, uint32_t (&c)[8], uint16_t *s, uint16_t *b) {
+    float lo = x[0], hi = x[0], bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        bad += x[i] * 0.f; // NaN where a value is not finite
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        lo = fminf(lo, __shfl_xor(lo, o, 64));
+        hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+        bad += __shfl_xor(bad, o, 64);
+    }
+    const uint32_t bb = pack_bf16(lo, 0.f) & 0xFFFFu;
+    const float bias = bf16_lo(bb);
+    const uint32_t sb = pack_bf16((hi - bias) / 15.f, 0.f) & 0xFFFFu;
+    const float scale = bf16_lo(sb);
+    const bool whole = bad == 0.f && __builtin_isfinite(scale) && __builtin_isfinite(bias);
+    *s = whole ? (uint16_t)sb : 0x7FC0u;
+    *b = whole ? (uint16_t)bb : 0x7FC0u;
+    // binary64: the quotient's place next to a border between codes is exact
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        double q = 0.0;
+        if (whole && scale > 0.f)
+            q = rint(((double)x[i] - (double)bias) / (double)scale);
+        q = q < 0.0 ? 0.0 : (q > 15.0 ? 15.0 : q);
+        c[i] = (uint32_t)q;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_kernel(MoveArgs a) {
+    constexpr int LPT = D / 8;                // lanes of a token, 8 columns each
+    constexpr int TPP = kThreads / LPT;       // tokens a pass
+    constexpr int W = D / 32;
+    __shared__ uint32_t vc[kBlock][D / 8 + 1]; // V codes of a token, 4 bits a column
+    const Span w = span_of<D>(a);
+    if (!w.rec)
+        return;
+    uint32_t *kw = reinterpret_cast<uint32_t *>(w.rec);
+    uint32_t *vw = kw + 4 * D;
+    uint16_t *sc = reinterpret_cast<uint16_t *>(w.rec + 32 * D);
+    const int cl = threadIdx.x % LPT;
+    for (int t0 = 0; t0 < kBlock; t0 += TPP) {
+        const int t = t0 + threadIdx.x / LPT;
+        const bool mine = t >= w.lo && t < w.hi;
+        const int64_t row = mine ? w.row + t : w.row + w.lo;
+        const char *k = static_cast<const char *>(a.K) +
+                        (row * a.ldk + w.head * a.k_head) * (a.bf16 ? 2 : 4);
+        const char *v = static_cast<const char *>(a.V) +
+                        (row * a.ldv + w.head * a.v_head) * (a.bf16 ? 2 : 4);
+        const f32x8 xk = load8<true>(k, a.bf16, cl * 8, D), xv = load8<true>(v, a.bf16, cl * 8, D);
+        uint32_t ck[8], cv[8];
+        uint16_t sk, bk, sv, bv;
+        quantise(xk, ck, &sk, &bk);
+        quantise(xv, cv, &sv, &bv);
+        if (!mine)
+            continue;
+        uint32_t word = 0, vals = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            word |= ck[i] << nibble_at(i);
+            vals |= cv[i] << (4 * i);
+        }
+        kw[word_at((t >> 4) * W + cl / 4, (cl & 3) * 16 + (t & 15))] = word;
+        vc[t][cl] = vals;
+        if (cl % 8 == 0) {
+            uint16_t *g = sc + (cl / 8) * 128 + scale_at(t);
+            g[0] = sk;
+            g[32] = bk;
+            g[64] = sv;
+            g[96] = bv;
+        }
+    }
+    __syncthreads();
+    // V words: 8 tokens of a column each; tokens that are not the call's keep
+    // their bits
+    for (int e = threadIdx.x; e < 4 * D; e += kThreads) {
+        const int col = e % D, g = e / D;
+        uint32_t mask = 0, word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = (i >> 2) * 16 + g * 4 + (i & 3);
+            if (t >= w.lo && t < w.hi) {
+                mask |= 15u << nibble_at(i);
+                word |= ((vc[t][col >> 3] >> (4 * (col & 7))) & 15u) << nibble_at(i);
+            }
+        }
+        if (!mask)
+            continue;
+        uint32_t *p = vw + word_at(col >> 4, g * 16 + (col & 15));
+        *p = mask == 0xFFFFFFFFu ? word : (*p & ~mask) | word;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
+    constexpr int LPT = D / 8, TPP = kThreads / LPT, W = D / 32;
+    __shared__ uint32_t codes[8 * D];
+    __shared__ uint16_t sc[D / 64 * 128];
+    const Span w = span_of<D>(a);
+    const int e = a.bf16 ? 2 : 4;
+    // rows before position 0 lie in no record
+    for (int i = threadIdx.x; i < w.before * LPT; i += kThreads) {
+        const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int64_t row = w.row0 + i / LPT;
+        if (a.K)
+            store8<true>(static_cast<char *>(a.K) + (row * a.ldk + w.head * a.k_head) * e, a.bf16,
+                         i % LPT * 8, D, zero);
+        if (a.V)
+            store8<true>(static_cast<char *>(a.V) + (row * a.ldv + w.head * a.v_head) * e, a.bf16,
+                         i % LPT * 8, D, zero);
+    }
+    if (w.hi <= w.lo)
+        return;
+    if (w.rec) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(w.rec);
+        for (int e = threadIdx.x; e < 2 * D; e += kThreads)
+            reinterpret_cast<u32x4 *>(codes)[e] = reinterpret_cast<const u32x4 *>(src)[e];
+        for (int e = threadIdx.x; e < D; e += kThreads)
+            reinterpret_cast<uint32_t *>(sc)[e] = src[8 * D + e];
+    }
+    __syncthreads();
+    const int cl = threadIdx.x % LPT;
+    for (int t0 = 0; t0 < kBlock; t0 += TPP) {
+        const int t = t0 + threadIdx.x / LPT;
+        if (t < w.lo || t >= w.hi)
+            continue;
+        f32x8 k = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v = k;
+        if (w.rec) {
+            const uint16_t *g = sc + (cl / 8) * 128 + scale_at(t);
+            const float sk = bf16_lo(g[0]), bk = bf16_lo(g[32]);
+            const float sv = bf16_lo(g[64]), bv = bf16_lo(g[96]);
+            const uint32_t word = codes[word_at((t >> 4) * W + cl / 4, (cl & 3) * 16 + (t & 15))];
+            const int lane = ((t & 15) >> 2) * 16, shift = nibble_at((t >> 4) * 4 + (t & 3));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int col = cl * 8 + i;
+                const uint32_t x = codes[4 * D + word_at(col >> 4, lane + (col & 15))];
+                k[i] = fmaf(sk, (float)((word >> nibble_at(i)) & 15u), bk);
+                v[i] = fmaf(sv, (float)((x >> shift) & 15u), bv);
+            }
+        }
+        const int64_t row = w.row + t;
+        if (a.K)
+            store8<true>(static_cast<char *>(a.K) + (row * a.ldk + w.head * a.k_head) * e, a.bf16,
+                         cl * 8, D, k);
+        if (a.V)
+            store8<true>(static_cast<char *>(a.V) + (row * a.ldv + w.head * a.v_head) * e, a.bf16,
+                         cl * 8, D, v);
+    }
+}
+
+} // namespace
+
+hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks));
+    if (head_dim == 64)
+        hipLaunchKernelGGL(append_kernel<64>, grid, dim3(kThreads), 0, stream, a);
+    else if (head_dim == 128)
+        hipLaunchKernelGGL(append_kernel<128>, grid, dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL(append_kernel<256>, grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks));
+    if (head_dim == 64)
+        hipLaunchKernelGGL(read_kernel<64>, grid, dim3(kThreads), 0, stream, a);
+    else if (head_dim == 128)
+        hipLaunchKernelGGL(read_kernel<128>, grid, dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL(read_kernel<256>, grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+} // namespace tsl
