@@ -32,7 +32,7 @@ SOURCES = ["abi.cpp", "plan.cpp", "pack.hip", "combine.hip", "embed.hip", "moe.h
            "noalloc.hip"]
 BLOCK_SOURCES = ["block.cpp", "norm.hip", "grad.hip", "decode.hip", "combine.hip", "skinny.hip",
                  "prefill.hip", "q4gemm.hip"]
-ATTN_SOURCES = ["attn.cpp", "rotary.hip", "kvcache.hip", "attend.hip"]
+ATTN_SOURCES = ["attn.cpp", "rotary.hip", "kvcache.hip", "attend.hip", "prompt.hip"]
 BLOCK_FLAGS = ["-DTSL_EPILOGUE=1"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-mcode-object-version=5", "-Wall",
          # only the C ABI of include/tsl.h is exported (it sets default visibility)

@@ -193,33 +193,42 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
 
 // How cache_attention divides its work; a function of sizes alone.
 struct AttendPlan {
-    int32_t tiles, splits, min_share;
+    int32_t tile_rows, tiles, splits, min_share;
     size_t bytes;
 };
 
-// Workgroups that a call of few rows is divided into at least, where its
-// tokens allow it: three for each of the 256 CUs.
-constexpr int64_t kAttendUnits = 768;
-// Records that are worth a range of their own: two for each wave.
-constexpr int kAttendShare = 8;
+// Query rows of a sequence and K/V head up to which a call takes the kernel of
+// few rows, where every tile of 16 expands the records it reads anew.
+constexpr int64_t kFewRows = 64;
+// Workgroups that a call is divided into at least, where its tokens allow it:
+// three for each of the 256 CUs with few rows, one with many.
+constexpr int64_t kAttendUnits = 768, kPromptUnits = 256;
+// Records that are worth a range of their own: two for each wave, with many
+// rows enough to outweigh the join.
+constexpr int kAttendShare = 8, kPromptShare = 16;
 
 tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
                        int32_t sinks, AttendPlan *p) {
     const int64_t group = n_q_heads / c.n_kv_heads;
-    const int64_t max_rows = std::min<int64_t>(q.max_rows, q.rows);
+    const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
+    const bool few = rows <= kFewRows || c.head_dim > 128;
+    p->tile_rows = few ? kTileRows : (rows <= 128 ? 128 : 256);
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
     if (window)
-        seen = std::min<int64_t>(seen, (int64_t)window + sinks + kTileRows + 2 * kBlock);
+        seen = std::min<int64_t>(seen, (int64_t)window + sinks + p->tile_rows + 2 * kBlock);
     const int64_t records = (seen + kBlock - 1) / kBlock;
-    p->tiles = (int32_t)((max_rows * group + kTileRows - 1) / kTileRows);
+    p->tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
     const int64_t units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
-    int64_t splits = units > 0 ? (kAttendUnits + units - 1) / units : 1;
-    splits = std::max<int64_t>(1, std::min(splits, (records + kAttendShare - 1) / kAttendShare));
+    const int64_t target = few ? kAttendUnits : kPromptUnits;
+    p->min_share = few ? kAttendShare : kPromptShare;
+    int64_t splits = units > 0 ? (target + units - 1) / units : 1;
+    splits = std::max<int64_t>(1, std::min(splits, (records + p->min_share - 1) / p->min_share));
     p->splits = (int32_t)splits;
-    p->min_share = kAttendShare;
-    if (units * splits > kMaxBlocks || units * (kTileRows / 4) > kMaxBlocks)
+    if (units * splits > kMaxBlocks || units * (p->tile_rows / 4) > kMaxBlocks)
         return TSL_ERR_UNSUPPORTED;
-    p->bytes = splits > 1 ? (size_t)(units * splits) * kTileRows * (size_t)(c.head_dim + 2) * 4 : 0;
+    p->bytes = splits > 1
+                   ? (size_t)(units * splits) * p->tile_rows * (size_t)(c.head_dim + 2) * 4
+                   : 0;
     return TSL_OK;
 }
 
@@ -409,12 +418,14 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     if (p.bytes) {
         a.part = static_cast<float *>(workspace);
         a.part_ml = a.part + (int64_t)a.c.n_seqs * a.c.n_kv_heads * p.tiles * p.splits *
-                                 kTileRows * cache->head_dim;
+                                 p.tile_rows * cache->head_dim;
     }
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = launch_attend_decode(cache->head_dim, a, hs);
+    hipError_t e = p.tile_rows == kTileRows
+                       ? launch_attend_decode(cache->head_dim, a, hs)
+                       : launch_attend_prompt(cache->head_dim, p.tile_rows, a, hs);
     if (e == hipSuccess && p.splits > 1)
-        e = launch_attend_join(cache->head_dim, kTileRows, a, hs);
+        e = launch_attend_join(cache->head_dim, p.tile_rows, a, hs);
     return from_hip(e);
 }
 
