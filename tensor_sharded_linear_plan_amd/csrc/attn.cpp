@@ -212,7 +212,7 @@ tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads,
     const int64_t group = n_q_heads / c.n_kv_heads;
     const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
     const bool few = rows <= kFewRows || c.head_dim > 128;
-    p->tile_rows = few ? kTileRows : (rows <= 128 ? 128 : 256);
+    p->tile_rows = few ? kTileRows : kPromptRows;
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
     if (window)
         seen = std::min<int64_t>(seen, (int64_t)window + sinks + p->tile_rows + 2 * kBlock);
@@ -423,7 +423,7 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t e = p.tile_rows == kTileRows
                        ? launch_attend_decode(cache->head_dim, a, hs)
-                       : launch_attend_prompt(cache->head_dim, p.tile_rows, a, hs);
+                       : launch_attend_prompt(cache->head_dim, a, hs);
     if (e == hipSuccess && p.splits > 1)
         e = launch_attend_join(cache->head_dim, p.tile_rows, a, hs);
     return from_hip(e);

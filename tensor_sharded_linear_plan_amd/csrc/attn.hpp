@@ -79,8 +79,8 @@ struct AttendArgs {
 constexpr int kTileRows = 16; // query rows of a tile of attend_decode
 
 hipError_t launch_attend_decode(int head_dim, const AttendArgs &a, hipStream_t stream);
-// tile_rows query rows a workgroup, 128 or 256; head_dim 64 or 128.
-hipError_t launch_attend_prompt(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
+constexpr int kPromptRows = 256; // of attend_prompt, head_dim 64 or 128
+hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
 
 // ---- where tokens lie and which are seen ------------------------------------------
