@@ -201,11 +201,12 @@ struct AttendPlan {
 // few rows, where every tile of 16 expands the records it reads anew.
 constexpr int64_t kFewRows = 64;
 // Workgroups that a call is divided into at least, where its tokens allow it:
-// three for each of the 256 CUs with few rows, one with many.
-constexpr int64_t kAttendUnits = 768, kPromptUnits = 256;
-// Records that are worth a range of their own: two for each wave, with many
-// rows enough to outweigh the join.
-constexpr int kAttendShare = 8, kPromptShare = 16;
+// with few rows the four that share each of the 256 CUs, with many the one.
+constexpr int64_t kAttendUnits = 1024, kPromptUnits = 256;
+// Records of a range: at least what is worth it (few rows: two for each wave;
+// many: enough to outweigh the join), and with few rows at most so many, so that
+// sequences of different lengths end together.
+constexpr int kAttendShare = 8, kPromptShare = 16, kAttendMost = 64;
 
 tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
                        int32_t sinks, AttendPlan *p) {
@@ -222,9 +223,12 @@ tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads,
     const int64_t target = few ? kAttendUnits : kPromptUnits;
     p->min_share = few ? kAttendShare : kPromptShare;
     int64_t splits = units > 0 ? (target + units - 1) / units : 1;
-    splits = std::max<int64_t>(1, std::min(splits, (records + p->min_share - 1) / p->min_share));
+    if (few)
+        splits = std::max<int64_t>(splits, (records + kAttendMost - 1) / kAttendMost);
+    splits = std::min<int64_t>(splits, (records + p->min_share - 1) / p->min_share);
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
     p->splits = (int32_t)splits;
-    if (units * splits > kMaxBlocks || units * (p->tile_rows / 4) > kMaxBlocks)
+    if (units * splits > kMaxBlocks || (splits > 1 && units * p->tile_rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
     p->bytes = splits > 1
                    ? (size_t)(units * splits) * p->tile_rows * (size_t)(c.head_dim + 2) * 4

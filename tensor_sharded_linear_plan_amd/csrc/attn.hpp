@@ -76,6 +76,7 @@ struct AttendArgs {
     float *part_ml;    // ... [tile rows][2]: reference exponent and sum
 };
 
+constexpr int kMaxSplits = 512;
 constexpr int kTileRows = 16; // query rows of a tile of attend_decode
 
 hipError_t launch_attend_decode(int head_dim, const AttendArgs &a, hipStream_t stream);
