@@ -200,35 +200,36 @@ struct AttendPlan {
 // Query rows of a sequence and K/V head up to which a call takes the kernel of
 // few rows, where every tile of 16 expands the records it reads anew.
 constexpr int64_t kFewRows = 64;
-// Workgroups that a call is divided into at least, where its tokens allow it:
-// with few rows the four that share each of the 256 CUs, with many the one.
-constexpr int64_t kAttendUnits = 1024, kPromptUnits = 256;
-// Records of a range: at least what is worth it (few rows: two for each wave;
-// many: enough to outweigh the join), and with few rows at most so many, so that
-// sequences of different lengths end together.
-constexpr int kAttendShare = 8, kPromptShare = 16, kAttendMost = 64;
+constexpr int64_t kCUs = 256;
+// Records of a range: at least what is worth it (few rows: two steps of each of
+// four waves; many: enough to outweigh the join), and with few rows at most so
+// many, so that sequences of different lengths end together.
+constexpr int kPromptShare = 16, kAttendMost = 64;
 
 tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
                        int32_t sinks, AttendPlan *p) {
     const int64_t group = n_q_heads / c.n_kv_heads;
     const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
     const bool few = rows <= kFewRows || c.head_dim > 128;
-    p->tile_rows = few ? kTileRows : kPromptRows;
+    const int at_once = c.head_dim > 128 || rows > 8 ? 1 : (c.head_dim == 64 && rows <= 4 ? 4 : 2);
+    p->tile_rows = few ? 16 / at_once : kPromptRows;
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
     if (window)
         seen = std::min<int64_t>(seen, (int64_t)window + sinks + p->tile_rows + 2 * kBlock);
     const int64_t records = (seen + kBlock - 1) / kBlock;
     p->tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
     const int64_t units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
-    const int64_t target = few ? kAttendUnits : kPromptUnits;
-    p->min_share = few ? kAttendShare : kPromptShare;
-    int64_t splits = units > 0 ? (target + units - 1) / units : 1;
+    // a workgroup for every place there is, where the tokens allow it
+    const int64_t target = kCUs * (few ? attend_groups(c.head_dim, at_once) : 1);
+    p->min_share = few ? 8 * at_once : kPromptShare;
+    int64_t splits = units > 0 ? target / units : 1;
     if (few)
         splits = std::max<int64_t>(splits, (records + kAttendMost - 1) / kAttendMost);
     splits = std::min<int64_t>(splits, (records + p->min_share - 1) / p->min_share);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
     p->splits = (int32_t)splits;
-    if (units * splits > kMaxBlocks || (splits > 1 && units * p->tile_rows > kMaxBlocks))
+    if (units * splits > kMaxBlocks ||
+        (splits > 1 && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
     p->bytes = splits > 1
                    ? (size_t)(units * splits) * p->tile_rows * (size_t)(c.head_dim + 2) * 4
@@ -425,8 +426,8 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
                                  p.tile_rows * cache->head_dim;
     }
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = p.tile_rows == kTileRows
-                       ? launch_attend_decode(cache->head_dim, a, hs)
+    hipError_t e = p.tile_rows < kPromptRows
+                       ? launch_attend_decode(cache->head_dim, p.tile_rows, a, hs)
                        : launch_attend_prompt(cache->head_dim, a, hs);
     if (e == hipSuccess && p.splits > 1)
         e = launch_attend_join(cache->head_dim, p.tile_rows, a, hs);

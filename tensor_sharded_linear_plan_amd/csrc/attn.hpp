@@ -77,9 +77,16 @@ struct AttendArgs {
 };
 
 constexpr int kMaxSplits = 512;
-constexpr int kTileRows = 16; // query rows of a tile of attend_decode
+constexpr int kJoinWave = 32; // ranges that one wave adds; a workgroup more
+// attend_decode: tiles of 16 / P query rows, P records at a time (P = 2 with
+// head_dim up to 128, 4 with 64), two stages of them for each of four waves in a
+// CU's 160 KB of LDS.  Workgroups that share a CU:
+constexpr int attend_groups(int head_dim, int p) {
+    const int n = 160 * 1024 / (4 * 2 * p * record_bytes(head_dim) + 512);
+    return n > 4 ? 4 : n;
+}
 
-hipError_t launch_attend_decode(int head_dim, const AttendArgs &a, hipStream_t stream);
+hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
 constexpr int kPromptRows = 256; // of attend_prompt, head_dim 64 or 128
 hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
@@ -160,6 +167,16 @@ __host__ __device__ __forceinline__ bool sees(const AttendArgs &a, int pos, int 
 __host__ __device__ __forceinline__ int window_start(const AttendArgs &a, int pos) {
     return a.window ? pos - a.window + 1 : 0;
 }
+
+// Two binary32 values as a pair of bf16, to nearest even (one instruction).
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// Keeps a branch that few steps take from being made part of all of them.
+__device__ __forceinline__ void rare() { asm volatile(""); }
 
 // Where no running maximum was set yet; its exponentials of it are zero.
 constexpr float kNoMax = -3.0e38f;

@@ -79,9 +79,6 @@ __device__ __forceinline__ uint32_t wave_pk_max(uint32_t v) {
     return lo | hi << 16;
 }
 
-// Keeps a branch that few steps take from being made part of all of them.
-__device__ __forceinline__ void rare() { asm volatile(""); }
-
 // Nothing is scheduled across.
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -555,7 +552,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     else if (a.o_bf16)
         each([&](int col, f32x4 v) {
             *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + at + col) =
-                u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
         });
     else
         each([&](int col, f32x4 v) {
