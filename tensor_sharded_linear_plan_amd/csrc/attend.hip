@@ -2,10 +2,15 @@
 // (generated tokens): o_i = sum_j p_ij v_j, p = softmax over the visible j of
 // scale q_i . k_j, one pass over the tokens with a running maximum and sum.
 //
-// A workgroup takes up to 16 query rows of one sequence and K/V head (the heads
-// that share it, of one or several tokens) and a range of the records they see;
-// its four waves take records in turn and join at the end through LDS.  Where the
-// tiles are few the ranges are many, and attend_join adds them.
+// A wave takes up to 16 query rows of one sequence and K/V head (the heads that
+// share it, of one or several tokens) and walks a range of the records they see.
+// All records of a call in a row, tile after tile, are cut into as many equal
+// parts as waves fit on the chip, so that sequences of any lengths end together
+// and a wave starts once; where a part runs over the end of a tile the wave goes
+// on with the next, and attend_join adds what two or more waves have of a tile.
+// Waves do not wait for each other: a start, from the first instruction to the
+// first product, takes 3 to 5 us, mostly of three reads that follow from each
+// other (lengths, page, record).
 //
 // The products run on 16x16x32 MFMAs, transposed: S^T = K Q^T and O^T = V^T P^T,
 // so a lane holds one query row throughout (column l % 16) and the
@@ -19,22 +24,16 @@
 // memory and the vector units).
 //
 // Records come by direct copies into LDS (global_load_lds), each wave its own
-// two stages: the next record is on its way while this one is multiplied, and
-// the registers that a prefetch would hold are free, so that four workgroups
-// share a CU.
+// three stages: two records are on their way while one is multiplied.
 #include "attn.hpp"
 #include "gemm_common.hpp"
 
 namespace tsl {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4; // of a workgroup
 
-__device__ __forceinline__ float pick(u32x4 w, int e) {
-    return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-}
-
-constexpr int kStages = 2;
+constexpr int kStages = 3; // 2 .. 4 (the waits below)
 
 // At most N of the wave's copies into LDS are still under way.
 template <int N> __device__ __forceinline__ void wait_copies() {
@@ -42,188 +41,298 @@ template <int N> __device__ __forceinline__ void wait_copies() {
     asm volatile("" ::: "memory");
 }
 
-// P records a step: the 16 columns of a product are P times the tile's 16 / P
-// rows, and a lane keeps of each product what is of its own record.
+// The sum of the lanes up to each: within rows of 16, then over the rows.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true); // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
+              c = __builtin_amdgcn_readlane(v, 47);
+    const int row = (int)((threadIdx.x & 63) >> 4);
+    return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
+}
+
+// The part of a wave, of all records in a row cut into equal parts: it begins
+// `skip` records into sequence s (rows q).  64 sequences at a time (the host lets
+// at most kMaxShared share).
+struct Part {
+    int s, skip, left, per_seq;
+    SeqRows q;
+};
+template <int ROWS> __device__ __forceinline__ Part part_of(const AttendArgs &a, int me) {
+    const int lane = threadIdx.x & 63;
+    Part part = {0, 0, 0, 0, {0, 0, 0}};
+    int total = 0, begin = 0, before = 0;
+    bool finding = false;
+    for (int base = 0;;) {
+        SeqRows q = {0, 0, 0};
+        int own = 0;
+        if (base + lane < a.c.n_seqs) {
+            q = seq_rows(a.c, base + lane);
+            int rows = (q.n < a.c.max_rows ? q.n : a.c.max_rows) * a.group;
+            for (int t = 0; rows > 0; ++t, rows -= ROWS)
+                own += view_of(a, q, t, ROWS, rows).count;
+        }
+        own *= a.c.n_kv_heads;
+        const int upto = wave_scan(own), all = __builtin_amdgcn_readlane(upto, 63);
+        if (!finding) {
+            total += all;
+            base += 64;
+            if (base < a.c.n_seqs)
+                continue;
+            int share = quotient(total + a.parts - 1, a.by_parts);
+            share = share > a.min_share ? share : a.min_share;
+            if ((int64_t)share * me >= total)
+                return part;
+            begin = share * me;
+            part.left = total - begin < share ? total - begin : share;
+            finding = true;
+            base = 0;
+            if (a.c.n_seqs > 64)
+                continue;
+        }
+        // the first sequence that ends behind the beginning
+        const uint64_t past = __ballot(before + upto > begin);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            part.s = base + at;
+            part.per_seq = __builtin_amdgcn_readlane(own, at);
+            part.skip = begin - before - (__builtin_amdgcn_readlane(upto, at) - part.per_seq);
+            part.q.row0 = __builtin_amdgcn_readlane(q.row0, at);
+            part.q.n = __builtin_amdgcn_readlane(q.n, at);
+            part.q.ctx = __builtin_amdgcn_readlane(q.ctx, at);
+            return part;
+        }
+        before += all;
+        base += 64;
+    }
+}
+
+// Rotation of the lanes of a row of 16 by 16 / P ... 8, added or compared: what the
+// P groups of columns of a row have, in each of them.
+template <int P, class F> __device__ __forceinline__ float over_groups(float v, F f) {
+    if (P >= 2)
+        v = f(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, true)));
+    if (P >= 4)
+        v = f(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, true)));
+    return v;
+}
+
+// The 16 columns of a product are P times the tile's 16 / P rows, and a lane keeps
+// of each product 8 / P of its tokens: with few rows the vector work on logits and
+// probabilities, which is more than half of all, is divided among the columns
+// instead of repeated.
 template <int D, int P>
-__global__ void __launch_bounds__(64 * kWaves, attend_groups(D, P)) attend_decode_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, attend_groups(D)) attend_decode_kernel(AttendArgs a) {
     constexpr int G = D / 64, W = D / 32, DT = D / 16, ROWS = 16 / P;
     constexpr int REC = record_bytes(D), PIECES = REC / 16; // 16 bytes a lane
-    constexpr int COPIES = (PIECES + 63) / 64, STEP = P * REC;
-    // a wave's stages, and after the walk its sums
-    __shared__ __attribute__((aligned(16))) char ring[kWaves][kStages * STEP];
-    __shared__ float red_m[kWaves][16], red_l[kWaves][16];
-    static_assert(kStages * STEP >= DT * 1024, "sums of a wave");
+    constexpr int COPIES = (PIECES + 63) / 64, TPL = 8 / P; // tokens of a lane
+    __shared__ __attribute__((aligned(16))) char ring[kWaves][kStages * REC]; // a wave's stages
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int own = c / ROWS, cr = c % ROWS; // the lane's record of a step, its row
+    const int own = c / ROWS, cr = c % ROWS; // the lane's tokens of a record, its row
 
-    int b = blockIdx.x;
-    const int split = b % a.splits;
-    b /= a.splits;
-    const int unit = b; // (sequence, head, tile)
-    const int tile = b % a.tiles;
-    b /= a.tiles;
-    const int head = b % a.c.n_kv_heads, s = b / a.c.n_kv_heads;
-    const SeqRows q = seq_rows(a.c, s);
+    // Whole: the wave's (sequence, head, tile).  Shared: its part of all records
+    // of the call in a row, tiles innermost, then heads, then sequences.
+    const int me = blockIdx.x * kWaves + wave;
+    int s, head = 0, tile = 0, at = 0; // at: the record of the tile's list to start at
+    int left = INT32_MAX;              // records of the part
+    SeqRows q;
+    if (!a.shared) {
+        if (me >= a.units)
+            return;
+        const int b = quotient(me, a.by_tiles);
+        tile = me - b * a.tiles;
+        s = quotient(b, a.by_heads);
+        head = b - s * a.c.n_kv_heads;
+        q = seq_rows(a.c, s);
+    } else {
+        const Part part = part_of<ROWS>(a, me);
+        if (part.left <= 0)
+            return;
+        s = part.s;
+        q = part.q;
+        left = part.left;
+        // at most 2^10 heads: the quotient is off by at most one
+        const int per_head = quotient(part.per_seq, a.by_heads);
+        head = __builtin_amdgcn_readfirstlane(
+            (int)((float)part.skip * __builtin_amdgcn_rcpf((float)per_head)));
+        head -= head * per_head > part.skip;
+        head += (head + 1) * per_head <= part.skip;
+        at = part.skip - head * per_head;
+    }
+
+    auto next_tile = [&] {
+        if (++tile == a.tiles) {
+            tile = 0;
+            if (++head == a.c.n_kv_heads) {
+                head = 0;
+                q = seq_rows(a.c, ++s);
+            }
+        }
+    };
+    while (true) {
+    const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
     const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
     const int rows = n * a.group - tile * ROWS; // of this tile and later ones
-    if (rows <= 0)
+    TileView view = {0, 0, 0, 0, 0, 0, 0};
+    if (rows > 0)
+        view = view_of(a, q, tile, ROWS, rows);
+    else if (!a.shared)
         return;
+    // on to the tile where the part begins, past those without records
+    if (a.shared && at >= view.count) {
+        at -= view.count;
+        next_tile();
+        continue;
+    }
     const int start = q.ctx - q.n;
-    const int last_rho = tile * ROWS + (rows < ROWS ? rows : ROWS) - 1;
-    const TileView view = tile_view(a, start + tile * ROWS / a.group, start + last_rho / a.group);
-    const int begin = split * view.share;
-    const int stop = begin + view.share < view.count ? begin + view.share : view.count;
-    if (begin >= stop && split > 0)
-        return;
+    const int begin = at;
+    const int stop = view.count - at < left ? view.count : at + left;
+    const bool complete = begin == 0 && stop == view.count;
 
-    // pages of the wave's next 64 records, one a lane
-    const int mine = begin + wave * P;
-    const int n_mine = mine < stop ? (stop - mine + kWaves * P - 1) / (kWaves * P) : 0; // steps
-    auto index_at = [&](int k, int p) { return mine + k * (kWaves * P) + p; };
-    int pages = -1;
+    // the wave's next 64 records, one a lane: where they lie, and as bits which
+    // are there and which all rows of the tile see all of
+    const int n_mine = stop - begin;
+    uint32_t at_lo = 0, at_hi = 0;
+    uint64_t there = 0, clear = 0, next_there = 0, next_clear = 0;
     auto look_up = [&](int k0) {
-        const int r = index_at(k0 + lane / P, lane % P);
-        const int page = r < stop ? view_block(view, r) >> a.c.shift : a.c.max_pages;
-        pages = page < a.c.max_pages ? a.c.page_table[s * a.c.ld_table + page] : -1;
-        pages = pages < a.c.n_pages ? pages : -1;
+        const int r = begin + k0 + lane;
+        const int blk = view_block(view, r);
+        const char *rec = r < stop ? record_of(a.c, s, head, blk, REC) : nullptr;
+        next_there = __ballot(rec != nullptr);
+        next_clear = __ballot(sees_all(a, view, blk));
+        // one that is not there is read from page 0, and passed over
+        const uint64_t p = reinterpret_cast<uint64_t>(rec ? rec : a.c.pages);
+        at_lo = (uint32_t)p;
+        at_hi = (uint32_t)(p >> 32);
     };
     const uint32_t lds0 = (uint32_t)(uintptr_t)&ring[wave][0];
-    // the records of step k into their stage; one that is not there is read from
-    // page 0, and its tokens are hidden
-    auto copy = [&](int k) {
-        constexpr int kSteps = 64 / P;
-        if (k % kSteps == 0)
+    auto issue = [&](int k) { // record k of the wave into its stage
+        if ((k & 63) == 0)
             look_up(k);
-        uint32_t there = 0;
+        const uint64_t p = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)at_hi, k & 63) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)at_lo, k & 63);
+        const char *rec = reinterpret_cast<const char *>(p);
+        const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + (k % kStages) * REC));
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int page = __builtin_amdgcn_readlane(pages, k % kSteps * P + p);
-            const int blk = view_block(view, index_at(k, p));
-            const char *rec = a.c.pages + head * a.c.head_bytes;
-            if (page >= 0) {
-                there |= 1u << p;
-                rec += page * a.c.page_bytes + (int64_t)(blk & ((1 << a.c.shift) - 1)) * REC;
-            }
-            const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(
-                (int)(lds0 + (k % kStages) * STEP + p * REC));
-#pragma unroll
-            for (int i = 0; i < COPIES; ++i)
-                if ((i + 1) * 64 <= PIECES || lane < PIECES - i * 64)
-                    dma16(rec + i * 1024, (uint32_t)lane * 16, to + i * 1024);
-        }
-        return there;
+        for (int i = 0; i < COPIES; ++i)
+            if ((i + 1) * 64 <= PIECES || lane < PIECES - i * 64)
+                dma16(rec + i * 1024, (uint32_t)lane * 16, to + i * 1024);
     };
-    uint32_t there = 0, there1 = 0;
-    if (n_mine > 0)
-        there1 = copy(0);
-
     // the lane's query row
     const bool live = cr < rows;
     const int rho = tile * ROWS + (live ? cr : 0);
-    const int i = rho / a.group, hq = head * a.group + rho % a.group;
+    const int i = quotient(rho, a.by_group), hq = head * a.group + rho - i * a.group;
     const int pos = start + i, lo = window_start(a, pos);
     const uint16_t *qp = a.Q + (int64_t)(q.row0 + i) * a.ldq + hq * a.q_head + 8 * g;
     bf16x8 qr[W];
-    float qsum[G];
 #pragma unroll
     for (int w = 0; w < W; ++w) // the scale's sign goes to Q: the largest product
         qr[w] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(qp + 32 * w) ^
                                                (a.scale < 0.f ? 0x80008000u : 0u)); // is the largest logit
     const float scale = fmaxf(fabsf(a.scale), 1.17549435e-38f); // not 0: it meets infinities
-#pragma unroll
-    for (int k = 0; k < G; ++k) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 2 * k; w < 2 * k + 2; ++w)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                t += (float)qr[w][j];
-        t += __shfl_xor(t, 16, 64);
-        t += __shfl_xor(t, 32, 64);
-        qsum[k] = t;
-    }
 
     f32x4 o[DT], off[G], base[G];
-    float ob[G], m = kNoMax, l = 0.f;
+    float ob[G], qsum[G], m = kNoMax, l = 0.f;
     const bf16x8 all128 = __builtin_bit_cast(bf16x8, u32x4{0x43004300u, 0x43004300u, 0x43004300u, 0x43004300u});
 #pragma unroll
     for (int t = 0; t < DT; ++t)
         o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-        ob[k] = 0.f;
-        off[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const float z = -128.f * qsum[k];
-        base[k] = f32x4{z, z, z, z};
+    for (int d = 0; d < G; ++d) {
+        ob[d] = 0.f;
+        off[d] = base[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // -128 sum(q), in every row of the product: what a product begins with
+#pragma unroll
+        for (int w = 2 * d; w < 2 * d + 2; ++w)
+            base[d] = mfma_bf16(all128, qr[w], base[d]);
+        base[d] = -base[d];
+        qsum[d] = base[d][0] * -0.0078125f;
     }
 
-    for (int k = 0; k < n_mine; ++k) {
-        there = there1;
-        if (k + 1 < n_mine) {
+    // (one place that looks up and copies: cold code is what a start takes long over)
+    for (int k = 1 - kStages; k < n_mine; ++k) {
+        if (k + kStages - 1 < n_mine) {
             wait_lgkm0(); // the stage was read
-            there1 = copy(k + 1);
-            wait_copies<P * COPIES>();
+            issue(k + kStages - 1);
+            if (k < 0)
+                continue;
+            wait_copies<(kStages - 1) * COPIES>();
+        } else if (k < 0) {
+            continue;
+        } else if (kStages > 3 && k + 2 < n_mine) {
+            wait_copies<2 * COPIES>();
+        } else if (kStages > 2 && k + 1 < n_mine) {
+            wait_copies<COPIES>();
         } else {
             wait_copies<0>();
         }
-        const u32x4 *rec = reinterpret_cast<const u32x4 *>(&ring[wave][(k % kStages) * STEP]);
-        // scales of the lane's 8 tokens
-        const u32x4 *sc = rec + own * (REC / 16) + 2 * D + g;
-
-        f32x4 acc[2][G];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            u32x4 kc[G];
-#pragma unroll
-            for (int d = 0; d < G; ++d)
-                kc[d] = rec[p * (REC / 16) + d * 64 + lane];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int d = 0; d < G; ++d) {
-                    f32x4 t = base[d];
-#pragma unroll
-                    for (int w = 2 * d; w < 2 * d + 2; ++w)
-                        t = mfma_bf16(q4_to_bf16_plus128(kc[(u * W + w) >> 2][(u * W + w) & 3]), qr[w], t);
-                    if (p == 0)
-                        acc[u][d] = t;
-                    else
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[u][d][e] = own == p ? t[e] : acc[u][d][e];
-                }
+        if ((k & 63) == 0) { // (looked up kStages - 1 records ago)
+            there = next_there;
+            clear = next_clear;
         }
-        float x[8]; // products, the scale not yet in them
+        if (!(there >> (k & 63) & 1))
+            continue;
+        const u32x4 *rec = reinterpret_cast<const u32x4 *>(&ring[wave][(k % kStages) * REC]);
+        // scales of the lane's tokens, in pairs
+        typedef uint32_t pairs __attribute__((ext_vector_type(TPL / 2)));
+        auto scales = [&](int d, int kind) {
+            const pairs v = *reinterpret_cast<const pairs *>(reinterpret_cast<const char *>(rec + 2 * D) +
+                                                             d * 256 + kind * 64 + g * 16 + own * TPL * 2);
+            return v;
+        };
+
+        float x[TPL]; // products, the scale not yet in them
 #pragma unroll
         for (int d = 0; d < G; ++d) {
-            const u32x4 ks = sc[d * 16], kb = sc[d * 16 + 4];
+            f32x4 acc[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float t = pick(kb, e) * qsum[d];
-                x[e] = fmaf(pick(ks, e), acc[e >> 2][d][e & 3], d ? x[e] + t : t);
+            for (int u = 0; u < 2; ++u) {
+                acc[u] = base[d];
+#pragma unroll
+                for (int w = 2 * d; w < 2 * d + 2; ++w) {
+                    const int n = u * W + w;
+                    acc[u] = mfma_bf16(q4_to_bf16_plus128(rec[(n >> 2) * 64 + lane][n & 3]), qr[w], acc[u]);
+                }
+            }
+            const pairs ks = scales(d, 0), kb = scales(d, 1);
+#pragma unroll
+            for (int e = 0; e < TPL; ++e) {
+                float t = acc[e >> 2][e & 3];
+                if (P == 2)
+                    t = own ? acc[1][e] : acc[0][e];
+                if (P == 4) {
+                    const float lo2 = own & 2 ? acc[1][e] : acc[0][e], hi2 = own & 2 ? acc[1][2 + e] : acc[0][2 + e];
+                    t = own & 1 ? hi2 : lo2;
+                }
+                const float s1 = e & 1 ? bf16_hi(ks[e >> 1]) : bf16_lo(ks[e >> 1]);
+                const float b1 = e & 1 ? bf16_hi(kb[e >> 1]) : bf16_lo(kb[e >> 1]);
+                x[e] = d ? fmaf(b1, qsum[d], x[e]) : b1 * qsum[d];
+                x[e] = fmaf(s1, t, x[e]);
             }
         }
-        u32x4 keep = {~0u, ~0u, ~0u, ~0u}; // of the V scales: a hidden token's may be NaN
-        bool all = there == (1u << P) - 1;
+        pairs keep; // of the V scales: a hidden token's may be NaN
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            all = all && sees_all(a, view, view_block(view, index_at(k, p)));
+        for (int e = 0; e < TPL / 2; ++e)
+            keep[e] = ~0u;
+        const bool all = clear >> (k & 63) & 1;
         if (!all) {
             rare();
-            const int blk = view_block(view, index_at(k, own));
-            const bool here = there >> own & 1;
+            const int blk = view_block(view, begin + k);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const bool v = here & sees(a, pos, lo, blk * kBlock + (e >> 2) * 16 + g * 4 + (e & 3));
+            for (int e = 0; e < TPL; ++e) {
+                const int at = own * TPL + e;
+                const bool v = sees(a, pos, lo, blk * kBlock + (at >> 2) * 16 + g * 4 + (at & 3));
                 x[e] = v ? x[e] : -__builtin_inff();
                 keep[e >> 1] &= v ? ~0u : (e & 1 ? 0xFFFFu : 0xFFFF0000u);
             }
         }
         float top = x[0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e)
+        for (int e = 1; e < TPL; ++e)
             top = fmaxf(top, x[e]);
         top *= scale;
         // the reference exponent follows the maximum at a distance of 2^8:
@@ -244,210 +353,257 @@ __global__ void __launch_bounds__(64 * kWaves, attend_groups(D, P)) attend_decod
                 off[d] *= f;
             }
         }
-        float pr[8];
+        float pr[TPL];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < TPL; ++e) {
             pr[e] = exp2_fast(fmaf(x[e], scale, -m));
             l += pr[e];
         }
 #pragma unroll
         for (int d = 0; d < G; ++d) {
-            u32x4 vs = sc[d * 16 + 8], vb = sc[d * 16 + 12];
+            pairs vs = scales(d, 2), vb = scales(d, 3);
             if (!all) {
                 rare();
                 vs &= keep;
                 vb &= keep;
             }
-            u32x4 hi, rem;
+            u32x4 hi = {0, 0, 0, 0}, rem = {0, 0, 0, 0};
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < TPL / 2; ++h) {
                 const float w0 = pr[2 * h] * bf16_lo(vs[h]), w1 = pr[2 * h + 1] * bf16_hi(vs[h]);
                 ob[d] = fmaf(pr[2 * h], bf16_lo(vb[h]), ob[d]);
                 ob[d] = fmaf(pr[2 * h + 1], bf16_hi(vb[h]), ob[d]);
-                hi[h] = pack_pair(w0, w1);
-                rem[h] = pack_pair(w0 - bf16_lo(hi[h]), w1 - bf16_hi(hi[h]));
-            }
-            // what 128 + c has over c: the same products with a tile of 128
-            off[d] = mfma_bf16(all128, __builtin_bit_cast(bf16x8, hi), off[d]);
-            off[d] = mfma_bf16(all128, __builtin_bit_cast(bf16x8, rem), off[d]);
+                const uint32_t p16 = pack_pair(w0, w1);
+                const uint32_t r16 = pack_pair(w0 - bf16_lo(p16), w1 - bf16_hi(p16));
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const u32x4 vc = rec[p * (REC / 16) + D + d * 64 + lane];
-                const uint32_t take = P == 1 || own == p ? ~0u : 0u;
-                const bf16x8 wh = __builtin_bit_cast(bf16x8, hi & take), wl = __builtin_bit_cast(bf16x8, rem & take);
-#pragma unroll
-                for (int t = 4 * d; t < 4 * d + 4; ++t) {
-                    const bf16x8 v = q4_to_bf16_plus128(vc[t & 3]);
-                    o[t] = mfma_bf16(v, wh, o[t]);
-                    o[t] = mfma_bf16(v, wl, o[t]);
+                for (int k = 0; k < P; ++k) {
+                    hi[k * (TPL / 2) + h] = P == 1 || own == k ? p16 : 0u;
+                    rem[k * (TPL / 2) + h] = P == 1 || own == k ? r16 : 0u;
                 }
+            }
+            const bf16x8 wh = __builtin_bit_cast(bf16x8, hi), wl = __builtin_bit_cast(bf16x8, rem);
+            // what 128 + c has over c: the same products with a tile of 128
+            off[d] = mfma_bf16(all128, wh, off[d]);
+            off[d] = mfma_bf16(all128, wl, off[d]);
+            const u32x4 vc = rec[D + d * 64 + lane];
+#pragma unroll
+            for (int t = 4 * d; t < 4 * d + 4; ++t) {
+                const bf16x8 v = q4_to_bf16_plus128(vc[t & 3]);
+                o[t] = mfma_bf16(v, wh, o[t]);
+                o[t] = mfma_bf16(v, wl, o[t]);
             }
         }
     }
 
-    // join the lanes of a row, then the waves and their columns
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-#pragma unroll
-    for (int d = 0; d < G; ++d) {
-        ob[d] += __shfl_xor(ob[d], 16, 64);
-        ob[d] += __shfl_xor(ob[d], 32, 64);
-    }
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-        reinterpret_cast<f32x4 *>(ring[wave])[t * 64 + lane] = (o[t] - off[t >> 2]) + ob[t >> 2];
-    if (g == 0) {
-        red_m[wave][c] = m;
-        red_l[wave][c] = l;
-    }
-    __syncthreads();
-    if (!live || own)
-        return;
-    float top = red_m[0][c];
-#pragma unroll
-    for (int w = 0; w < kWaves * P; ++w)
-        top = fmaxf(top, red_m[w / P][c + w % P * ROWS]);
-    float sum = 0.f, f[kWaves * P];
-#pragma unroll
-    for (int w = 0; w < kWaves * P; ++w) {
-        f[w] = exp2_fast(red_m[w / P][c + w % P * ROWS] - top);
-        sum += f[w] * red_l[w / P][c + w % P * ROWS];
-    }
-    const float inv = a.splits > 1 ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
-    const int64_t slot = ((int64_t)unit * a.splits + split) * ROWS + c;
-    if (a.splits > 1 && wave == 0 && g == 0) {
-        a.part_ml[2 * slot] = top;
-        a.part_ml[2 * slot + 1] = sum;
-    }
-#pragma unroll
-    for (int t0 = 0; t0 < DT; t0 += kWaves) {
-        const int t = t0 + wave;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kWaves * P; ++w)
-            v += reinterpret_cast<const f32x4 *>(ring[w / P])[t * 64 + lane + w % P * ROWS] * f[w];
-        v *= inv;
-        const int col = 16 * t + 4 * g;
-        if (a.splits > 1) {
-            *reinterpret_cast<f32x4 *>(a.part + slot * D + col) = v;
-        } else {
-            const int64_t at = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head + col;
-            if (a.o_bf16)
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + at) =
-                    u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
-            else
-                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + at) = v;
+    // join the lanes and columns of a row
+    {
+        auto more = [](float u, float v) { return fmaxf(u, v); };
+        auto sum = [](float u, float v) { return u + v; };
+        const float top = over_groups<P>(m, more);
+        float f = exp2_fast(m - top);
+        l += __shfl_xor(l, 16, 64);
+        l += __shfl_xor(l, 32, 64);
+        l = over_groups<P>(l * f, sum);
+        const float inv = !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        const int64_t slot = (int64_t)(me + unit) * ROWS + c;
+        const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head + 4 * g;
+        const bool mine = live && !own;
+        if (!complete && mine && g == 0) {
+            a.part_ml[2 * slot] = top;
+            a.part_ml[2 * slot + 1] = l;
         }
+#pragma unroll
+        for (int d = 0; d < G; ++d) {
+            ob[d] += __shfl_xor(ob[d], 16, 64);
+            ob[d] += __shfl_xor(ob[d], 32, 64);
+#pragma unroll
+            for (int t = 4 * d; t < 4 * d + 4; ++t) {
+                f32x4 v = ((o[t] - off[d]) + ob[d]) * f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = over_groups<P>(v[e], sum) * inv;
+                if (!mine)
+                    continue;
+                if (!complete)
+                    *reinterpret_cast<f32x4 *>(a.part + slot * D + 16 * t + 4 * g) = v;
+                else if (a.o_bf16)
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + to + 16 * t) =
+                        u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
+                else
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + to + 16 * t) = v;
+            }
+        }
+    }
+    if (!a.shared)
+        return;
+    if (lane == 0) { // for the join: the waves that share the tile
+        if (begin == 0)
+            a.spans[2 * unit] = me;
+        if (stop == view.count)
+            a.spans[2 * unit + 1] = me;
+    }
+    left -= stop - begin;
+    if (left <= 0)
+        return;
+    at = 0;
+    next_tile();
     }
 }
 
-// The ranges of a row added, by 256 / 64 / WPR rows a workgroup, WPR waves each: a
-// row's threads take its ranges' references and sums together, then its waves
-// the ranges in turn, D / 64 columns a lane, eight rows of partial sums on their
-// way at a time.
+// The ranges of a row added: by a wave, four rows a workgroup, or where they are
+// many by 16 waves and then one over those waves' results.  D / 8 lanes take a
+// range, eight columns each, so that a wave has 512 / D ranges at a time, four
+// times over; each group of lanes has a running reference as over tokens.  Bound
+// by latency, that of instructions not yet in the cache among it: the code is
+// short, and walks the ranges and the waves' results in one place.
 template <int D, int WPR>
-__global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int tile_rows) {
-    constexpr int V = D / 64, kAhead = 8, RPW = 4 / WPR, N = 64 * WPR;
-    typedef float vec __attribute__((ext_vector_type(V)));
-    __shared__ float fac[RPW][kMaxSplits], red[2][4];
-    __shared__ vec sums[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int me = threadIdx.x % N, mw = wave % WPR, slot_row = wave / WPR;
-    const int per_unit = (a.c.max_rows * a.group + RPW - 1) / RPW;
-    int b = blockIdx.x / per_unit;
-    const int rho = blockIdx.x % per_unit * RPW + slot_row;
-    const int tile = rho / tile_rows, unit = b * a.tiles + tile;
-    const int head = b % a.c.n_kv_heads, s = b / a.c.n_kv_heads;
+__global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(AttendArgs a, int tile_rows) {
+    constexpr int LPR = D / 8, AT_ONCE = 64 / LPR, AHEAD = 4, RPW = WPR == 1 ? 4 : 1;
+    __shared__ __attribute__((aligned(16))) float sums[WPR][D];
+    __shared__ float2 sums_ml[WPR];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int all_rows = a.c.max_rows * a.group;
+    const int b = quotient(blockIdx.x * RPW, a.by_rows);
+    const int rho = blockIdx.x * RPW - b * a.rows_up + (WPR == 1 ? wave : 0);
+    if (rho >= all_rows)
+        return;
+    const int tile = quotient(rho, a.by_tile_rows), unit = b * a.tiles + tile;
+    const int s = quotient(b, a.by_heads), head = b - s * a.c.n_kv_heads;
+    int from = 0, last = 0;
+    if (a.shared) {
+        from = a.spans[2 * unit];
+        last = a.spans[2 * unit + 1];
+    }
     const SeqRows q = seq_rows(a.c, s);
     const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
-    const bool live = rho < n * a.group;
-    if (WPR == 4 && !live)
+    if (rho >= n * a.group)
         return;
-    const int end = n * a.group < (tile + 1) * tile_rows ? n * a.group : (tile + 1) * tile_rows;
-    const int start = q.ctx - q.n;
-    TileView view = tile_view(a, start + tile * tile_rows / a.group, start + (end - 1) / a.group);
-    if (!live)
-        view.used = 0;
-    const int64_t slot0 = (int64_t)unit * a.splits * tile_rows + rho % tile_rows;
-
-    float top = kNoMax;
-    for (int k = me; k < view.used; k += N)
-        top = fmaxf(top, a.part_ml[2 * (slot0 + (int64_t)k * tile_rows)]);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        top = fmaxf(top, __shfl_xor(top, o, 64));
-    if (WPR > 1) {
-        red[0][wave] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    TileView view = view_of(a, q, tile, tile_rows, n * a.group - tile * tile_rows);
+    // its ranges: the splits in use, or those of the waves that shared it (one
+    // that had all of it has written the result)
+    int64_t slot0 = from + unit;
+    int used = last - from + 1;
+    if (!a.shared) {
+        divide(a, view);
+        used = view.used;
+        slot0 = (int64_t)unit * a.splits;
+    } else if (view.count == 0) {
+        used = 0;
+    } else if (used == 1) {
+        return;
     }
-    float sum = 0.f;
-    for (int k = me; k < view.used; k += N) {
-        const float *ml = a.part_ml + 2 * (slot0 + (int64_t)k * tile_rows);
-        const float f = exp2_fast(ml[0] - top);
-        fac[slot_row][k] = f;
-        sum += f * ml[1];
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        sum += __shfl_xor(sum, o, 64);
-    red[1][wave] = sum;
-    __syncthreads();
-    if (WPR > 1)
-        sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    slot0 = slot0 * tile_rows + rho - tile * tile_rows;
+    const float *part = a.part + slot0 * D;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + slot0;
+    int64_t step = tile_rows;
+    int first = WPR == 1 ? 0 : wave, stride = WPR;
 
-    const float *part = a.part + slot0 * D + lane * V;
-    const int64_t step = (int64_t)tile_rows * D;
-    vec v;
+    f32x4 v0, v1;
+    float top, sum;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+        v0 = v1 = f32x4{0.f, 0.f, 0.f, 0.f};
+        top = kNoMax;
+        sum = 0.f;
+#pragma unroll 1
+        for (int k0 = first * AT_ONCE + lane / LPR; k0 - lane / LPR < used; k0 += stride * AT_ONCE * AHEAD) {
+            f32x4 w[AHEAD][2];
+            float2 f[AHEAD];
+            float to = top;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        v[j] = 0.f;
-    for (int k = mw; k < view.used; k += WPR * kAhead) {
-        vec w[kAhead];
+            for (int i = 0; i < AHEAD; ++i) {
+                const int k = k0 + i * stride * AT_ONCE, at = k < used ? k : 0;
+                const f32x4 *p = reinterpret_cast<const f32x4 *>(part + at * step * D) + lane % LPR * 2;
+                f[i] = ml[at * step];
+                w[i][0] = p[0];
+                w[i][1] = p[1];
+                if (k >= used)
+                    f[i].x = -__builtin_inff();
+            }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int at = k + WPR * i;
-            w[i] = *reinterpret_cast<const vec *>(part + (at < view.used ? at : k) * step);
+            for (int i = 0; i < AHEAD; ++i)
+                to = fmaxf(to, f[i].x);
+            const float g = exp2_fast(top - to);
+            top = to;
+            v0 *= g;
+            v1 *= g;
+            sum *= g;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float e = exp2_fast(f[i].x - top);
+                if (k0 + i * stride * AT_ONCE < used) { // (not 0 times what is not a number)
+                    v0 += w[i][0] * e;
+                    v1 += w[i][1] * e;
+                    sum += f[i].y * e;
+                }
+            }
         }
+        // over the groups of lanes
+#pragma unroll 1
+        for (int o = LPR; o < 64; o <<= 1) {
+            const float other = __shfl_xor(top, o, 64), to = fmaxf(top, other);
+            const float e = exp2_fast(top - to), g = exp2_fast(other - to);
+            top = to;
+            sum = sum * e + __shfl_xor(sum, o, 64) * g;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (k + WPR * i < view.used)
-                v += w[i] * fac[slot_row][k + WPR * i];
-    }
-    if (WPR > 1) {
-        sums[wave][lane] = v;
+            for (int j = 0; j < 4; ++j) {
+                v0[j] = v0[j] * e + __shfl_xor(v0[j], o, 64) * g;
+                v1[j] = v1[j] * e + __shfl_xor(v1[j], o, 64) * g;
+            }
+        }
+        if (WPR == 1 || pass == 1)
+            break;
+        if (lane < LPR) {
+            reinterpret_cast<f32x4 *>(sums[wave])[lane * 2] = v0;
+            reinterpret_cast<f32x4 *>(sums[wave])[lane * 2 + 1] = v1;
+            sums_ml[wave] = make_float2(top, sum);
+        }
         __syncthreads();
         if (wave)
             return;
-        v = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+        part = sums[0];
+        ml = sums_ml;
+        step = 1;
+        used = WPR;
+        first = 0;
+        stride = 1;
     }
-    if (!live)
-        return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t at = (int64_t)(q.row0 + rho / a.group) * a.ldo +
-                       (head * a.group + rho % a.group) * a.o_head + lane * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (a.o_bf16)
-            static_cast<uint16_t *>(a.O)[at + j] = (uint16_t)pack_pair(v[j] * inv, 0.f);
-        else
-            static_cast<float *>(a.O)[at + j] = v[j] * inv;
+    const int i = quotient(rho, a.by_group);
+    const int64_t at = (int64_t)(q.row0 + i) * a.ldo + (head * a.group + rho - i * a.group) * a.o_head +
+                       lane * 8;
+    if (lane >= LPR)
+        return;
+    v0 *= inv;
+    v1 *= inv;
+    if (a.o_bf16) {
+        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.O) + at) =
+            u32x4{pack_pair(v0[0], v0[1]), pack_pair(v0[2], v0[3]), pack_pair(v1[0], v1[1]), pack_pair(v1[2], v1[3])};
+    } else {
+        f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + at);
+        o[0] = v0;
+        o[1] = v1;
     }
 }
 
 template <int D, int P> hipError_t decode(const AttendArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.tiles * a.splits));
+    const dim3 grid((unsigned)((a.parts + kWaves - 1) / kWaves));
     hipLaunchKernelGGL((attend_decode_kernel<D, P>), grid, dim3(64 * kWaves), 0, stream, a);
     return hipGetLastError();
 }
 
-template <int D> hipError_t join(int tile_rows, const AttendArgs &a, hipStream_t stream) {
+template <int D> hipError_t join(int tile_rows, AttendArgs a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.c.max_rows * a.group, units = (int64_t)a.c.n_seqs * a.c.n_kv_heads;
-    if (a.splits > kJoinWave)
-        hipLaunchKernelGGL((attend_join_kernel<D, 4>), dim3((unsigned)(units * rows)), dim3(256), 0, stream,
+    const bool many = a.splits > kJoinWave || (a.shared && a.parts / (units * a.tiles) > kJoinWave);
+    a.rows_up = (int32_t)(many ? rows : (rows + 3) / 4 * 4);
+    a.by_rows = make_div((uint32_t)a.rows_up);
+    a.by_tile_rows = make_div((uint32_t)tile_rows);
+    if (many)
+        hipLaunchKernelGGL((attend_join_kernel<D, 16>), dim3((unsigned)(units * rows)), dim3(1024), 0, stream,
                            a, tile_rows);
     else
-        hipLaunchKernelGGL((attend_join_kernel<D, 1>), dim3((unsigned)(units * ((rows + 3) / 4))), dim3(256),
+        hipLaunchKernelGGL((attend_join_kernel<D, 1>), dim3((unsigned)(units * (a.rows_up / 4))), dim3(256),
                            0, stream, a, tile_rows);
     return hipGetLastError();
 }
@@ -459,8 +615,9 @@ hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a
         return tile_rows == 4 ? decode<64, 4>(a, stream)
                               : (tile_rows == 8 ? decode<64, 2>(a, stream) : decode<64, 1>(a, stream));
     if (head_dim == 128)
-        return tile_rows == 8 ? decode<128, 2>(a, stream) : decode<128, 1>(a, stream);
-    return decode<256, 1>(a, stream);
+        return tile_rows == 4 ? decode<128, 4>(a, stream)
+                              : (tile_rows == 8 ? decode<128, 2>(a, stream) : decode<128, 1>(a, stream));
+    return tile_rows == 8 ? decode<256, 2>(a, stream) : decode<256, 1>(a, stream);
 }
 
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream) {

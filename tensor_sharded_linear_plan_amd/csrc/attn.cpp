@@ -194,6 +194,8 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
 // How cache_attention divides its work; a function of sizes alone.
 struct AttendPlan {
     int32_t tile_rows, tiles, splits, min_share;
+    int32_t shared, parts;
+    int64_t units, ranges;  // (sequence, head, tile); ranges with sums of their own
     size_t bytes;
 };
 
@@ -201,39 +203,52 @@ struct AttendPlan {
 // few rows, where every tile of 16 expands the records it reads anew.
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kCUs = 256;
-// Records of a range: at least what is worth it (few rows: two steps of each of
-// four waves; many: enough to outweigh the join), and with few rows at most so
-// many, so that sequences of different lengths end together.
-constexpr int kPromptShare = 16, kAttendMost = 64;
+// Records that a wave takes alone, with no join after it: 0.9 us each, and a join
+// 5 us.
+constexpr int kWholeRecords = 6;
+// Records that are worth a wave of their own with few rows, and a workgroup's
+// range with many.
+constexpr int kAttendShare = 1, kPromptShare = 16;
 
 tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
                        int32_t sinks, AttendPlan *p) {
     const int64_t group = n_q_heads / c.n_kv_heads;
     const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
+    if (rows > kMaxContext)
+        return TSL_ERR_UNSUPPORTED;
     const bool few = rows <= kFewRows || c.head_dim > 128;
-    const int at_once = c.head_dim > 128 || rows > 8 ? 1 : (c.head_dim == 64 && rows <= 4 ? 4 : 2);
-    p->tile_rows = few ? 16 / at_once : kPromptRows;
+    p->tile_rows = !few ? kPromptRows : (rows > 8 ? 16 : (rows > 4 || c.head_dim > 128 ? 8 : 4));
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
     if (window)
         seen = std::min<int64_t>(seen, (int64_t)window + sinks + p->tile_rows + 2 * kBlock);
     const int64_t records = (seen + kBlock - 1) / kBlock;
     p->tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
-    const int64_t units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
-    // a workgroup for every place there is, where the tokens allow it
-    const int64_t target = kCUs * (few ? attend_groups(c.head_dim, at_once) : 1);
-    p->min_share = few ? 8 * at_once : kPromptShare;
-    int64_t splits = units > 0 ? target / units : 1;
-    if (few)
-        splits = std::max<int64_t>(splits, (records + kAttendMost - 1) / kAttendMost);
-    splits = std::min<int64_t>(splits, (records + p->min_share - 1) / p->min_share);
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
-    p->splits = (int32_t)splits;
-    if (units * splits > kMaxBlocks ||
-        (splits > 1 && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
+    p->units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
+    p->min_share = few ? kAttendShare : kPromptShare;
+    const int64_t most = std::max<int64_t>(1, (records + p->min_share - 1) / p->min_share);
+    p->shared = 0;
+    p->splits = 1;
+    p->parts = (int32_t)std::min<int64_t>(p->units, kMaxBlocks + 1);
+    p->ranges = 0;
+    // (a call of more sequences than that has several tiles for every wave as it
+    // is; records are counted in 32 bits)
+    const int64_t held = ((int64_t)q.max_pages * c.page_tokens + kBlock - 1) / kBlock;
+    if (few && records > kWholeRecords && q.n_seqs <= kMaxShared && p->units * held <= INT32_MAX) {
+        p->shared = 1;
+        const int64_t places = kCUs * 4 * attend_groups(c.head_dim); // waves that fit
+        p->parts = (int32_t)std::min(places, p->units * most);
+        p->ranges = p->parts + p->units;
+    }
+    if (!few) {
+        p->splits = (int32_t)std::max<int64_t>(
+            1, std::min({most, (int64_t)kMaxSplits, p->units > 0 ? kCUs / p->units : 1}));
+        p->ranges = p->splits > 1 ? p->units * p->splits : 0;
+    }
+    if (p->parts > kMaxBlocks || p->units > kMaxBlocks ||
+        (p->ranges && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    p->bytes = splits > 1
-                   ? (size_t)(units * splits) * p->tile_rows * (size_t)(c.head_dim + 2) * 4
-                   : 0;
+    p->bytes = (size_t)p->ranges * p->tile_rows * (size_t)(c.head_dim + 2) * 4 +
+               (p->shared ? (size_t)p->units * 8 : 0);
     return TSL_OK;
 }
 
@@ -418,18 +433,26 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     a.sinks = sinks;
     a.o_bf16 = odtype == TSL_BF16;
     a.tiles = p.tiles;
+    a.by_group = make_div((uint32_t)a.group);
+    a.by_tiles = make_div((uint32_t)p.tiles);
+    a.by_heads = make_div((uint32_t)cache->n_kv_heads);
+    a.by_splits = make_div((uint32_t)p.splits);
     a.splits = p.splits;
+    a.shared = p.shared;
+    a.parts = p.parts;
+    a.by_parts = make_div((uint32_t)p.parts);
+    a.units = (int32_t)p.units;
     a.min_share = p.min_share;
-    if (p.bytes) {
+    if (p.ranges) {
         a.part = static_cast<float *>(workspace);
-        a.part_ml = a.part + (int64_t)a.c.n_seqs * a.c.n_kv_heads * p.tiles * p.splits *
-                                 p.tile_rows * cache->head_dim;
+        a.part_ml = a.part + p.ranges * p.tile_rows * cache->head_dim;
+        a.spans = reinterpret_cast<int32_t *>(a.part_ml + p.ranges * p.tile_rows * 2);
     }
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     hipError_t e = p.tile_rows < kPromptRows
                        ? launch_attend_decode(cache->head_dim, p.tile_rows, a, hs)
                        : launch_attend_prompt(cache->head_dim, a, hs);
-    if (e == hipSuccess && p.splits > 1)
+    if (e == hipSuccess && p.ranges)
         e = launch_attend_join(cache->head_dim, p.tile_rows, a, hs);
     return from_hip(e);
 }

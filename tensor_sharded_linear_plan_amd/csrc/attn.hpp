@@ -62,6 +62,24 @@ struct MoveArgs {
 hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream);
 hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream);
 
+// Division of numbers below 2^31 by one that the host knows: a product's upper
+// half and a shift, where the compiler's division takes 35 instructions -- of
+// which a workgroup's start would have a dozen.
+struct Div {
+    uint32_t mul, shift;
+};
+inline Div make_div(uint32_t d) {
+    Div v = {0, 0};
+    while ((uint64_t(1) << v.shift) < d)
+        ++v.shift;
+    v.mul = (uint32_t)((((uint64_t(1) << v.shift) - d) << 32) / d + 1);
+    return v;
+}
+__host__ __device__ __forceinline__ int quotient(int n, Div d) {
+    const uint32_t hi = (uint32_t)(((uint64_t)(uint32_t)n * d.mul) >> 32);
+    return (int)((hi + (uint32_t)n) >> d.shift);
+}
+
 struct AttendArgs {
     CacheArgs c;
     const uint16_t *Q;
@@ -69,20 +87,31 @@ struct AttendArgs {
     int64_t ldq, q_head, ldo, o_head;
     float scale; // times log2 e
     int32_t group, window, sinks, o_bf16;
+    Div by_group, by_tiles, by_heads, by_splits, by_parts; // heads: of the cache
     int32_t tiles;     // row tiles of a sequence and K/V head
-    int32_t splits;    // ranges of tokens a tile is divided into at most
-    int32_t min_share; // records of a range at least
-    float *part;       // [seq][head][tile][split][tile rows][head_dim], splits > 1
-    float *part_ml;    // ... [tile rows][2]: reference exponent and sum
+    int32_t splits;    // ranges of tokens a tile is divided into at most (many rows)
+    int32_t shared;    // few rows: all records of the call in a row, cut into parts
+    int32_t parts;     // few rows: waves
+    int32_t units;     // sequences * heads * tiles
+    int32_t min_share; // records of a range or part at least
+    // sums of ranges: [range][tile rows][head_dim], and of each row its reference
+    // exponent and sum; range = unit * splits + split, or unit + wave, with
+    // unit = (sequence * heads + head) * tiles + tile
+    float *part, *part_ml;
+    int32_t *spans; // shared: the first and last wave of each unit
+    int32_t rows_up; // the join: a unit's rows, rounded up to a workgroup's
+    Div by_rows, by_tile_rows;
 };
 
-constexpr int kMaxSplits = 512;
-constexpr int kJoinWave = 32; // ranges that one wave adds; a workgroup more
-// attend_decode: tiles of 16 / P query rows, P records at a time (P = 2 with
-// head_dim up to 128, 4 with 64), two stages of them for each of four waves in a
-// CU's 160 KB of LDS.  Workgroups that share a CU:
-constexpr int attend_groups(int head_dim, int p) {
-    const int n = 160 * 1024 / (4 * 2 * p * record_bytes(head_dim) + 512);
+constexpr int kMaxSplits = 1024;
+constexpr int kMaxWaves = 4096;  // parts of a shared call: 16 waves on each of 256 CUs
+constexpr int kMaxShared = 1024; // sequences of a shared call
+constexpr int kJoinWave = 16; // ranges that one wave adds; 16 waves more
+// attend_decode: tiles of 16 / P query rows (P 1, 2, or with head_dim up to 128 4),
+// three stages of a record for each of four waves in a CU's 160 KB of LDS.
+// Workgroups that share a CU (four: a start more a CU does not hide better):
+constexpr int attend_groups(int head_dim) {
+    const int n = 160 * 1024 / (4 * 3 * record_bytes(head_dim));
     return n > 4 ? 4 : n;
 }
 
@@ -135,8 +164,8 @@ __host__ __device__ __forceinline__ TileView tile_view(const AttendArgs &a, int 
     TileView v;
     v.first = first;
     v.last = last;
-    const int64_t cap = (int64_t)a.c.max_pages << (a.c.shift + 5);
-    const int end = last + 1 < cap ? last + 1 : (int)cap; // tokens below it
+    const int cap = a.c.max_pages << (a.c.shift + 5); // at most 2^30
+    const int end = last + 1 < cap ? last + 1 : cap;  // tokens below it
     v.lead = v.from = v.count = 0;
     if (end > 0) {
         int lo = a.window && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
@@ -147,10 +176,19 @@ __host__ __device__ __forceinline__ TileView tile_view(const AttendArgs &a, int 
         v.lead = lead < v.from ? lead : v.from;
         v.count = v.lead + ((end + 31) >> 5) - v.from;
     }
-    v.share = (v.count + a.splits - 1) / a.splits;
+    return v;
+}
+// Its ranges where a tile is divided into at most a.splits.
+__host__ __device__ __forceinline__ void divide(const AttendArgs &a, TileView &v) {
+    v.share = quotient(v.count + a.splits - 1, a.by_splits);
     v.share = v.share > a.min_share ? v.share : a.min_share;
     v.used = (v.count + v.share - 1) / v.share;
-    return v;
+}
+// What tile `tile` of `tile_rows` query rows sees; `rows` of it and later ones.
+__host__ __device__ __forceinline__ TileView view_of(const AttendArgs &a, const SeqRows &q, int tile,
+                                                     int tile_rows, int rows) {
+    const int last = tile * tile_rows + (rows < tile_rows ? rows : tile_rows) - 1, start = q.ctx - q.n;
+    return tile_view(a, start + quotient(tile * tile_rows, a.by_group), start + quotient(last, a.by_group));
 }
 __host__ __device__ __forceinline__ int view_block(const TileView &v, int i) {
     return i < v.lead ? i : v.from + i - v.lead;

@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     // a long sequence at the same place of each round would keep to one of them
     // (prompts of 2500, 267, 1756 and 1630 tokens ran in 651 us that way, in
     // 423 us so).
-    int b = blockIdx.x;
-    const int split = b % a.splits;
-    b /= a.splits;
+    int b = quotient(blockIdx.x, a.by_splits);
+    const int split = blockIdx.x - b * a.splits;
     const int heads = a.c.n_seqs * a.c.n_kv_heads;
     const int tile = a.tiles - 1 - b / heads;
     b %= heads;
-    const int head = b % a.c.n_kv_heads, s = (b / a.c.n_kv_heads + tile) % a.c.n_seqs;
+    const int turn = quotient(b, a.by_heads), head = b - turn * a.c.n_kv_heads;
+    const int s = (turn + tile) % a.c.n_seqs;
     const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
     const SeqRows q = seq_rows(a.c, s);
     const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         return;
     const int start = q.ctx - q.n;
     const int last_rho = tile * kRows + (rows < kRows ? rows : kRows) - 1;
-    const TileView view = tile_view(a, start + tile * kRows / a.group, start + last_rho / a.group);
+    TileView view = view_of(a, q, tile, kRows, rows);
+    divide(a, view);
     const int begin = split * view.share;
     const int stop = begin + view.share < view.count ? begin + view.share : view.count;
     if (begin >= stop && split > 0)
@@ -132,13 +133,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     const int mine = wave * 32 + c;
     const bool live = mine < rows;
     const int rho = live ? tile * kRows + mine : last_rho;
-    const int i = rho / a.group, hq = head * a.group + rho % a.group;
+    const int i = quotient(rho, a.by_group), hq = head * a.group + rho - i * a.group;
     const int pos = start + i, lo = window_start(a, pos);
     const bool idle = wave * 32 >= rows;
     const int wave_last = wave * 32 + 31 < rows ? tile * kRows + wave * 32 + 31 : last_rho;
     TileView wv = view;
-    wv.first = __builtin_amdgcn_readfirstlane(start + (tile * kRows + wave * 32) / a.group);
-    wv.last = __builtin_amdgcn_readfirstlane(start + wave_last / a.group);
+    wv.first = __builtin_amdgcn_readfirstlane(start + quotient(tile * kRows + wave * 32, a.by_group));
+    wv.last = __builtin_amdgcn_readfirstlane(start + quotient(wave_last, a.by_group));
 
     // Q as binary16, its largest element in 2^14 .. 2^15; the scale's sign goes
     // to it, so that the largest product is the largest logit

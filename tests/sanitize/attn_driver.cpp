@@ -80,7 +80,9 @@ static void views() {
         a.splits = 1 + pick(9);
         a.min_share = 1 + pick(9);
         const int first = pick(500) - 20, last = first + pick(70);
-        const TileView v = tile_view(a, first, last);
+        a.by_splits = make_div((uint32_t)a.splits);
+        TileView v = tile_view(a, first, last);
+        divide(a, v);
         const int cap = a.c.max_pages << (a.c.shift + 5);
         std::vector<int> list;
         for (int i = 0; i < v.count; ++i)
@@ -130,6 +132,21 @@ static void views() {
     }
 }
 
+// Division by the host's multipliers is exact below 2^31.
+static void divisions() {
+    for (int round = 0; round < 200000; ++round) {
+        const uint32_t d = round < 5000 ? 1 + round : 1 + (state >> 1) % (1u << (1 + pick(30)));
+        const Div v = make_div(d);
+        for (int k = 0; k < 4; ++k) {
+            state = state * 1664525u + 1013904223u;
+            const int n = k == 0 ? INT32_MAX : (int)(state >> 1);
+            EXPECT(quotient(n, v) == (int)((uint32_t)n / d));
+            const int m = (int)(n / d * d); // a multiple, and the number before it
+            EXPECT(quotient(m, v) == (int)(m / d) && (m == 0 || quotient(m - 1, v) == (int)((m - 1) / d)));
+        }
+    }
+}
+
 static void calls() {
     size_t b = 0;
     tsl_cache c = {addr(1 << 20), 10, 64, 2, 128};
@@ -162,6 +179,7 @@ static void calls() {
 int main() {
     records();
     views();
+    divisions();
     calls();
     if (!failures)
         printf("all checks passed\n");

@@ -252,7 +252,7 @@ def test_equal_calls_give_equal_bits_and_sizes_are_hints():
     check(first, Q, b, K, V, hq, d ** -0.5, 0, 0, "bf16", False)
     for _ in range(3):
         assert torch().equal(run(pages, b, hq, q, d ** -0.5)[1].buf, first.buf)
-    for hint in (1, 64, 10 ** 9):
+    for hint in (1, 64, 300, 700, 10 ** 9):
         Q, O = run(pages, b, hq, q, d ** -0.5, max_context=hint)
         check(O, Q, b, K, V, hq, d ** -0.5, 0, 0, "bf16", False)
 
