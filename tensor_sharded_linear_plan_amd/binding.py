@@ -21,6 +21,7 @@ runtime.
 """
 import ctypes
 import os
+import struct
 
 try:  # see the module docstring: torch's HIP runtime must be loaded first
     import torch as _torch  # noqa: F401
@@ -259,17 +260,15 @@ BLOCK_EXPORTS = ("add_rms_norm", "add_rms_norm_grad_workspace_size", "add_rms_no
 for _f in BLOCK_EXPORTS[:-1]:
     getattr(_block, _f).restype = ctypes.c_int
 
-_P_CACHE, _P_SEQS = ctypes.POINTER(Cache), ctypes.POINTER(Seqs)
-_attn.rotate_heads.argtypes = [_i32, ctypes.POINTER(RotateItem), _i64, ctypes.POINTER(Rotary),
-                               ctypes.c_int, _vp]
-_attn.cache_size.argtypes = [_P_CACHE, ctypes.POINTER(_sz)]
+# (their structures go as the bytes that a call packs: a generated token's calls
+# are short enough for the marshalling to count)
+_attn.rotate_heads.argtypes = [_i32, _vp, _i64, _vp, ctypes.c_int, _vp]
+_attn.cache_size.argtypes = [_vp, ctypes.POINTER(_sz)]
 for _f in ("cache_append", "cache_read"):
-    getattr(_attn, _f).argtypes = [_P_CACHE, _P_SEQS, ctypes.c_int, _vp, _i64, _i64, _vp, _i64, _i64,
-                                   _vp]
-_attn.cache_attention_workspace_size.argtypes = [_P_CACHE, _P_SEQS, _i32, _i32, _i32,
-                                                 ctypes.POINTER(_sz)]
-_attn.cache_attention.argtypes = [_P_CACHE, _P_SEQS, _i32, _vp, _i64, _i64, ctypes.c_float, _i32,
-                                  _i32, ctypes.c_int, _vp, _i64, _i64, _vp, _sz, _vp]
+    getattr(_attn, _f).argtypes = [_vp, _vp, ctypes.c_int, _vp, _i64, _i64, _vp, _i64, _i64, _vp]
+_attn.cache_attention_workspace_size.argtypes = [_vp, _vp, _i32, _i32, _i32, ctypes.POINTER(_sz)]
+_attn.cache_attention.argtypes = [_vp, _vp, _i32, _vp, _i64, _i64, ctypes.c_float, _i32, _i32,
+                                  ctypes.c_int, _vp, _i64, _i64, _vp, _sz, _vp]
 _attn.tsl_attn_last_hip_error_string.argtypes = []
 _attn.tsl_attn_last_hip_error_string.restype = ctypes.c_char_p
 
@@ -614,77 +613,81 @@ def shard_gated_grad(gate, up, wdtype, packed_gate_t, packed_up_t, packed_t_byte
            "shard_gated_grad")
 
 
+# layouts of Rotary, RotateItem, Cache and Seqs
+_ROTARY, _ROTATE_ITEM = struct.Struct("=QqQQiiii"), struct.Struct("=QqqQqqiii4x")
+_CACHE, _SEQS = struct.Struct("=Qqiii4x"), struct.Struct("=QQQqqiiii")
+
+
 def _rotary(r):
     """r: a dict (or Rotary) with the tsl_rotary fields; pair_axis a sequence of
-    axes or None (style defaults to ROTARY_HALVES, axes to 1, ld_pos to 0)."""
+    axes or None (style defaults to ROTARY_HALVES, axes to 1, ld_pos to 0).
+    Returns its bytes and what they point to."""
     if isinstance(r, Rotary):
-        return r
-    axis = r.get("pair_axis")
+        return bytes(r), None
+    get, axis, keep = r.get, r.get("pair_axis"), None
     if axis is not None:
         if len(axis) != r["rot_dim"] // 2:
             raise ValueError("one axis per pair")
-        axis = (ctypes.c_uint8 * max(len(axis), 1))(*axis)
-    out = Rotary(_ptr(r["positions"]), r.get("ld_pos", 0), _ptr(r["freq"]),
-                 ctypes.cast(axis, ctypes.c_void_p) if axis is not None else None,
-                 r.get("axes", 1), r["rot_dim"], r["head_dim"], r.get("style", ROTARY_HALVES))
-    out._keep = axis
-    return out
+        keep = ctypes.create_string_buffer(bytes(axis), max(len(axis), 1))
+    return _ROTARY.pack(_ptr(r["positions"]) or 0, get("ld_pos", 0), _ptr(r["freq"]) or 0,
+                        ctypes.addressof(keep) if keep is not None else 0, get("axes", 1),
+                        r["rot_dim"], r["head_dim"], get("style", ROTARY_HALVES)), keep
 
 
 def rotate_heads(items, M, rotary, inverse=0, stream=None):
     """items: sequence of dicts (or RotateItem) with the tsl_rotate_item fields."""
-    n = len(items)
-    arr = (RotateItem * max(n, 1))()
-    for i, it in enumerate(items):
-        arr[i] = it if isinstance(it, RotateItem) else \
-            RotateItem(_ptr(it["X"]), it["ldx"], it["x_head"], _ptr(it["Y"]), it["ldy"],
-                       it["y_head"], it["n_heads"], it["xdtype"], it["ydtype"])
-    r = _rotary(rotary)
-    _check(_attn.rotate_heads(n, arr, M, ctypes.byref(r), inverse, _stream(stream)), "rotate_heads")
+    arr = b"".join([bytes(i) if isinstance(i, RotateItem) else
+                    _ROTATE_ITEM.pack(_ptr(i["X"]) or 0, i["ldx"], i["x_head"], _ptr(i["Y"]) or 0,
+                                      i["ldy"], i["y_head"], i["n_heads"], i["xdtype"], i["ydtype"])
+                    for i in items])
+    r, keep = _rotary(rotary)
+    _check(_attn.rotate_heads(len(items), arr, M, r, inverse, _stream(stream)), "rotate_heads")
 
 
 def _cache(c):
     """c: a dict (or Cache) with the tsl_cache fields."""
-    return c if isinstance(c, Cache) else Cache(_ptr(c.get("pages")), c["n_pages"], c["page_tokens"],
-                                                c["n_kv_heads"], c["head_dim"])
+    if isinstance(c, Cache):
+        return bytes(c)
+    return _CACHE.pack(_ptr(c.get("pages")) or 0, c["n_pages"], c["page_tokens"], c["n_kv_heads"],
+                       c["head_dim"])
 
 
 def _seqs(q):
     """q: a dict (or Seqs) with the tsl_seqs fields (the arrays default to
     None, for size queries)."""
-    return q if isinstance(q, Seqs) else Seqs(_ptr(q.get("row_start")), _ptr(q.get("context")),
-                                              _ptr(q.get("page_table")), q.get("ld_table", 0),
-                                              q["rows"], q["n_seqs"], q["max_rows"],
-                                              q["max_context"], q["max_pages"])
+    if isinstance(q, Seqs):
+        return bytes(q)
+    get = q.get
+    return _SEQS.pack(_ptr(get("row_start")) or 0, _ptr(get("context")) or 0,
+                      _ptr(get("page_table")) or 0, get("ld_table", 0), q["rows"], q["n_seqs"],
+                      q["max_rows"], q["max_context"], q["max_pages"])
 
 
 def cache_size(cache):
     b = _sz(0)
-    _check(_attn.cache_size(ctypes.byref(_cache(cache)), ctypes.byref(b)), "cache_size")
+    _check(_attn.cache_size(_cache(cache), ctypes.byref(b)), "cache_size")
     return b.value
 
 
 def cache_append(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, stream=None):
-    _check(_attn.cache_append(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), dtype, _ptr(K),
-                              ldk, k_head, _ptr(V), ldv, v_head, _stream(stream)), "cache_append")
+    _check(_attn.cache_append(_cache(cache), _seqs(seqs), dtype, _ptr(K), ldk, k_head, _ptr(V), ldv,
+                              v_head, _stream(stream)), "cache_append")
 
 
 def cache_read(cache, seqs, dtype, K, ldk, k_head, V, ldv, v_head, stream=None):
-    _check(_attn.cache_read(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), dtype, _ptr(K),
-                            ldk, k_head, _ptr(V), ldv, v_head, _stream(stream)), "cache_read")
+    _check(_attn.cache_read(_cache(cache), _seqs(seqs), dtype, _ptr(K), ldk, k_head, _ptr(V), ldv,
+                            v_head, _stream(stream)), "cache_read")
 
 
 def cache_attention_workspace_size(cache, seqs, n_q_heads, window=0, sinks=0):
     b = _sz(0)
-    _check(_attn.cache_attention_workspace_size(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)),
-                                                n_q_heads, window, sinks, ctypes.byref(b)),
-           "cache_attention_workspace_size")
+    _check(_attn.cache_attention_workspace_size(_cache(cache), _seqs(seqs), n_q_heads, window, sinks,
+                                                ctypes.byref(b)), "cache_attention_workspace_size")
     return b.value
 
 
 def cache_attention(cache, seqs, n_q_heads, Q, ldq, q_head, scale, window, sinks, odtype, O, ldo,
                     o_head, workspace=None, ws_bytes=0, stream=None):
-    _check(_attn.cache_attention(ctypes.byref(_cache(cache)), ctypes.byref(_seqs(seqs)), n_q_heads,
-                                 _ptr(Q), ldq, q_head, scale, window, sinks, odtype, _ptr(O), ldo,
-                                 o_head, _ptr(workspace), ws_bytes, _stream(stream)),
-           "cache_attention")
+    _check(_attn.cache_attention(_cache(cache), _seqs(seqs), n_q_heads, _ptr(Q), ldq, q_head, scale,
+                                 window, sinks, odtype, _ptr(O), ldo, o_head, _ptr(workspace),
+                                 ws_bytes, _stream(stream)), "cache_attention")

@@ -187,6 +187,8 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
     a.ldv = ldv;
     a.v_head = v_head;
     a.bf16 = dtype == TSL_BF16;
+    a.by_heads = make_div((uint32_t)a.c.n_kv_heads);
+    a.by_blocks = make_div((uint32_t)std::max(a.seq_blocks, 1));
     *out = a;
     return TSL_OK;
 }

@@ -51,17 +51,6 @@ struct CacheArgs {
     int32_t rows, n_seqs, max_rows, max_pages;
 };
 
-struct MoveArgs {
-    CacheArgs c;
-    void *K, *V;
-    int64_t ldk, k_head, ldv, v_head;
-    int32_t bf16;
-    int32_t seq_blocks; // records a sequence's rows may span
-};
-
-hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream);
-hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream);
-
 // Division of numbers below 2^31 by one that the host knows: a product's upper
 // half and a shift, where the compiler's division takes 35 instructions -- of
 // which a workgroup's start would have a dozen.
@@ -79,6 +68,18 @@ __host__ __device__ __forceinline__ int quotient(int n, Div d) {
     const uint32_t hi = (uint32_t)(((uint64_t)(uint32_t)n * d.mul) >> 32);
     return (int)((hi + (uint32_t)n) >> d.shift);
 }
+
+struct MoveArgs {
+    CacheArgs c;
+    void *K, *V;
+    int64_t ldk, k_head, ldv, v_head;
+    int32_t bf16;
+    int32_t seq_blocks; // records a sequence's rows may span
+    Div by_heads, by_blocks;
+};
+
+hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream);
+hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream);
 
 struct AttendArgs {
     CacheArgs c;
