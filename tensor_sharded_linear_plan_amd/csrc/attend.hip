@@ -70,7 +70,7 @@ template <int ROWS> __device__ __forceinline__ Part part_of(const AttendArgs &a,
         int own = 0;
         if (base + lane < a.c.n_seqs) {
             q = seq_rows(a.c, base + lane);
-            int rows = (q.n < a.c.max_rows ? q.n : a.c.max_rows) * a.group;
+            int rows = rows_of(a, q);
             for (int t = 0; rows > 0; ++t, rows -= ROWS)
                 own += view_of(a, q, t, ROWS, rows).count;
         }
@@ -175,8 +175,7 @@ __global__ void __launch_bounds__(64 * kWaves, attend_groups(D)) attend_decode_k
     };
     while (true) {
     const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
-    const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
-    const int rows = n * a.group - tile * ROWS; // of this tile and later ones
+    const int rows = rows_of(a, q) - tile * ROWS; // of this tile and later ones
     TileView view = {0, 0, 0, 0, 0, 0, 0};
     if (rows > 0)
         view = view_of(a, q, tile, ROWS, rows);
@@ -463,10 +462,9 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
     __shared__ float2 sums_ml[WPR];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int all_rows = a.c.max_rows * a.group;
     const int b = quotient(blockIdx.x * RPW, a.by_rows);
     const int rho = blockIdx.x * RPW - b * a.rows_up + (WPR == 1 ? wave : 0);
-    if (rho >= all_rows)
+    if (rho >= a.rows)
         return;
     const int tile = quotient(rho, a.by_tile_rows), unit = b * a.tiles + tile;
     const int s = quotient(b, a.by_heads), head = b - s * a.c.n_kv_heads;
@@ -476,10 +474,10 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
         last = a.spans[2 * unit + 1];
     }
     const SeqRows q = seq_rows(a.c, s);
-    const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
-    if (rho >= n * a.group)
+    const int rows = rows_of(a, q);
+    if (rho >= rows)
         return;
-    TileView view = view_of(a, q, tile, tile_rows, n * a.group - tile * tile_rows);
+    TileView view = view_of(a, q, tile, tile_rows, rows - tile * tile_rows);
     // its ranges: the splits in use, or those of the waves that shared it (one
     // that had all of it has written the result)
     int64_t slot0 = from + unit;
@@ -594,7 +592,7 @@ template <int D, int P> hipError_t decode(const AttendArgs &a, hipStream_t strea
 }
 
 template <int D> hipError_t join(int tile_rows, AttendArgs a, hipStream_t stream) {
-    const int64_t rows = (int64_t)a.c.max_rows * a.group, units = (int64_t)a.c.n_seqs * a.c.n_kv_heads;
+    const int64_t rows = a.rows, units = (int64_t)a.c.n_seqs * a.c.n_kv_heads;
     const bool many = a.splits > kJoinWave || (a.shared && a.parts / (units * a.tiles) > kJoinWave);
     a.rows_up = (int32_t)(many ? rows : (rows + 3) / 4 * 4);
     a.by_rows = make_div((uint32_t)a.rows_up);

@@ -193,16 +193,17 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
     return TSL_OK;
 }
 
-// How cache_attention divides its work; a function of sizes alone.
+// How one of cache_attention's kernels divides its work; a function of sizes alone.
 struct AttendPlan {
+    int32_t rows;      // query rows of a sequence and K/V head, at most
     int32_t tile_rows, tiles, splits, min_share;
     int32_t shared, parts;
-    int64_t units, ranges;  // (sequence, head, tile); ranges with sums of their own
+    int64_t units, ranges; // (sequence, head, tile); ranges with sums of their own
     size_t bytes;
 };
 
-// Query rows of a sequence and K/V head up to which a call takes the kernel of
-// few rows, where every tile of 16 expands the records it reads anew.
+// Query rows of a sequence and K/V head up to which the kernel of few rows takes
+// it, where every tile of 16 expands the records it reads anew.
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kCUs = 256;
 // Records that a wave takes alone, with no join after it: 0.9 us each, and a join
@@ -212,19 +213,15 @@ constexpr int kWholeRecords = 6;
 // range with many.
 constexpr int kAttendShare = 1, kPromptShare = 16;
 
-tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
-                       int32_t sinks, AttendPlan *p) {
-    const int64_t group = n_q_heads / c.n_kv_heads;
-    const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
-    if (rows > kMaxContext)
-        return TSL_ERR_UNSUPPORTED;
-    const bool few = rows <= kFewRows || c.head_dim > 128;
-    p->tile_rows = !few ? kPromptRows : (rows > 8 ? 16 : (rows > 4 || c.head_dim > 128 ? 8 : 4));
+tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool few, int tile_rows,
+                       int32_t window, int32_t sinks, AttendPlan *p) {
+    p->rows = (int32_t)rows;
+    p->tile_rows = tile_rows;
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
     if (window)
-        seen = std::min<int64_t>(seen, (int64_t)window + sinks + p->tile_rows + 2 * kBlock);
+        seen = std::min<int64_t>(seen, (int64_t)window + sinks + tile_rows + 2 * kBlock);
     const int64_t records = (seen + kBlock - 1) / kBlock;
-    p->tiles = (int32_t)((rows + p->tile_rows - 1) / p->tile_rows);
+    p->tiles = (int32_t)((rows + tile_rows - 1) / tile_rows);
     p->units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
     p->min_share = few ? kAttendShare : kPromptShare;
     const int64_t most = std::max<int64_t>(1, (records + p->min_share - 1) / p->min_share);
@@ -246,12 +243,40 @@ tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads,
             1, std::min({most, (int64_t)kMaxSplits, p->units > 0 ? kCUs / p->units : 1}));
         p->ranges = p->splits > 1 ? p->units * p->splits : 0;
     }
-    if (p->parts > kMaxBlocks || p->units > kMaxBlocks ||
+    if (p->parts > kMaxBlocks || p->units * p->splits > kMaxBlocks ||
         (p->ranges && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    p->bytes = (size_t)p->ranges * p->tile_rows * (size_t)(c.head_dim + 2) * 4 +
-               (p->shared ? (size_t)p->units * 8 : 0);
+    p->bytes = round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +
+                            (p->shared ? (size_t)p->units * 8 : 0),
+                        256);
     return TSL_OK;
+}
+
+// The kernels of a call: of few rows, of many, or both, each for the sequences of
+// its kind.  A lone sequence goes by max_rows.
+struct AttendPlans {
+    bool few, many;
+    AttendPlan f, m;
+    size_t bytes() const { return (few ? f.bytes : 0) + (many ? m.bytes : 0); }
+};
+
+tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads, int32_t window,
+                       int32_t sinks, AttendPlans *p) {
+    const int64_t group = n_q_heads / c.n_kv_heads;
+    const int64_t rows = std::min<int64_t>(q.max_rows, q.rows) * group;
+    if (rows > kMaxContext)
+        return TSL_ERR_UNSUPPORTED;
+    p->many = rows > kFewRows && c.head_dim <= 128;
+    p->few = !p->many || q.n_seqs > 1;
+    if (p->few) {
+        // beside long sequences most of the others have one row
+        const int64_t most = p->many ? kFewRows : rows, typical = p->many ? group : rows;
+        const int tile = typical > 8 ? 16 : (typical > 4 || c.head_dim > 128 ? 8 : 4);
+        const tsl_status st = plan_kernel(c, q, most, true, tile, window, sinks, &p->f);
+        if (st != TSL_OK)
+            return st;
+    }
+    return p->many ? plan_kernel(c, q, rows, false, kPromptRows, window, sinks, &p->m) : TSL_OK;
 }
 
 tsl_status attend_check(const tsl_cache *cache, const tsl_seqs *seqs, int32_t n_q_heads,
@@ -382,9 +407,9 @@ extern "C" tsl_status cache_attention_workspace_size(const tsl_cache *cache, con
     if (!bytes)
         return TSL_ERR_INVALID_ARG;
     tsl_status st = attend_check(cache, seqs, n_q_heads, window, sinks, false);
-    AttendPlan p;
+    AttendPlans p;
     if (st == TSL_OK && (st = attend_plan(*cache, *seqs, n_q_heads, window, sinks, &p)) == TSL_OK)
-        *bytes = p.bytes;
+        *bytes = p.bytes();
     return st;
 }
 
@@ -405,17 +430,17 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
         return TSL_ERR_INVALID_ARG;
     if (!q.wide() || !o.wide())
         return TSL_ERR_MISALIGNED;
-    AttendPlan p;
+    AttendPlans p;
     if ((st = attend_plan(*cache, *seqs, n_q_heads, window, sinks, &p)) != TSL_OK)
         return st;
     if (nothing(*seqs))
         return TSL_OK;
-    if (p.bytes) {
-        if (!workspace || ws_bytes < p.bytes)
+    if (p.bytes()) {
+        if (!workspace || ws_bytes < p.bytes())
             return TSL_ERR_BUFFER_TOO_SMALL;
         if (!aligned(workspace, 256))
             return TSL_ERR_MISALIGNED;
-        const Heads ws = {workspace, 1, 1, (int64_t)p.bytes, (int64_t)p.bytes, 0, 1};
+        const Heads ws = {workspace, 1, 1, (int64_t)p.bytes(), (int64_t)p.bytes(), 0, 1};
         if (clash(ws, q) || clash(ws, o) || meets_cache(ws, *cache, *seqs, true))
             return TSL_ERR_INVALID_ARG;
     }
@@ -434,29 +459,41 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     a.window = window;
     a.sinks = sinks;
     a.o_bf16 = odtype == TSL_BF16;
-    a.tiles = p.tiles;
     a.by_group = make_div((uint32_t)a.group);
-    a.by_tiles = make_div((uint32_t)p.tiles);
     a.by_heads = make_div((uint32_t)cache->n_kv_heads);
-    a.by_splits = make_div((uint32_t)p.splits);
-    a.splits = p.splits;
-    a.shared = p.shared;
-    a.parts = p.parts;
-    a.by_parts = make_div((uint32_t)p.parts);
-    a.units = (int32_t)p.units;
-    a.min_share = p.min_share;
-    if (p.ranges) {
-        a.part = static_cast<float *>(workspace);
-        a.part_ml = a.part + p.ranges * p.tile_rows * cache->head_dim;
-        a.spans = reinterpret_cast<int32_t *>(a.part_ml + p.ranges * p.tile_rows * 2);
-    }
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    hipError_t e = p.tile_rows < kPromptRows
-                       ? launch_attend_decode(cache->head_dim, p.tile_rows, a, hs)
-                       : launch_attend_prompt(cache->head_dim, a, hs);
-    if (e == hipSuccess && p.ranges)
-        e = launch_attend_join(cache->head_dim, p.tile_rows, a, hs);
-    return from_hip(e);
+    char *ws = static_cast<char *>(workspace);
+    for (const bool few : {true, false}) {
+        if (few ? !p.few : !p.many)
+            continue;
+        const AttendPlan &k = few ? p.f : p.m;
+        // query rows of a sequence and head that this kernel takes
+        a.rows_min = few || !p.few ? 0 : (int32_t)kFewRows + 1;
+        a.rows_max = few && p.many ? (int32_t)kFewRows : INT32_MAX;
+        a.rows = k.rows;
+        a.by_tiles = make_div((uint32_t)k.tiles);
+        a.by_parts = make_div((uint32_t)k.parts);
+        a.by_splits = make_div((uint32_t)k.splits);
+        a.tiles = k.tiles;
+        a.splits = k.splits;
+        a.shared = k.shared;
+        a.parts = k.parts;
+        a.units = (int32_t)k.units;
+        a.min_share = k.min_share;
+        if (k.ranges) {
+            a.part = reinterpret_cast<float *>(ws);
+            a.part_ml = a.part + k.ranges * k.tile_rows * cache->head_dim;
+            a.spans = reinterpret_cast<int32_t *>(a.part_ml + k.ranges * k.tile_rows * 2);
+            ws += k.bytes;
+        }
+        hipError_t e = few ? launch_attend_decode(cache->head_dim, k.tile_rows, a, hs)
+                           : launch_attend_prompt(cache->head_dim, a, hs);
+        if (e == hipSuccess && k.ranges)
+            e = launch_attend_join(cache->head_dim, k.tile_rows, a, hs);
+        if (e != hipSuccess)
+            return from_hip(e);
+    }
+    return TSL_OK;
 }
 
 extern "C" const char *tsl_attn_last_hip_error_string(void) {

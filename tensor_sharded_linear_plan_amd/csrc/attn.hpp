@@ -89,6 +89,8 @@ struct AttendArgs {
     float scale; // times log2 e
     int32_t group, window, sinks, o_bf16;
     Div by_group, by_tiles, by_heads, by_splits, by_parts; // heads: of the cache
+    int32_t rows;      // query rows of a sequence and K/V head, at most
+    int32_t rows_min, rows_max; // sequences with fewer or more are another kernel's
     int32_t tiles;     // row tiles of a sequence and K/V head
     int32_t splits;    // ranges of tokens a tile is divided into at most (many rows)
     int32_t shared;    // few rows: all records of the call in a row, cut into parts
@@ -184,6 +186,11 @@ __host__ __device__ __forceinline__ void divide(const AttendArgs &a, TileView &v
     v.share = quotient(v.count + a.splits - 1, a.by_splits);
     v.share = v.share > a.min_share ? v.share : a.min_share;
     v.used = (v.count + v.share - 1) / v.share;
+}
+// Query rows of a sequence and K/V head, 0 where they are not this kernel's.
+__host__ __device__ __forceinline__ int rows_of(const AttendArgs &a, const SeqRows &q) {
+    const int rows = (q.n < a.c.max_rows ? q.n : a.c.max_rows) * a.group;
+    return rows < a.rows_min || rows > a.rows_max ? 0 : rows;
 }
 // What tile `tile` of `tile_rows` query rows sees; `rows` of it and later ones.
 __host__ __device__ __forceinline__ TileView view_of(const AttendArgs &a, const SeqRows &q, int tile,

@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     const int s = (turn + tile) % a.c.n_seqs;
     const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
     const SeqRows q = seq_rows(a.c, s);
-    const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
-    const int rows = n * a.group - tile * kRows;
+    const int rows = rows_of(a, q) - tile * kRows;
     if (rows <= 0)
         return;
     const int start = q.ctx - q.n;

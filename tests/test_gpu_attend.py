@@ -143,6 +143,22 @@ def test_attend_prompts(d, hq, hkv, page, rows, ctx, window, sinks, okind, pad, 
     check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, okind, True)
 
 
+@pytest.mark.parametrize("d,hq,hkv,window,sinks", [(128, 28, 4, 0, 0), (64, 8, 2, 0, 0), (64, 8, 2, 60, 3),
+                                                   (128, 8, 8, 0, 0), (128, 32, 1, 100, 0), (256, 4, 2, 0, 0)])
+def test_generated_tokens_beside_a_prompt(d, hq, hkv, window, sinks):
+    """Sequences of one or a few rows in one call with long ones, in any order."""
+    g = hq // hkv
+    few = 64 // g  # rows that the kernel of few rows takes
+    rows = [1, 300, 1, few, few + 1, 0, 2, 64 + 130 // g]
+    ctx = [700, 300, 1, few + 90, few + 90, 50, 333, 700]
+    b = au.Batch(rows, ctx, 64, seed=6, lead=2, tail=2)
+    pages = au.Pages(b.n_pages, 64, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 61)
+    au.fill(pages, b, K, V)
+    Q, O = run(pages, b, hq, q, d ** -0.5, window, sinks, "f32")
+    check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, "f32", True)
+
+
 @pytest.mark.parametrize("rows,ctx", [([1, 1, 2], [64, 1024, 513]), ([40, 256], [296, 256])])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_equal_weights_give_the_exact_mean(rows, ctx, d):
