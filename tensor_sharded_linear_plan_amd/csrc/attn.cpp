@@ -199,19 +199,26 @@ struct AttendPlan {
     int32_t tile_rows, tiles, splits, min_share;
     int32_t shared, parts;
     int64_t units, ranges; // (sequence, head, tile); ranges with sums of their own
+    int32_t images;        // records of a sequence and head that are expanded once, 0: none
+    size_t image_bytes;
     size_t bytes;
 };
 
 // Query rows of a sequence and K/V head up to which the kernel of few rows takes
 // it, where every tile of 16 expands the records it reads anew.
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewRows = 96;
 constexpr int64_t kCUs = 256;
 // Records that a wave takes alone, with no join after it: 0.9 us each, and a join
 // 5 us.
 constexpr int kWholeRecords = 6;
 // Records that are worth a wave of their own with few rows, and a workgroup's
 // range with many.
-constexpr int kAttendShare = 1, kPromptShare = 16;
+constexpr int kAttendShare = 1, kPromptShare = 8;
+
+// Tiles of a sequence and head from which on expanding its records once is faster
+// than for each tile, and the most memory that takes.
+constexpr int kImageTiles = 2;
+constexpr int64_t kImageBytes = int64_t(1) << 30;
 
 tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool few, int tile_rows,
                        int32_t window, int32_t sinks, AttendPlan *p) {
@@ -246,7 +253,22 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool
     if (p->parts > kMaxBlocks || p->units * p->splits > kMaxBlocks ||
         (p->ranges && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    p->bytes = round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +
+    // with several tiles a sequence's records are expanded once for all of them
+    p->images = 0;
+    p->image_bytes = 0;
+    if (!few && p->tiles >= kImageTiles) {
+        int64_t n = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
+        n = (n + kBlock - 1) / kBlock;
+        if (window)
+            n = std::min<int64_t>(n, ((int64_t)window + std::min<int64_t>(q.max_rows, q.rows)) / kBlock + 2 +
+                                         ((int64_t)sinks + kBlock - 1) / kBlock);
+        n *= (int64_t)q.n_seqs * c.n_kv_heads;
+        if (n <= kImageBytes / (128 * c.head_dim)) {
+            p->images = (int32_t)(n / ((int64_t)q.n_seqs * c.n_kv_heads));
+            p->image_bytes = round_up((size_t)n * 128 * c.head_dim, 256) + round_up((size_t)n * 4, 256);
+        }
+    }
+    p->bytes = p->image_bytes + round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +
                             (p->shared ? (size_t)p->units * 8 : 0),
                         256);
     return TSL_OK;
@@ -480,13 +502,23 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
         a.parts = k.parts;
         a.units = (int32_t)k.units;
         a.min_share = k.min_share;
+        a.image_records = k.images;
+        if (k.images) {
+            a.by_images = make_div((uint32_t)k.images);
+            a.images = ws;
+            a.image_info = reinterpret_cast<uint32_t *>(
+                ws + round_up((size_t)k.images * (size_t)seqs->n_seqs * cache->n_kv_heads * 128 * cache->head_dim, 256));
+        }
         if (k.ranges) {
-            a.part = reinterpret_cast<float *>(ws);
+            char *const at = ws + k.image_bytes;
+            a.part = reinterpret_cast<float *>(at);
             a.part_ml = a.part + k.ranges * k.tile_rows * cache->head_dim;
             a.spans = reinterpret_cast<int32_t *>(a.part_ml + k.ranges * k.tile_rows * 2);
-            ws += k.bytes;
         }
-        hipError_t e = few ? launch_attend_decode(cache->head_dim, k.tile_rows, a, hs)
+        ws += k.bytes;
+        hipError_t e = k.images ? launch_attend_images(cache->head_dim, a, hs) : hipSuccess;
+        if (e == hipSuccess)
+            e = few ? launch_attend_decode(cache->head_dim, k.tile_rows, a, hs)
                            : launch_attend_prompt(cache->head_dim, a, hs);
         if (e == hipSuccess && k.ranges)
             e = launch_attend_join(cache->head_dim, k.tile_rows, a, hs);

@@ -102,6 +102,13 @@ struct AttendArgs {
     // unit = (sequence * heads + head) * tiles + tile
     float *part, *part_ml;
     int32_t *spans; // shared: the first and last wave of each unit
+    // many rows, where records are expanded once for the call: of each sequence
+    // and head up to image_records images of 128 head_dim bytes (0: none), and
+    // of each its exponents and flags
+    char *images;
+    uint32_t *image_info;
+    int32_t image_records;
+    Div by_images;
     int32_t rows_up; // the join: a unit's rows, rounded up to a workgroup's
     Div by_rows, by_tile_rows;
 };
@@ -121,6 +128,7 @@ constexpr int attend_groups(int head_dim) {
 hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
 constexpr int kPromptRows = 256; // of attend_prompt, head_dim 64 or 128
 hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream);
+hipError_t launch_attend_images(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
 
 // ---- where tokens lie and which are seen ------------------------------------------
@@ -198,8 +206,22 @@ __host__ __device__ __forceinline__ TileView view_of(const AttendArgs &a, const 
     const int last = tile * tile_rows + (rows < tile_rows ? rows : tile_rows) - 1, start = q.ctx - q.n;
     return tile_view(a, start + quotient(tile * tile_rows, a.by_group), start + quotient(last, a.by_group));
 }
+// What all rows of a sequence together see.
+__host__ __device__ __forceinline__ TileView sequence_view(const AttendArgs &a, const SeqRows &q) {
+    const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
+    return tile_view(a, q.ctx - q.n, q.ctx - q.n + n - 1);
+}
 __host__ __device__ __forceinline__ int view_block(const TileView &v, int i) {
     return i < v.lead ? i : v.from + i - v.lead;
+}
+// Whether some row of the tile may see token j (first tokens and a window between them).
+__host__ __device__ __forceinline__ bool any_sees(const AttendArgs &a, const TileView &v, int j) {
+    return (j <= v.last) & (!a.window | (j > v.first - a.window) | (j < a.sinks));
+}
+// ... and all of a record's.
+__host__ __device__ __forceinline__ bool any_sees_all(const AttendArgs &a, const TileView &v, int blk) {
+    const int j = blk * kBlock;
+    return (j + 31 <= v.last) & (!a.window | (j > v.first - a.window) | (j + 31 < a.sinks));
 }
 // Whether every row of the tile sees all tokens of a record.
 __host__ __device__ __forceinline__ bool sees_all(const AttendArgs &a, const TileView &v, int blk) {

@@ -22,6 +22,7 @@
 // them comes to 2^15 (none is lost above 2^-33 of the largest): the common step
 // looks for no maximum.
 #include "attn.hpp"
+#include "gemm_common.hpp"
 
 namespace tsl {
 namespace {
@@ -88,7 +89,46 @@ template <int ROW> __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * ROW + ((piece ^ (ROW == 128 ? row >> 1 & 7 : row & 15)) << 4);
 }
 
-template <int D>
+// Clears what `drop` names of eight bf16.
+template <typename F> __device__ __forceinline__ void drop_where(u32x4 &w, F drop) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w[e >> 1] &= drop(e) ? ~(e & 1 ? 0xFFFF0000u : 0xFFFFu) : 0xFFFFFFFFu;
+}
+
+// Exponents of K and V values, all |15 s| + |b| < 2^(e + 15), from scales and biases
+// (|.|, eight a lane; lanes l % 8 < 4 hold scales); `bad`: some of V's are not finite.
+__device__ __forceinline__ void bounds(u32x4 k, u32x4 v, int lane, int &ek, int &ev, bool &bad) {
+    auto reduce = [&]() {
+        const uint32_t mk = pk_max(pk_max(k[0], k[1]), pk_max(k[2], k[3]));
+        const uint32_t mv = pk_max(pk_max(v[0], v[1]), pk_max(v[2], v[3]));
+        const uint32_t a1 = (mk & 0xFFFFu) > (mk >> 16) ? mk & 0xFFFFu : mk >> 16;
+        const uint32_t b1 = (mv & 0xFFFFu) > (mv >> 16) ? mv & 0xFFFFu : mv >> 16;
+        uint32_t both = a1 | b1 << 16;
+        both += (lane & 7) < 4 ? 0x02000200u : 0u; // 16 |s|
+        return wave_pk_max(both);
+    };
+    uint32_t both = reduce();
+    bad = false;
+    if ((both & 0xFFFFu) >= 0x7F80u || (both >> 16) >= 0x7F80u) {
+        // values that are not finite say nothing of the others'
+        rare();
+        bool off = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t half = e & 1 ? 0xFFFF0000u : 0xFFFFu, inf = 0x7F807F80u & half;
+            off = off | ((v[e >> 1] & half) >= inf);
+            k[e >> 1] = (k[e >> 1] & half) >= inf ? k[e >> 1] & ~half : k[e >> 1];
+            v[e >> 1] = (v[e >> 1] & half) >= inf ? v[e >> 1] & ~half : v[e >> 1];
+        }
+        bad = __any(off);
+        both = reduce();
+    }
+    ek = (int)((both & 0xFFFFu) >> 7) - 127 - 13;
+    ev = (int)(both >> 23) - 127 - 13;
+}
+
+template <int D, bool IMAGES>
 __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArgs a) {
     constexpr int G = D / 64, W = D / 32, ST = D / 16, DT = D / 32;
     constexpr int TB = 8 / G;                         // records of a step
@@ -183,10 +223,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         const int r = begin + step * TB + t;
         return r < stop ? view_block(view, r) : (kMaxContext >> 5) + 1;
     };
-    // tokens that some row of the tile sees: the others enter LDS as zeros
-    auto any_sees = [&](int j) {
-        return (j <= view.last) & (!a.window | (j > view.first - a.window) | (j < a.sinks));
-    };
     // Eight lanes (times G) look after a record: its page, loaded a step before
     // its codes, and who sees it.  Bit 8 G t of a mask is record t's.
     const int lt = (lane >> 3) / G;
@@ -199,10 +235,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     // records whose tokens all rows of the wave see, and those whose every token
     // some row of the tile does
     auto seen_by = [&](int step, uint64_t there, uint64_t &clear, bool &full) {
-        const int blk = block_at(step, lt), j = blk * kBlock;
+        const int blk = block_at(step, lt);
         clear = there & __ballot(sees_all(a, wv, blk));
-        full = (there & __ballot((j + 31 <= view.last) &
-                                 (!a.window | (j > view.first - a.window) | (j + 31 < a.sinks)))) == ~0ull;
+        full = (there & __ballot(any_sees_all(a, view, blk))) == ~0ull;
     };
 
     // ---- what a wave holds of the step after the next: one piece of the K codes
@@ -246,46 +281,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             vx = p[8];
         }
     };
-    // exponents of the step's K and V: all |values| < 2^(e + 15)
     auto exponents = [&](int step, bool full, int &ek, int &ev, bool &bad) {
         u32x4 k = kx & 0x7FFF7FFFu, v = vx & 0x7FFF7FFFu;
         if (!full) {
             rare();
             const int j = block_at(step, lt) * kBlock + (lane & 3) * 4;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t drop = any_sees(j + (e >> 2) * 16 + (e & 3)) ? 0u : (e & 1 ? 0xFFFF0000u : 0xFFFFu);
-                k[e >> 1] &= ~drop;
-                v[e >> 1] &= ~drop;
-            }
+            auto unseen = [&](int e) { return !any_sees(a, view, j + (e >> 2) * 16 + (e & 3)); };
+            drop_where(k, unseen);
+            drop_where(v, unseen);
         }
-        auto reduce = [&]() {
-            const uint32_t mk = pk_max(pk_max(k[0], k[1]), pk_max(k[2], k[3]));
-            const uint32_t mv = pk_max(pk_max(v[0], v[1]), pk_max(v[2], v[3]));
-            const uint32_t a1 = (mk & 0xFFFFu) > (mk >> 16) ? mk & 0xFFFFu : mk >> 16;
-            const uint32_t b1 = (mv & 0xFFFFu) > (mv >> 16) ? mv & 0xFFFFu : mv >> 16;
-            uint32_t both = a1 | b1 << 16;
-            both += (lane & 7) < 4 ? 0x02000200u : 0u; // 16 |s|
-            return wave_pk_max(both);
-        };
-        uint32_t both = reduce();
-        bad = false;
-        if ((both & 0xFFFFu) >= 0x7F80u || (both >> 16) >= 0x7F80u) {
-            // values that are not finite say nothing of the others'
-            rare();
-            bool off = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t half = e & 1 ? 0xFFFF0000u : 0xFFFFu, inf = 0x7F807F80u & half;
-                off = off | ((v[e >> 1] & half) >= inf);
-                k[e >> 1] = (k[e >> 1] & half) >= inf ? k[e >> 1] & ~half : k[e >> 1];
-                v[e >> 1] = (v[e >> 1] & half) >= inf ? v[e >> 1] & ~half : v[e >> 1];
-            }
-            bad = __any(off);
-            both = reduce();
-        }
-        ek = (int)((both & 0xFFFFu) >> 7) - 127 - 13;
-        ev = (int)(both >> 23) - 127 - 13;
+        bounds(k, v, lane, ek, ev, bad);
     };
 
     auto expand_k = [&](int step, bool full, int ek, char *buf) {
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             if (!full) {
                 rare();
                 // D = 128: group d of token 16 pc + tk; D = 64: token 16 d + tk
-                const bool ok = any_sees(block_at(step, pt) * kBlock + 16 * (D == 128 ? pc : d) + tk);
+                const bool ok = any_sees(a, view, block_at(step, pt) * kBlock + 16 * (D == 128 ? pc : d) + tk);
                 sw = ok ? sw : 0u;
                 bw = ok ? bw : 0u;
             }
@@ -323,17 +328,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         u32x4 sw = vs, bw = vb;
         if (!plain) {
             rare();
-            // what no row sees, and what is not finite (its rows are marked
+            // what no row of the tile sees, and what is not finite (its rows are marked
             // instead), must not meet a probability of zero
-            const int blk = block_at(step, pt);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t half = e & 1 ? 0xFFFF0000u : 0xFFFFu, inf = 0x7F807F80u & half;
-                const int tok = blk * kBlock + (e >> 2) * 16 + (lane >> 4) * 4 + (e & 3);
-                const bool ok = any_sees(tok) & ((sw[e >> 1] & inf) != inf) & ((bw[e >> 1] & inf) != inf);
-                sw[e >> 1] = ok ? sw[e >> 1] : sw[e >> 1] & ~half;
-                bw[e >> 1] = ok ? bw[e >> 1] : bw[e >> 1] & ~half;
-            }
+            const int tok = block_at(step, pt) * kBlock + (lane >> 4) * 4;
+            const u32x4 s0 = sw, b0 = bw;
+            auto out = [&](int e) {
+                const uint32_t inf = e & 1 ? 0x7F800000u : 0x7F80u;
+                return !any_sees(a, view, tok + (e >> 2) * 16 + (e & 3)) | ((s0[e >> 1] & inf) == inf) |
+                       ((b0[e >> 1] & inf) == inf);
+            };
+            drop_where(sw, out);
+            drop_where(bw, out);
         }
         f16x2 sv[4], bv[4];
         auto scaled = [&](float x) { return (_Float16)ldexpf(x, -ev); };
@@ -381,17 +386,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             x = half + st == 0 ? mfma32(k[st], qr[0], f32x16{}) : mfma32(k[st], qr[half * HS + st], x);
     };
     // logits of tokens that a row does not see: -inf
-    auto mask = [&](int step, int t, uint64_t there, uint64_t clear, f32x16 &x) {
-        if (bit(clear, t))
-            return;
+    auto mask_record = [&](int blk, bool here, f32x16 &x) {
         rare();
-        const int blk = block_at(step, t);
-        const bool here = bit(there, t);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int j = blk * kBlock + 8 * (r >> 2) + 4 * h + (r & 3);
             x[r] = here && sees(a, pos, lo, j) ? x[r] : -__builtin_inff();
         }
+    };
+    auto mask = [&](int step, int t, uint64_t there, uint64_t clear, f32x16 &x) {
+        if (!bit(clear, t))
+            mask_record(block_at(step, t), bit(there, t), x);
     };
     auto probabilities = [&](const f32x16 &x, float f, f16x8 (&p)[2]) {
         const float ref = kProbScale - m;
@@ -421,9 +426,155 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             o[t] *= g;
     };
 
-    // ---- the walk ----
+    // rare: which rows see a V of the record that is not finite, and in which group
+    auto find_taint = [&](int blk) {
+        const char *rec = record_of(a.c, s, head, blk, record_bytes(D));
+        for (int e = 0; e < 32 * G && rec; ++e) {
+            const int tok = e & 31, g = e >> 5;
+            const uint16_t *sc = reinterpret_cast<const uint16_t *>(rec + 32 * D) + g * 128 + 64 +
+                                 ((tok & 15) >> 2) * 8 + (tok >> 4) * 4 + (tok & 3);
+            if (((sc[0] & 0x7F80u) == 0x7F80u || (sc[32] & 0x7F80u) == 0x7F80u) &&
+                sees(a, pos, lo, blk * kBlock + tok))
+                taint |= 1u << g;
+        }
+    };
+    int ev = 0; // the accumulators' exponent
+
+    // ---- the walk over images ----
+    const TileView all = IMAGES ? sequence_view(a, q) : view;
+    const bool laid_out = IMAGES && all.count <= a.image_records;
+    if (laid_out && steps > 0) {
+        constexpr int PER = 4 / G, IMG = 128 * D, STAGE = 32768, SLOTS = 4; // records of a stage
+        const int count = stop - begin, stages = (count + PER - 1) / PER;
+        const int64_t base = (int64_t)(s * a.c.n_kv_heads + head) * a.image_records;
+        auto image_of = [&](int n) {
+            const int blk = view_block(view, begin + n);
+            return blk < all.lead ? blk : blk - all.from + all.lead;
+        };
+        const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+        auto copy = [&](int st) { // the wave's 4 KB of a stage
+            const int n = st * PER + wave * 4096 / IMG;
+            const char *from = a.images + (base + image_of(n < count ? n : count - 1)) * IMG + (wave * 4096) % IMG;
+            from = reinterpret_cast<const char *>(
+                (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint64_t)from) |
+                (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)((uint64_t)from >> 32)) << 32);
+            const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane(
+                (int)(lds0 + (st % SLOTS) * STAGE + wave * 4096));
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                dma16(from + p * 1024, (uint32_t)lane * 16, to + p * 1024);
+        };
+        // the stage is there for all waves; two more are on their way
+        auto arrive = [&](int st) {
+            if (st + 1 < stages)
+                wait_vmcnt<4>();
+            else
+                wait_vmcnt<0>();
+            barrier();
+            if (st + 2 < stages)
+                copy(st + 2);
+        };
+        uint32_t words = 0; // exponents and flags of 64 records, one a lane
+        uint64_t clear = 0;
+        auto look_up = [&](int n) {
+            const int k = n + lane;
+            words = k < count ? a.image_info[base + image_of(k)] : 0;
+            clear = __ballot(((words >> 21) & 1) & sees_all(a, wv, view_block(view, begin + k)));
+        };
+        auto word_of = [&](int n) { return (uint32_t)__builtin_amdgcn_readlane((int)words, n & 63); };
+        auto image = [&](int n) { return lds + (n / PER % SLOTS) * STAGE + (n % PER) * IMG + lane * 16; };
+        auto read_k = [&](const char *img, int half, f16x8 (&k)[HS]) {
+#pragma unroll
+            for (int st = 0; st < HS; ++st)
+                k[st] = *reinterpret_cast<const f16x8 *>(img + (half * HS + st) * 1024);
+        };
+        auto read_v = [&](const char *img, int kap, f16x8 (&v)[DT]) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                v[d] = *reinterpret_cast<const f16x8 *>(img + 64 * D + (2 * d + kap) * 1024);
+        };
+        f32x16 x[2];
+        look_up(0);
+        copy(0);
+        if (stages > 1)
+            copy(1);
+        uint32_t word = word_of(0);
+        ev = (int)(word >> 10 & 1023) - 256;
+        int top = ev;
+        arrive(0);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            f16x8 k[HS];
+            read_k(image(0), half, k);
+            logits(k, half, x[0]);
+        }
+        if (!(clear & 1))
+            mask_record(view_block(view, begin), word >> 21 & 1, x[0]);
+        for (int n0 = 0; n0 < count; n0 += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int n = n0 + t;
+                if (t && n >= count)
+                    break;
+                f32x16 &now = x[t], &then = x[t ^ 1];
+                if ((n + 1) % PER == 0 && n + 1 < count)
+                    arrive((n + 1) / PER);
+                const int ek = (int)(word & 1023) - 256, er = (int)(word >> 10 & 1023) - 256;
+                if (er != ev) {
+                    rare();
+                    top = top > er ? top : er;
+                    const int to = er > top - 64 ? er : top - 64;
+                    const float g = ldexpf(1.f, ev - to);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        o[d] *= g;
+                    ev = to;
+                }
+                const float f = fmaxf(ldexpf(fabsf(a.scale), qe + ek), 1.17549435e-38f);
+                f16x8 k0[HS], k1[HS], v0[DT], v1[DT], p[2];
+                read_k(image(n + 1), 0, k0);
+                fence();
+                float sum = probabilities(now, f, p);
+                if (__any(!(sum < kProbMost))) {
+                    raise(now, f);
+                    sum = probabilities(now, f, p);
+                }
+                l += sum;
+                if (er != ev) { // 2^64 below an earlier one's
+                    rare();
+                    const _Float16 g = (_Float16)ldexpf(1.f, er - ev);
+                    p[0] *= g;
+                    p[1] *= g;
+                }
+                if (word >> 20 & 1 && !idle)
+                    find_taint(view_block(view, begin + n));
+                read_k(image(n + 1), 1, k1);
+                fence();
+                logits(k0, 0, then);
+                read_v(image(n), 0, v0);
+                fence();
+                logits(k1, 1, then);
+                read_v(image(n), 1, v1);
+                fence();
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = mfma32(v0[d], p[0], o[d]);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = mfma32(v1[d], p[1], o[d]);
+                if (((n + 1) & 63) == 0)
+                    look_up(n + 1);
+                word = word_of(n + 1);
+                if (!(clear >> ((n + 1) & 63) & 1))
+                    mask_record(view_block(view, begin + n + 1), word >> 21 & 1, then);
+            }
+        }
+    }
+
+    // ---- the walk over codes ----
+    if (!laid_out) {
     uint64_t there = 0, there1 = 0, clear = 0, clear1 = 0; // of this step, the next
-    int ek = 0, ev = 0, ek1 = 0, ev1 = 0, page = -1;
+    int ek = 0, ek1 = 0, ev1 = 0, page = -1;
     bool bad = false, bad1 = false, full1 = false;
     f32x16 x[2];
     if (steps > 0) {
@@ -493,21 +644,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             else
                 mask(step + 1, 0, there1, clear1, then);
         }
-        if (bad && !idle) // rare: which rows see a V that is not finite, and in which group
-            for (int t = 0; t < TB; ++t) {
-                const int blk = block_at(step, t);
-                const char *rec = bit(there, t) ? record_of(a.c, s, head, blk, record_bytes(D)) : nullptr;
-                if (!rec)
-                    continue;
-                for (int e = 0; e < 32 * G; ++e) {
-                    const int tok = e & 31, g = e >> 5;
-                    const uint16_t *sc = reinterpret_cast<const uint16_t *>(rec + 32 * D) + g * 128 + 64 +
-                                         ((tok & 15) >> 2) * 8 + (tok >> 4) * 4 + (tok & 3);
-                    if (((sc[0] & 0x7F80u) == 0x7F80u || (sc[32] & 0x7F80u) == 0x7F80u) &&
-                        sees(a, pos, lo, blk * kBlock + tok))
-                        taint |= 1u << g;
-                }
-            }
+        if (bad && !idle)
+            for (int t = 0; t < TB; ++t)
+                if (bit(there, t))
+                    find_taint(block_at(step, t));
         if (ev1 != ev) {
             const float g = ldexpf(1.f, ev - ev1);
 #pragma unroll
@@ -521,6 +661,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         clear = clear1;
         fetch(step + 2, page, there1);
         page = page_of(step + 3);
+    }
     }
 
     l += __shfl_xor(l, 32, 64);
@@ -560,22 +701,163 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         });
 }
 
+// One wave expands one record that some row of its sequence sees: K as the
+// operands of its first product, ST pieces of 1 KB in the order in which a wave
+// reads them (lane 32 h + c holds 8 columns of token c), then V as those of the
+// second (column c, 8 tokens), in binary16 by exponents of the record's own.
+// V's are multiples of 8, so that few neighbours differ: 22 octaves below the
+// largest value keep all bits.
+template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(AttendArgs a) {
+    constexpr int G = D / 64, W = D / 32;
+    const int lane = threadIdx.x & 63;
+    const int at = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int unit = quotient(at, a.by_images), k = at - unit * a.image_records;
+    const int s = quotient(unit, a.by_heads), head = unit - s * a.c.n_kv_heads;
+    if (s >= a.c.n_seqs)
+        return;
+    const SeqRows q = seq_rows(a.c, s);
+    if (rows_of(a, q) <= 0)
+        return;
+    const TileView all = sequence_view(a, q);
+    if (k >= all.count || all.count > a.image_records)
+        return;
+    const int blk = view_block(all, k);
+    const char *rec = record_of(a.c, s, head, blk, record_bytes(D));
+    char *img = a.images + (int64_t)at * (128 * D);
+    if (!rec) {
+        for (int i = lane; i < 8 * D; i += 64)
+            reinterpret_cast<u32x4 *>(img)[i] = u32x4{0, 0, 0, 0};
+        if (lane == 0)
+            a.image_info[at] = 256 | 256 << 10;
+        return;
+    }
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(rec);
+    u32x4 kraw[G], vraw[G], vs[G], vb[G], kx = {0, 0, 0, 0}, vx = {0, 0, 0, 0};
+    uint32_t ks[G][2][2]; // group, token half, scale and bias
+    const int tk = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int pc = 0; pc < G; ++pc) {
+        kraw[pc] = p[pc * 64 + lane];
+        vraw[pc] = p[D + pc * 64 + lane];
+        vs[pc] = p[2 * D + pc * 16 + 8 + g];
+        vb[pc] = p[2 * D + pc * 16 + 12 + g];
+        const uint16_t *sc = reinterpret_cast<const uint16_t *>(rec + 32 * D) + pc * 128 + (tk >> 2) * 8 + (tk & 3);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            ks[pc][u][0] = sc[4 * u];
+            ks[pc][u][1] = sc[4 * u + 32];
+        }
+    }
+    if (lane < 8 * G) {
+        kx = p[2 * D + (lane >> 3) * 16 + (lane & 7)];
+        vx = p[2 * D + (lane >> 3) * 16 + (lane & 7) + 8];
+    }
+    const bool full = any_sees_all(a, all, blk);
+    kx &= 0x7FFF7FFFu;
+    vx &= 0x7FFF7FFFu;
+    if (!full) {
+        const int j = blk * kBlock + (lane & 3) * 4;
+        auto unseen = [&](int e) { return !any_sees(a, all, j + (e >> 2) * 16 + (e & 3)); };
+        drop_where(kx, unseen);
+        drop_where(vx, unseen);
+    }
+    int ek, ev;
+    bool bad;
+    bounds(kx, vx, lane, ek, ev, bad);
+    ev = (ev + 7) & ~7;
+    if (lane == 0)
+        a.image_info[at] = (uint32_t)(ek + 256) | (uint32_t)(ev + 256) << 10 | (uint32_t)bad << 20 | 1u << 21;
+#pragma unroll
+    for (int pc = 0; pc < G; ++pc) {
+        // K: word n of a lane's four is 8 columns (4 g + 16 .. of 32 ww) of token 16 u + tk
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int at16 = pc * 4 + n, u = at16 / W, ww = at16 % W, tok = 16 * u + tk;
+            const bool ok = full || any_sees(a, all, blk * kBlock + tok);
+            const uint32_t sw = ok ? ks[ww / 2][u][0] : 0u, bw = ok ? ks[ww / 2][u][1] : 0u;
+            const _Float16 x = (_Float16)ldexpf(bf16_lo(sw), -ek), y = (_Float16)ldexpf(bf16_lo(bw), -ek);
+            f16x2 cd[4];
+            codes16(kraw[pc][n], cd);
+            u32x4 out;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                out[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cd[j], f16x2{x, x}, f16x2{y, y}));
+            const int chunk = 4 * ww + g;
+            *reinterpret_cast<u32x4 *>(img + (chunk >> 1) * 1024 + ((chunk & 1) * 32 + tok) * 16) = out;
+        }
+        // V: tokens 4 g .. and 16 + 4 g .. of column 16 (4 pc + n) + tk
+        u32x4 sw = vs[pc], bw = vb[pc];
+        if (!full | bad) {
+            const int tok = blk * kBlock + g * 4;
+            const u32x4 s0 = sw, b0 = bw;
+            auto out = [&](int e) {
+                const uint32_t inf = e & 1 ? 0x7F800000u : 0x7F80u;
+                return !any_sees(a, all, tok + (e >> 2) * 16 + (e & 3)) | ((s0[e >> 1] & inf) == inf) |
+                       ((b0[e >> 1] & inf) == inf);
+            };
+            drop_where(sw, out);
+            drop_where(bw, out);
+        }
+        f16x2 sv[4], bv[4];
+        auto scaled = [&](float v) { return (_Float16)ldexpf(v, -ev); };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sv[j] = f16x2{scaled(bf16_lo(sw[j])), scaled(bf16_hi(sw[j]))};
+            bv[j] = f16x2{scaled(bf16_lo(bw[j])), scaled(bf16_hi(bw[j]))};
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int col = (pc * 4 + n) * 16 + tk;
+            f16x2 cd[4];
+            codes16(vraw[pc][n], cd);
+            u32x2 half[2]; // of the tokens' two operands
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                half[j >> 1][j & 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(cd[j], sv[j], bv[j]));
+            // lanes 32 apart hold the two halves of a lane's 8 tokens: the lower
+            // takes those of the first operand, the upper of the second
+            const int up = g >> 1;
+            const u32x2 mine = up ? half[1] : half[0], give = up ? half[0] : half[1];
+            const u32x2 got = {(uint32_t)__shfl_xor((int)give[0], 32, 64), (uint32_t)__shfl_xor((int)give[1], 32, 64)};
+            const u32x4 out = up ? u32x4{got[0], got[1], mine[0], mine[1]} : u32x4{mine[0], mine[1], got[0], got[1]};
+            *reinterpret_cast<u32x4 *>(img + 64 * D + ((col >> 5) * 2 + up) * 1024 + ((g & 1) * 32 + (col & 31)) * 16) = out;
+        }
+    }
+}
+
 } // namespace
 
-// K and V of two steps.
+// K and V of two steps, or four stages of images.
 constexpr int kPromptLds = 4 * 32768;
 
-hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream) {
+namespace {
+template <int D> hipError_t prompt(const AttendArgs &a, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.tiles * a.splits));
-    const void *f = head_dim == 64 ? reinterpret_cast<const void *>(attend_prompt_kernel<64>)
-                                   : reinterpret_cast<const void *>(attend_prompt_kernel<128>);
+    const bool images = a.image_records > 0;
+    const void *f = images ? reinterpret_cast<const void *>(attend_prompt_kernel<D, true>)
+                           : reinterpret_cast<const void *>(attend_prompt_kernel<D, false>);
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kPromptLds);
     if (e != hipSuccess)
         return e;
-    if (head_dim == 64)
-        hipLaunchKernelGGL(attend_prompt_kernel<64>, grid, dim3(64 * kWaves), kPromptLds, stream, a);
+    if (images)
+        hipLaunchKernelGGL((attend_prompt_kernel<D, true>), grid, dim3(64 * kWaves), kPromptLds, stream, a);
     else
-        hipLaunchKernelGGL(attend_prompt_kernel<128>, grid, dim3(64 * kWaves), kPromptLds, stream, a);
+        hipLaunchKernelGGL((attend_prompt_kernel<D, false>), grid, dim3(64 * kWaves), kPromptLds, stream, a);
+    return hipGetLastError();
+}
+} // namespace
+
+hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream) {
+    return head_dim == 64 ? prompt<64>(a, stream) : prompt<128>(a, stream);
+}
+
+hipError_t launch_attend_images(int head_dim, const AttendArgs &a, hipStream_t stream) {
+    const int64_t n = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.image_records;
+    const dim3 grid((unsigned)((n + 3) / 4));
+    if (head_dim == 64)
+        hipLaunchKernelGGL(attend_images_kernel<64>, grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL(attend_images_kernel<128>, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
