@@ -217,7 +217,7 @@ constexpr int kAttendShare = 1, kPromptShare = 8;
 
 // Tiles of a sequence and head from which on expanding its records once is faster
 // than for each tile, and the most memory that takes.
-constexpr int kImageTiles = 2;
+constexpr int kImageTiles = 4;
 constexpr int64_t kImageBytes = int64_t(1) << 30;
 
 tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool few, int tile_rows,
@@ -247,7 +247,7 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool
     }
     if (!few) {
         p->splits = (int32_t)std::max<int64_t>(
-            1, std::min({most, (int64_t)kMaxSplits, p->units > 0 ? kCUs / p->units : 1}));
+            1, std::min({most, (int64_t)kMaxSplits, p->units > 0 ? 2 * kCUs / p->units : 1}));
         p->ranges = p->splits > 1 ? p->units * p->splits : 0;
     }
     if (p->parts > kMaxBlocks || p->units * p->splits > kMaxBlocks ||

@@ -126,7 +126,7 @@ constexpr int attend_groups(int head_dim) {
 }
 
 hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
-constexpr int kPromptRows = 256; // of attend_prompt, head_dim 64 or 128
+constexpr int kPromptRows = 128; // of attend_prompt, head_dim 64 or 128
 hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_images(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);

@@ -32,7 +32,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kProbScale = 9.f;     // log2
 constexpr float kProbMost = 32768.f;  // of a lane's 16 probabilities together
-constexpr int kWaves = 8;
+constexpr int kWaves = 4; // a workgroup's; two share a CU
 constexpr int kRows = 32 * kWaves;
 static_assert(kRows == kPromptRows, "rows of a tile");
 
@@ -131,10 +131,10 @@ __device__ __forceinline__ void bounds(u32x4 k, u32x4 v, int lane, int &ek, int 
 template <int D, bool IMAGES>
 __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArgs a) {
     constexpr int G = D / 64, W = D / 32, ST = D / 16, DT = D / 32;
-    constexpr int TB = 8 / G;                         // records of a step
+    constexpr int TB = kWaves / G;                    // records of a step
     constexpr int KROW = D * 2, VROW = 64 * TB;       // bytes of a token, of a column
-    constexpr int BUF = 32 * TB * KROW;               // 32 KB: K, or V, of a step
-    extern __shared__ __attribute__((aligned(16))) char lds[]; // K, K, V, V
+    constexpr int BUF = 32 * TB * KROW;               // 16 KB: K, or V, of a step
+    __shared__ __attribute__((aligned(1024))) char lds[4 * BUF]; // K, K, V, V; or four stages of images
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,12 +224,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         return r < stop ? view_block(view, r) : (kMaxContext >> 5) + 1;
     };
     // Eight lanes (times G) look after a record: its page, loaded a step before
-    // its codes, and who sees it.  Bit 8 G t of a mask is record t's.
+    // its codes, and who sees it.  Bit 8 G t of a mask is record t's; the upper
+    // half of the lanes looks after none.
     const int lt = (lane >> 3) / G;
     auto bit = [](uint64_t w, int t) { return (w >> (8 * G * t)) & 1; };
     auto page_of = [&](int step) {
         const int blk = block_at(step, lt), page = blk >> a.c.shift;
-        const bool in = begin + step * TB + lt < stop && page < a.c.max_pages;
+        const bool in = lt < TB && begin + step * TB + lt < stop && page < a.c.max_pages;
         return in ? a.c.page_table[s * a.c.ld_table + page] : -1;
     };
     // records whose tokens all rows of the wave see, and those whose every token
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     auto seen_by = [&](int step, uint64_t there, uint64_t &clear, bool &full) {
         const int blk = block_at(step, lt);
         clear = there & __ballot(sees_all(a, wv, blk));
-        full = (there & __ballot(any_sees_all(a, view, blk))) == ~0ull;
+        full = (there & __ballot(any_sees_all(a, view, blk))) == (1ull << 8 * kWaves) - 1;
     };
 
     // ---- what a wave holds of the step after the next: one piece of the K codes
@@ -388,10 +389,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     // logits of tokens that a row does not see: -inf
     auto mask_record = [&](int blk, bool here, f32x16 &x) {
         rare();
+        // bits of the record's tokens: those below n
+        const int j = blk * kBlock;
+        auto below = [&](int n) { return n - j >= 32 ? ~0u : n > j ? (1u << (n - j)) - 1 : 0u; };
+        const uint32_t seen = (here ? below(pos + 1) & (~below(lo) | below(a.sinks)) : 0u) >> 4 * h;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int j = blk * kBlock + 8 * (r >> 2) + 4 * h + (r & 3);
-            x[r] = here && sees(a, pos, lo, j) ? x[r] : -__builtin_inff();
+            const int keep = (int)(seen << (31 - (8 * (r >> 2) + (r & 3)))) >> 31;
+            x[r] = __uint_as_float((__float_as_uint(x[r]) & keep) | (0xFF800000u & ~keep));
         }
     };
     auto mask = [&](int step, int t, uint64_t there, uint64_t clear, f32x16 &x) {
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     const TileView all = IMAGES ? sequence_view(a, q) : view;
     const bool laid_out = IMAGES && all.count <= a.image_records;
     if (laid_out && steps > 0) {
-        constexpr int PER = 4 / G, IMG = 128 * D, STAGE = 32768, SLOTS = 4; // records of a stage
+        constexpr int PER = TB / 2, IMG = 128 * D, STAGE = BUF, SLOTS = 4; // records of a stage
         const int count = stop - begin, stages = (count + PER - 1) / PER;
         const int64_t base = (int64_t)(s * a.c.n_kv_heads + head) * a.image_records;
         auto image_of = [&](int n) {
@@ -535,6 +540,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 read_k(image(n + 1), 0, k0);
                 fence();
                 float sum = probabilities(now, f, p);
+                read_k(image(n + 1), 1, k1);
+                fence();
+                logits(k0, 0, then);
+                read_v(image(n), 0, v0);
+                fence();
+                logits(k1, 1, then);
+                read_v(image(n), 1, v1);
+                fence();
                 if (__any(!(sum < kProbMost))) {
                     raise(now, f);
                     sum = probabilities(now, f, p);
@@ -548,14 +561,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 }
                 if (word >> 20 & 1 && !idle)
                     find_taint(view_block(view, begin + n));
-                read_k(image(n + 1), 1, k1);
-                fence();
-                logits(k0, 0, then);
-                read_v(image(n), 0, v0);
-                fence();
-                logits(k1, 1, then);
-                read_v(image(n), 1, v1);
-                fence();
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] = mfma32(v0[d], p[0], o[d]);
@@ -827,22 +832,13 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
 
 } // namespace
 
-// K and V of two steps, or four stages of images.
-constexpr int kPromptLds = 4 * 32768;
-
 namespace {
 template <int D> hipError_t prompt(const AttendArgs &a, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.tiles * a.splits));
-    const bool images = a.image_records > 0;
-    const void *f = images ? reinterpret_cast<const void *>(attend_prompt_kernel<D, true>)
-                           : reinterpret_cast<const void *>(attend_prompt_kernel<D, false>);
-    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kPromptLds);
-    if (e != hipSuccess)
-        return e;
-    if (images)
-        hipLaunchKernelGGL((attend_prompt_kernel<D, true>), grid, dim3(64 * kWaves), kPromptLds, stream, a);
+    if (a.image_records > 0)
+        hipLaunchKernelGGL((attend_prompt_kernel<D, true>), grid, dim3(64 * kWaves), 0, stream, a);
     else
-        hipLaunchKernelGGL((attend_prompt_kernel<D, false>), grid, dim3(64 * kWaves), kPromptLds, stream, a);
+        hipLaunchKernelGGL((attend_prompt_kernel<D, false>), grid, dim3(64 * kWaves), 0, stream, a);
     return hipGetLastError();
 }
 } // namespace
