@@ -41,18 +41,6 @@ template <int N> __device__ __forceinline__ void wait_copies() {
     asm volatile("" ::: "memory");
 }
 
-// The sum of the lanes up to each: within rows of 16, then over the rows.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true); // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
-              c = __builtin_amdgcn_readlane(v, 47);
-    const int row = (int)((threadIdx.x & 63) >> 4);
-    return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
-}
-
 // The part of a wave, of all records in a row cut into equal parts: it begins
 // `skip` records into sequence s (rows q).  64 sequences at a time (the host lets
 // at most kMaxShared share).
@@ -455,41 +443,50 @@ __global__ void __launch_bounds__(64 * kWaves, attend_groups(D)) attend_decode_k
 // times over; each group of lanes has a running reference as over tokens.  Bound
 // by latency, that of instructions not yet in the cache among it: the code is
 // short, and walks the ranges and the waves' results in one place.
-template <int D, int WPR>
+template <int D, int WPR, bool MANY>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(AttendArgs a, int tile_rows) {
     constexpr int LPR = D / 8, AT_ONCE = 64 / LPR, AHEAD = 4, RPW = WPR == 1 ? 4 : 1;
     __shared__ __attribute__((aligned(16))) float sums[WPR][D];
     __shared__ float2 sums_ml[WPR];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int b = quotient(blockIdx.x * RPW, a.by_rows);
-    const int rho = blockIdx.x * RPW - b * a.rows_up + (WPR == 1 ? wave : 0);
-    if (rho >= a.rows)
-        return;
-    const int tile = quotient(rho, a.by_tile_rows), unit = b * a.tiles + tile;
-    const int s = quotient(b, a.by_heads), head = b - s * a.c.n_kv_heads;
-    int from = 0, last = 0;
-    if (a.shared) {
-        from = a.spans[2 * unit];
-        last = a.spans[2 * unit + 1];
-    }
-    const SeqRows q = seq_rows(a.c, s);
-    const int rows = rows_of(a, q);
-    if (rho >= rows)
-        return;
-    TileView view = view_of(a, q, tile, tile_rows, rows - tile * tile_rows);
-    // its ranges: the splits in use, or those of the waves that shared it (one
-    // that had all of it has written the result)
-    int64_t slot0 = from + unit;
-    int used = last - from + 1;
-    if (!a.shared) {
-        divide(a, view);
+    int s, head, tile, rho, used;
+    int64_t slot0;
+    SeqRows q;
+    if (MANY) {
+        PromptTile at;
+        const int me = blockIdx.x * RPW + (WPR == 1 ? wave : 0);
+        if (!prompt_tile(a, me / kPromptRows, false, at) || at.splits == 1)
+            return; // (its workgroup has written the result)
+        s = at.s, head = at.head, tile = at.tile, q = at.q;
+        rho = tile * kPromptRows + me % kPromptRows;
+        const int rows = rows_of(a, q);
+        if (rho >= rows)
+            return;
+        TileView view = view_of(a, q, tile, kPromptRows, rows - tile * kPromptRows);
+        divide(a, at.splits, view);
         used = view.used;
-        slot0 = (int64_t)unit * a.splits;
-    } else if (view.count == 0) {
-        used = 0;
-    } else if (used == 1) {
-        return;
+        slot0 = (int64_t)at.unit * at.splits;
+    } else {
+        const int b = quotient(blockIdx.x * RPW, a.by_rows);
+        rho = blockIdx.x * RPW - b * a.rows_up + (WPR == 1 ? wave : 0);
+        if (rho >= a.rows)
+            return;
+        tile = quotient(rho, a.by_tile_rows);
+        const int unit = b * a.tiles + tile;
+        s = quotient(b, a.by_heads), head = b - s * a.c.n_kv_heads;
+        const int from = a.spans[2 * unit], last = a.spans[2 * unit + 1];
+        q = seq_rows(a.c, s);
+        const int rows = rows_of(a, q);
+        if (rho >= rows)
+            return;
+        // the waves that shared it (one that had all of it has written the result)
+        slot0 = from + unit;
+        used = last - from + 1;
+        if (view_of(a, q, tile, tile_rows, rows - tile * tile_rows).count == 0)
+            used = 0;
+        else if (used == 1)
+            return;
     }
     slot0 = slot0 * tile_rows + rho - tile * tile_rows;
     const float *part = a.part + slot0 * D;
@@ -593,16 +590,25 @@ template <int D, int P> hipError_t decode(const AttendArgs &a, hipStream_t strea
 
 template <int D> hipError_t join(int tile_rows, AttendArgs a, hipStream_t stream) {
     const int64_t rows = a.rows, units = (int64_t)a.c.n_seqs * a.c.n_kv_heads;
-    const bool many = a.splits > kJoinWave || (a.shared && a.parts / (units * a.tiles) > kJoinWave);
+    const bool many = a.parts / (units * a.tiles) > kJoinWave;
     a.rows_up = (int32_t)(many ? rows : (rows + 3) / 4 * 4);
     a.by_rows = make_div((uint32_t)a.rows_up);
     a.by_tile_rows = make_div((uint32_t)tile_rows);
     if (many)
-        hipLaunchKernelGGL((attend_join_kernel<D, 16>), dim3((unsigned)(units * rows)), dim3(1024), 0, stream,
-                           a, tile_rows);
+        hipLaunchKernelGGL((attend_join_kernel<D, 16, false>), dim3((unsigned)(units * rows)), dim3(1024), 0,
+                           stream, a, tile_rows);
     else
-        hipLaunchKernelGGL((attend_join_kernel<D, 1>), dim3((unsigned)(units * (a.rows_up / 4))), dim3(256),
-                           0, stream, a, tile_rows);
+        hipLaunchKernelGGL((attend_join_kernel<D, 1, false>), dim3((unsigned)(units * (a.rows_up / 4))),
+                           dim3(256), 0, stream, a, tile_rows);
+    return hipGetLastError();
+}
+
+template <int D> hipError_t prompt_join(const AttendArgs &a, hipStream_t stream) {
+    const unsigned rows = (unsigned)a.units * kPromptRows;
+    if (a.splits > kJoinWave)
+        hipLaunchKernelGGL((attend_join_kernel<D, 16, true>), dim3(rows), dim3(1024), 0, stream, a, kPromptRows);
+    else
+        hipLaunchKernelGGL((attend_join_kernel<D, 1, true>), dim3(rows / 4), dim3(256), 0, stream, a, kPromptRows);
     return hipGetLastError();
 }
 
@@ -621,6 +627,10 @@ hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream) {
     return head_dim == 64 ? join<64>(tile_rows, a, stream)
                           : (head_dim == 128 ? join<128>(tile_rows, a, stream) : join<256>(tile_rows, a, stream));
+}
+
+hipError_t launch_prompt_join(int head_dim, const AttendArgs &a, hipStream_t stream) {
+    return head_dim == 64 ? prompt_join<64>(a, stream) : prompt_join<128>(a, stream);
 }
 
 } // namespace tsl

@@ -205,23 +205,29 @@ struct AttendPlan {
 };
 
 // Query rows of a sequence and K/V head up to which the kernel of few rows takes
-// it, where every tile of 16 expands the records it reads anew.
-constexpr int64_t kFewRows = 96;
+// it, where every tile of 16 expands the records it reads anew.  Of one sequence
+// of 4000 tokens, heads of 128, 32 rows took 21 us with it and 20 with the other,
+// 64 25 and 22, 128 32 and 25; of 16000 tokens 64 33 and 35, 96 41 and 37; of 16
+// sequences of 4000 64 69 and 65, 128 117 and 75.
+constexpr int64_t kFewRows = 48;
 constexpr int64_t kCUs = 256;
-// Records that a wave takes alone, with no join after it: 0.9 us each, and a join
-// 5 us.
+// Records that a wave takes alone, with no join after it: 4 and 8 of them took
+// 9.0 and 12.7 us so, 10.4 and 10.6 divided.
 constexpr int kWholeRecords = 6;
 // Records that are worth a wave of their own with few rows, and a workgroup's
-// range with many.
+// range with many (128 rows over 4000 tokens: 32 us with ranges of 4, 25 of 8, 31
+// of 16).
 constexpr int kAttendShare = 1, kPromptShare = 8;
 
 // Tiles of a sequence and head from which on expanding its records once is faster
-// than for each tile, and the most memory that takes.
+// than for each tile (8 sequences of 2000 tokens: 2 tiles 58 us so and 53 without,
+// 4 82 and 85, 8 98 and 104; 5 tiles over 16000 tokens 75 and 82), and the most
+// memory that takes.
 constexpr int kImageTiles = 4;
 constexpr int64_t kImageBytes = int64_t(1) << 30;
 
-tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool few, int tile_rows,
-                       int32_t window, int32_t sinks, AttendPlan *p) {
+tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int64_t rows, bool few,
+                       int tile_rows, int32_t window, int32_t sinks, AttendPlan *p) {
     p->rows = (int32_t)rows;
     p->tile_rows = tile_rows;
     int64_t seen = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
@@ -230,6 +236,11 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool
     const int64_t records = (seen + kBlock - 1) / kBlock;
     p->tiles = (int32_t)((rows + tile_rows - 1) / tile_rows);
     p->units = (int64_t)q.n_seqs * c.n_kv_heads * p->tiles;
+    if (!few && q.n_seqs > 1) { // tiles that the rows of the call may come to
+        const int64_t all = q.rows * group;
+        p->units = std::min(p->units, (all / tile_rows + std::min<int64_t>(q.n_seqs, all / (kFewRows + 1))) *
+                                          c.n_kv_heads);
+    }
     p->min_share = few ? kAttendShare : kPromptShare;
     const int64_t most = std::max<int64_t>(1, (records + p->min_share - 1) / p->min_share);
     p->shared = 0;
@@ -246,22 +257,22 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t rows, bool
         p->ranges = p->parts + p->units;
     }
     if (!few) {
+        // one sequence has max_rows; how many ranges there are is for the kernel to say
         p->splits = (int32_t)std::max<int64_t>(
-            1, std::min({most, (int64_t)kMaxSplits, p->units > 0 ? 2 * kCUs / p->units : 1}));
-        p->ranges = p->splits > 1 ? p->units * p->splits : 0;
+            1, std::min(most, kPromptPlaces / std::max<int64_t>(1, (int64_t)p->tiles * c.n_kv_heads)));
+        if (p->splits > 1)
+            p->ranges = std::max(p->units, std::min<int64_t>(kPromptPlaces, p->units * p->splits));
+        p->parts = (int32_t)std::min<int64_t>(std::max(p->units, p->ranges), kMaxBlocks + 1);
     }
-    if (p->parts > kMaxBlocks || p->units * p->splits > kMaxBlocks ||
-        (p->ranges && (int64_t)q.n_seqs * c.n_kv_heads * rows > kMaxBlocks))
+    if (p->parts > kMaxBlocks ||
+        (p->ranges && (few ? (int64_t)q.n_seqs * c.n_kv_heads * rows : p->units * tile_rows) > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
     // with several tiles a sequence's records are expanded once for all of them
     p->images = 0;
     p->image_bytes = 0;
     if (!few && p->tiles >= kImageTiles) {
-        int64_t n = std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens);
-        n = (n + kBlock - 1) / kBlock;
-        if (window)
-            n = std::min<int64_t>(n, ((int64_t)window + std::min<int64_t>(q.max_rows, q.rows)) / kBlock + 2 +
-                                         ((int64_t)sinks + kBlock - 1) / kBlock);
+        int64_t n = most_records(std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens),
+                                 std::min<int64_t>(q.max_rows, q.rows), window, sinks);
         n *= (int64_t)q.n_seqs * c.n_kv_heads;
         if (n <= kImageBytes / (128 * c.head_dim)) {
             p->images = (int32_t)(n / ((int64_t)q.n_seqs * c.n_kv_heads));
@@ -294,11 +305,11 @@ tsl_status attend_plan(const tsl_cache &c, const tsl_seqs &q, int32_t n_q_heads,
         // beside long sequences most of the others have one row
         const int64_t most = p->many ? kFewRows : rows, typical = p->many ? group : rows;
         const int tile = typical > 8 ? 16 : (typical > 4 || c.head_dim > 128 ? 8 : 4);
-        const tsl_status st = plan_kernel(c, q, most, true, tile, window, sinks, &p->f);
+        const tsl_status st = plan_kernel(c, q, group, most, true, tile, window, sinks, &p->f);
         if (st != TSL_OK)
             return st;
     }
-    return p->many ? plan_kernel(c, q, rows, false, kPromptRows, window, sinks, &p->m) : TSL_OK;
+    return p->many ? plan_kernel(c, q, group, rows, false, kPromptRows, window, sinks, &p->m) : TSL_OK;
 }
 
 tsl_status attend_check(const tsl_cache *cache, const tsl_seqs *seqs, int32_t n_q_heads,
@@ -495,7 +506,6 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
         a.rows = k.rows;
         a.by_tiles = make_div((uint32_t)k.tiles);
         a.by_parts = make_div((uint32_t)k.parts);
-        a.by_splits = make_div((uint32_t)k.splits);
         a.tiles = k.tiles;
         a.splits = k.splits;
         a.shared = k.shared;
@@ -521,7 +531,8 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
             e = few ? launch_attend_decode(cache->head_dim, k.tile_rows, a, hs)
                            : launch_attend_prompt(cache->head_dim, a, hs);
         if (e == hipSuccess && k.ranges)
-            e = launch_attend_join(cache->head_dim, k.tile_rows, a, hs);
+            e = few ? launch_attend_join(cache->head_dim, k.tile_rows, a, hs)
+                    : launch_prompt_join(cache->head_dim, a, hs);
         if (e != hipSuccess)
             return from_hip(e);
     }

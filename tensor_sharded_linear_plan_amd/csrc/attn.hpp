@@ -88,18 +88,18 @@ struct AttendArgs {
     int64_t ldq, q_head, ldo, o_head;
     float scale; // times log2 e
     int32_t group, window, sinks, o_bf16;
-    Div by_group, by_tiles, by_heads, by_splits, by_parts; // heads: of the cache
+    Div by_group, by_tiles, by_heads, by_parts; // heads: of the cache
     int32_t rows;      // query rows of a sequence and K/V head, at most
     int32_t rows_min, rows_max; // sequences with fewer or more are another kernel's
     int32_t tiles;     // row tiles of a sequence and K/V head
-    int32_t splits;    // ranges of tokens a tile is divided into at most (many rows)
+    int32_t splits;    // many rows: ranges of tokens a tile is divided into at most
     int32_t shared;    // few rows: all records of the call in a row, cut into parts
     int32_t parts;     // few rows: waves
-    int32_t units;     // sequences * heads * tiles
+    int32_t units;     // sequences * heads * tiles; many rows: heads * tiles, at most
     int32_t min_share; // records of a range or part at least
     // sums of ranges: [range][tile rows][head_dim], and of each row its reference
-    // exponent and sum; range = unit * splits + split, or unit + wave, with
-    // unit = (sequence * heads + head) * tiles + tile
+    // exponent and sum; few rows: range = unit + wave, with unit = (sequence *
+    // heads + head) * tiles + tile; many: range = workgroup
     float *part, *part_ml;
     int32_t *spans; // shared: the first and last wave of each unit
     // many rows, where records are expanded once for the call: of each sequence
@@ -129,6 +129,7 @@ hipError_t launch_attend_decode(int head_dim, int tile_rows, const AttendArgs &a
 constexpr int kPromptRows = 128; // of attend_prompt, head_dim 64 or 128
 hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_images(int head_dim, const AttendArgs &a, hipStream_t stream);
+hipError_t launch_prompt_join(int head_dim, const AttendArgs &a, hipStream_t stream);
 hipError_t launch_attend_join(int head_dim, int tile_rows, const AttendArgs &a, hipStream_t stream);
 
 // ---- where tokens lie and which are seen ------------------------------------------
@@ -169,7 +170,7 @@ __host__ __device__ __forceinline__ char *record_of(const CacheArgs &c, int s, i
 struct TileView {
     int first, last;
     int lead, from, count;
-    int share, used; // records of a range, ranges with any
+    int share, used; // of a tile in ranges: records of one, ranges with any
 };
 __host__ __device__ __forceinline__ TileView tile_view(const AttendArgs &a, int first, int last) {
     TileView v;
@@ -189,12 +190,6 @@ __host__ __device__ __forceinline__ TileView tile_view(const AttendArgs &a, int 
     }
     return v;
 }
-// Its ranges where a tile is divided into at most a.splits.
-__host__ __device__ __forceinline__ void divide(const AttendArgs &a, TileView &v) {
-    v.share = quotient(v.count + a.splits - 1, a.by_splits);
-    v.share = v.share > a.min_share ? v.share : a.min_share;
-    v.used = (v.count + v.share - 1) / v.share;
-}
 // Query rows of a sequence and K/V head, 0 where they are not this kernel's.
 __host__ __device__ __forceinline__ int rows_of(const AttendArgs &a, const SeqRows &q) {
     const int rows = (q.n < a.c.max_rows ? q.n : a.c.max_rows) * a.group;
@@ -210,6 +205,16 @@ __host__ __device__ __forceinline__ TileView view_of(const AttendArgs &a, const 
 __host__ __device__ __forceinline__ TileView sequence_view(const AttendArgs &a, const SeqRows &q) {
     const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
     return tile_view(a, q.ctx - q.n, q.ctx - q.n + n - 1);
+}
+// ... and at most so many records of `cap` tokens.
+inline int64_t most_records(int64_t cap, int64_t rows, int64_t window, int64_t sinks) {
+    const int64_t all = (cap + kBlock - 1) / kBlock;
+    const int64_t some = (window + rows) / kBlock + 2 + (sinks + kBlock - 1) / kBlock;
+    return window && some < all ? some : all;
+}
+// Where a record that a tile sees stands in its sequence's list.
+__host__ __device__ __forceinline__ int place_of(const TileView &all, int blk) {
+    return blk < all.lead ? blk : blk - all.from + all.lead;
 }
 __host__ __device__ __forceinline__ int view_block(const TileView &v, int i) {
     return i < v.lead ? i : v.from + i - v.lead;
@@ -241,6 +246,94 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// The sum of the lanes up to each: within rows of 16, then over the rows.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true); // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
+              c = __builtin_amdgcn_readlane(v, 47);
+    const int row = (int)((threadIdx.x & 63) >> 4);
+    return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
+}
+
+// Many rows: a workgroup's tile.  The tiles that there are, of all sequences in a
+// row and in each the later ones first (they see more tokens), heads innermost;
+// each in as many ranges as let the workgroups fit the CUs.
+struct PromptTile {
+    int s, head, tile, unit, split, splits;
+    SeqRows q;
+};
+constexpr int kPromptPlaces = 512; // workgroups that run at once
+// `index`: unit * splits + split, or of the join the unit.
+__device__ __forceinline__ bool prompt_tile(const AttendArgs &a, int index, bool ranges, PromptTile &t) {
+    const int lane = threadIdx.x & 63;
+    int total = 0, before = 0, f = 0;
+    t.splits = 1;
+    t.split = 0;
+    t.unit = index;
+    bool finding = a.splits == 1; // (no need to know how many there are)
+    if (finding)
+        f = quotient(index, a.by_heads);
+    for (int base = 0;;) {
+        SeqRows q = {0, 0, 0};
+        int own = 0;
+        if (base + lane < a.c.n_seqs) {
+            q = seq_rows(a.c, base + lane);
+            own = (rows_of(a, q) + kPromptRows - 1) / kPromptRows;
+        }
+        const int upto = wave_scan(own), all = __builtin_amdgcn_readlane(upto, 63);
+        if (!finding) {
+            total += all;
+            base += 64;
+            if (base < a.c.n_seqs)
+                continue;
+            const int units = total * a.c.n_kv_heads;
+            if (units < kPromptPlaces) { // (exact: the quotients are below 2^10)
+                const float n = (float)kPromptPlaces + 0.5f;
+                const int fit = units ? (int)(n * __builtin_amdgcn_rcpf((float)units)) : 1;
+                t.splits = __builtin_amdgcn_readfirstlane(fit < a.splits ? fit : a.splits);
+            }
+            if (ranges && t.splits > 1) {
+                if (index >= kPromptPlaces)
+                    return false;
+                t.unit = __builtin_amdgcn_readfirstlane(
+                    (int)(((float)index + 0.5f) * __builtin_amdgcn_rcpf((float)t.splits)));
+                t.split = index - t.unit * t.splits;
+            }
+            if (t.unit >= units)
+                return false;
+            f = quotient(t.unit, a.by_heads);
+            finding = true;
+            base = 0;
+            if (a.c.n_seqs > 64)
+                continue;
+        }
+        const uint64_t past = __ballot(before + upto > f);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            t.s = base + at;
+            t.head = t.unit - f * a.c.n_kv_heads;
+            t.tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - f;
+            t.q.row0 = __builtin_amdgcn_readlane(q.row0, at);
+            t.q.n = __builtin_amdgcn_readlane(q.n, at);
+            t.q.ctx = __builtin_amdgcn_readlane(q.ctx, at);
+            return true;
+        }
+        before += all;
+        base += 64;
+        if (base >= a.c.n_seqs)
+            return false;
+    }
+}
+// Its ranges.
+__host__ __device__ __forceinline__ void divide(const AttendArgs &a, int splits, TileView &v) {
+    v.share = (int)(((uint32_t)v.count + splits - 1) / (uint32_t)splits);
+    v.share = v.share > a.min_share ? v.share : a.min_share;
+    v.used = (v.count + v.share - 1) / v.share;
 }
 
 // Keeps a branch that few steps take from being made part of all of them.

@@ -140,31 +140,19 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, h = lane >> 5;
 
-    // Later tiles see more tokens and start first; neighbouring workgroups take
-    // different heads, whose tokens stay in the L2 of one XCD.  The sequences of
-    // a tile take turns: workgroups go to the engines of an XCD in turn too, and
-    // a long sequence at the same place of each round would keep to one of them
-    // (prompts of 2500, 267, 1756 and 1630 tokens ran in 651 us that way, in
-    // 423 us so).
-    int b = quotient(blockIdx.x, a.by_splits);
-    const int split = blockIdx.x - b * a.splits;
-    const int heads = a.c.n_seqs * a.c.n_kv_heads;
-    const int tile = a.tiles - 1 - b / heads;
-    b %= heads;
-    const int turn = quotient(b, a.by_heads), head = b - turn * a.c.n_kv_heads;
-    const int s = (turn + tile) % a.c.n_seqs;
-    const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
-    const SeqRows q = seq_rows(a.c, s);
-    const int rows = rows_of(a, q) - tile * kRows;
-    if (rows <= 0)
+    PromptTile at;
+    if (!prompt_tile(a, blockIdx.x, true, at))
         return;
+    const int s = at.s, head = at.head, tile = at.tile, splits = at.splits;
+    const SeqRows q = at.q;
+    const int rows = rows_of(a, q) - tile * kRows;
     const int start = q.ctx - q.n;
     const int last_rho = tile * kRows + (rows < kRows ? rows : kRows) - 1;
     TileView view = view_of(a, q, tile, kRows, rows);
-    divide(a, view);
-    const int begin = split * view.share;
+    divide(a, splits, view);
+    const int begin = at.split * view.share;
     const int stop = begin + view.share < view.count ? begin + view.share : view.count;
-    if (begin >= stop && split > 0)
+    if (begin >= stop && at.split > 0)
         return;
     const int steps = begin < stop ? (stop - begin + TB - 1) / TB : 0;
 
@@ -453,8 +441,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         const int count = stop - begin, stages = (count + PER - 1) / PER;
         const int64_t base = (int64_t)(s * a.c.n_kv_heads + head) * a.image_records;
         auto image_of = [&](int n) {
-            const int blk = view_block(view, begin + n);
-            return blk < all.lead ? blk : blk - all.from + all.lead;
+            return place_of(all, view_block(view, begin + n));
         };
         const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
         auto copy = [&](int st) { // the wave's 4 KB of a stage
@@ -672,9 +659,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     l += __shfl_xor(l, 32, 64);
     if (!live)
         return;
-    const float inv = a.splits > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-    const int64_t slot = ((int64_t)unit * a.splits + split) * kRows + mine;
-    if (a.splits > 1 && h == 0) {
+    const float inv = splits > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+    const int64_t slot = (int64_t)blockIdx.x * kRows + mine;
+    if (splits > 1 && h == 0) {
         a.part_ml[2 * slot] = m;
         a.part_ml[2 * slot + 1] = l;
     }
@@ -692,17 +679,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 put(d * 32 + 8 * r4 + 4 * h, v);
             }
     };
-    const int64_t at = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head;
-    if (a.splits > 1)
+    const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head;
+    if (splits > 1)
         each([&](int col, f32x4 v) { *reinterpret_cast<f32x4 *>(a.part + slot * D + col) = v; });
     else if (a.o_bf16)
         each([&](int col, f32x4 v) {
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + at + col) =
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + to + col) =
                 u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
         });
     else
         each([&](int col, f32x4 v) {
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + at + col) = v;
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + to + col) = v;
         });
 }
 
@@ -834,7 +821,7 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
 
 namespace {
 template <int D> hipError_t prompt(const AttendArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.tiles * a.splits));
+    const dim3 grid((unsigned)a.parts);
     if (a.image_records > 0)
         hipLaunchKernelGGL((attend_prompt_kernel<D, true>), grid, dim3(64 * kWaves), 0, stream, a);
     else

@@ -77,12 +77,11 @@ static void views() {
         a.sinks = pick(2) ? 0 : pick(150);
         if (!pick(20))
             a.sinks = kMaxContext;
-        a.splits = 1 + pick(9);
+        const int splits = 1 + pick(9);
         a.min_share = 1 + pick(9);
         const int first = pick(500) - 20, last = first + pick(70);
-        a.by_splits = make_div((uint32_t)a.splits);
         TileView v = tile_view(a, first, last);
-        divide(a, v);
+        divide(a, splits, v);
         const int cap = a.c.max_pages << (a.c.shift + 5);
         std::vector<int> list;
         for (int i = 0; i < v.count; ++i)
@@ -104,15 +103,47 @@ static void views() {
         }
         for (int b : list)
             EXPECT(b >= 0 && 32 * b < cap);
-        EXPECT(v.used <= a.splits && (v.count == 0) == (v.used == 0));
+        EXPECT(v.used <= splits && (v.count == 0) == (v.used == 0));
         EXPECT((int64_t)v.used * v.share >= v.count && (v.used == 0 || (v.used - 1) * v.share < v.count));
+    }
+    // every tile's records stand in its sequence's list, each once, and the list is
+    // no longer than the bound
+    for (int round = 0; round < 20000; ++round) {
+        AttendArgs a{};
+        a.c.shift = pick(3);
+        a.c.max_pages = 1 + pick(12);
+        a.window = pick(3) ? 1 + pick(300) : 0;
+        a.sinks = pick(2) ? 0 : pick(200);
+        a.group = 1 + pick(9);
+        a.by_group = make_div((uint32_t)a.group);
+        a.c.max_rows = 1 + pick(90);
+        a.rows_max = INT32_MAX;
+        const int cap = a.c.max_pages << (a.c.shift + 5);
+        const SeqRows q = {0, 1 + pick(100), pick(cap + 40)};
+        const TileView all = sequence_view(a, q);
+        const int rows = rows_of(a, q), n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
+        EXPECT(all.count <= most_records(q.ctx < cap ? q.ctx : cap, n, a.window, a.sinks));
+        for (int tile = 0; tile * 16 < rows; ++tile) {
+            const TileView v = view_of(a, q, tile, 16, rows - tile * 16);
+            for (int i = 0; i < v.count; ++i) {
+                const int at = place_of(all, view_block(v, i));
+                EXPECT(at >= 0 && at < all.count && view_block(all, at) == view_block(v, i));
+            }
+            for (int j = 0; j < cap; ++j) // what a row sees, the sequence's rows do
+                if (sees(a, v.last, window_start(a, v.last), j))
+                    EXPECT(any_sees(a, all, j));
+        }
+        for (int blk = 0; blk < 24; ++blk) {
+            bool every = true;
+            for (int j = 32 * blk; j < 32 * blk + 32; ++j)
+                every = every && any_sees(a, all, j);
+            EXPECT(!any_sees_all(a, all, blk) || every);
+        }
     }
     // the ends of the ranges of positions
     AttendArgs a{};
     a.c.shift = 7;
     a.c.max_pages = 1 << 18;
-    a.splits = 5;
-    a.min_share = 8;
     for (int w : {0, 1, kMaxContext})
         for (int f : {-(1 << 22), -1, 0, kMaxContext - 64}) {
             a.window = w;
