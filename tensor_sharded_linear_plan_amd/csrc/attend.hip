@@ -582,6 +582,67 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
     }
 }
 
+// The same with many rows and few ranges: D / 8 lanes add up a row's, four at a
+// time.
+template <int D> __global__ void __launch_bounds__(256) prompt_join_kernel(AttendArgs a) {
+    constexpr int LPR = D / 8, ROWS = 256 / LPR, AHEAD = 4;
+    const int col = threadIdx.x % LPR * 8, me = blockIdx.x * ROWS;
+    PromptTile at;
+    if (!prompt_tile(a, me / kPromptRows, false, at) || at.splits == 1)
+        return; // (its workgroup has written the result)
+    const int mine = me % kPromptRows + threadIdx.x / LPR, rho = at.tile * kPromptRows + mine;
+    const int rows = rows_of(a, at.q);
+    if (rho >= rows)
+        return;
+    TileView view = view_of(a, at.q, at.tile, kPromptRows, rows - at.tile * kPromptRows);
+    divide(a, at.splits, view);
+    const int64_t slot = (int64_t)at.unit * at.splits * kPromptRows + mine;
+    const float *part = a.part + slot * D + col;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + slot;
+    f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+    float top = kNoMax, sum = 0.f;
+    for (int k0 = 0; k0 < view.used; k0 += AHEAD) {
+        f32x4 w[AHEAD][2];
+        float2 f[AHEAD];
+        float to = top;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = k0 + i < view.used ? k0 + i : k0;
+            const f32x4 *p = reinterpret_cast<const f32x4 *>(part + (int64_t)k * (kPromptRows * D));
+            f[i] = ml[(int64_t)k * kPromptRows];
+            w[i][0] = p[0];
+            w[i][1] = p[1];
+            to = fmaxf(to, f[i].x);
+        }
+        const float g = exp2_fast(top - to);
+        top = to;
+        v0 *= g;
+        v1 *= g;
+        sum *= g;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (k0 + i < view.used) {
+                const float e = exp2_fast(f[i].x - top);
+                v0 += w[i][0] * e;
+                v1 += w[i][1] * e;
+                sum += f[i].y * e;
+            }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i = quotient(rho, a.by_group);
+    const int64_t to = (int64_t)(at.q.row0 + i) * a.ldo + (at.head * a.group + rho - i * a.group) * a.o_head + col;
+    v0 *= inv;
+    v1 *= inv;
+    if (a.o_bf16) {
+        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.O) + to) =
+            u32x4{pack_pair(v0[0], v0[1]), pack_pair(v0[2], v0[3]), pack_pair(v1[0], v1[1]), pack_pair(v1[2], v1[3])};
+    } else {
+        f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + to);
+        o[0] = v0;
+        o[1] = v1;
+    }
+}
+
 template <int D, int P> hipError_t decode(const AttendArgs &a, hipStream_t stream) {
     const dim3 grid((unsigned)((a.parts + kWaves - 1) / kWaves));
     hipLaunchKernelGGL((attend_decode_kernel<D, P>), grid, dim3(64 * kWaves), 0, stream, a);
@@ -608,7 +669,7 @@ template <int D> hipError_t prompt_join(const AttendArgs &a, hipStream_t stream)
     if (a.splits > kJoinWave)
         hipLaunchKernelGGL((attend_join_kernel<D, 16, true>), dim3(rows), dim3(1024), 0, stream, a, kPromptRows);
     else
-        hipLaunchKernelGGL((attend_join_kernel<D, 1, true>), dim3(rows / 4), dim3(256), 0, stream, a, kPromptRows);
+        hipLaunchKernelGGL((prompt_join_kernel<D>), dim3(rows / (256 / (D / 8))), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

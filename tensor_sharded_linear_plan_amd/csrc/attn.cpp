@@ -199,7 +199,8 @@ struct AttendPlan {
     int32_t tile_rows, tiles, splits, min_share;
     int32_t shared, parts;
     int64_t units, ranges; // (sequence, head, tile); ranges with sums of their own
-    int32_t images;        // records of a sequence and head that are expanded once, 0: none
+    // records of a sequence and head that are expanded once (0: none), sequences
+    int32_t images, image_seqs;
     size_t image_bytes;
     size_t bytes;
 };
@@ -267,16 +268,21 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
     if (p->parts > kMaxBlocks ||
         (p->ranges && (few ? (int64_t)q.n_seqs * c.n_kv_heads * rows : p->units * tile_rows) > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    // with several tiles a sequence's records are expanded once for all of them
-    p->images = 0;
+    // with several tiles a sequence's records are expanded once for all of them,
+    // for as many sequences as there is room for
+    p->images = p->image_seqs = 0;
     p->image_bytes = 0;
     if (!few && p->tiles >= kImageTiles) {
         int64_t n = most_records(std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens),
                                  std::min<int64_t>(q.max_rows, q.rows), window, sinks);
-        n *= (int64_t)q.n_seqs * c.n_kv_heads;
-        if (n <= kImageBytes / (128 * c.head_dim)) {
-            p->images = (int32_t)(n / ((int64_t)q.n_seqs * c.n_kv_heads));
-            p->image_bytes = round_up((size_t)n * 128 * c.head_dim, 256) + round_up((size_t)n * 4, 256);
+        // (of sequences with more rows than the other kernel's, one has max_rows)
+        const int64_t prompts = std::min<int64_t>(q.n_seqs, 1 + std::max<int64_t>(0, q.rows * group - rows) / (kFewRows + 1));
+        const int64_t of_one = std::max<int64_t>(n, 1) * c.n_kv_heads, fit = kImageBytes / (of_one * 128 * c.head_dim);
+        if (n > 0 && fit > 0) {
+            p->images = (int32_t)n;
+            p->image_seqs = (int32_t)std::min(prompts, fit);
+            p->image_bytes = round_up((size_t)(of_one * p->image_seqs) * 128 * c.head_dim, 256) +
+                             round_up((size_t)(of_one * p->image_seqs) * 4, 256);
         }
     }
     p->bytes = p->image_bytes + round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +
@@ -513,11 +519,12 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
         a.units = (int32_t)k.units;
         a.min_share = k.min_share;
         a.image_records = k.images;
+        a.image_seqs = k.image_seqs;
         if (k.images) {
             a.by_images = make_div((uint32_t)k.images);
             a.images = ws;
             a.image_info = reinterpret_cast<uint32_t *>(
-                ws + round_up((size_t)k.images * (size_t)seqs->n_seqs * cache->n_kv_heads * 128 * cache->head_dim, 256));
+                ws + round_up((size_t)k.images * k.image_seqs * cache->n_kv_heads * 128 * cache->head_dim, 256));
         }
         if (k.ranges) {
             char *const at = ws + k.image_bytes;

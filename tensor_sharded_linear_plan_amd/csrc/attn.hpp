@@ -102,12 +102,12 @@ struct AttendArgs {
     // heads + head) * tiles + tile; many: range = workgroup
     float *part, *part_ml;
     int32_t *spans; // shared: the first and last wave of each unit
-    // many rows, where records are expanded once for the call: of each sequence
-    // and head up to image_records images of 128 head_dim bytes (0: none), and
-    // of each its exponents and flags
+    // many rows, where records are expanded once for the call: of image_seqs
+    // sequences and each head up to image_records images of 128 head_dim bytes
+    // (0: none), and of each its exponents and flags
     char *images;
     uint32_t *image_info;
-    int32_t image_records;
+    int32_t image_records, image_seqs;
     Div by_images;
     int32_t rows_up; // the join: a unit's rows, rounded up to a workgroup's
     Div by_rows, by_tile_rows;
@@ -265,6 +265,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 // each in as many ranges as let the workgroups fit the CUs.
 struct PromptTile {
     int s, head, tile, unit, split, splits;
+    int rank; // of the sequence among those that have tiles
     SeqRows q;
 };
 constexpr int kPromptPlaces = 512; // workgroups that run at once
@@ -272,6 +273,7 @@ constexpr int kPromptPlaces = 512; // workgroups that run at once
 __device__ __forceinline__ bool prompt_tile(const AttendArgs &a, int index, bool ranges, PromptTile &t) {
     const int lane = threadIdx.x & 63;
     int total = 0, before = 0, f = 0;
+    t.rank = 0;
     t.splits = 1;
     t.split = 0;
     t.unit = index;
@@ -316,6 +318,7 @@ __device__ __forceinline__ bool prompt_tile(const AttendArgs &a, int index, bool
         if (past) {
             const int at = __builtin_ctzll(past);
             t.s = base + at;
+            t.rank += __builtin_popcountll(__ballot(own > 0) & ((1ull << at) - 1));
             t.head = t.unit - f * a.c.n_kv_heads;
             t.tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - f;
             t.q.row0 = __builtin_amdgcn_readlane(q.row0, at);
@@ -324,12 +327,36 @@ __device__ __forceinline__ bool prompt_tile(const AttendArgs &a, int index, bool
             return true;
         }
         before += all;
+        t.rank += __builtin_popcountll(__ballot(own > 0));
         base += 64;
         if (base >= a.c.n_seqs)
             return false;
     }
 }
-// Its ranges.
+// The sequence with tiles of that rank.
+__device__ __forceinline__ bool prompt_of_rank(const AttendArgs &a, int rank, int &s, SeqRows &of) {
+    const int lane = threadIdx.x & 63;
+    for (int base = 0; base < a.c.n_seqs; base += 64) {
+        SeqRows q = {0, 0, 0};
+        if (base + lane < a.c.n_seqs)
+            q = seq_rows(a.c, base + lane);
+        uint64_t have = __ballot(rows_of(a, q) > 0);
+        const int n = __builtin_popcountll(have);
+        if (rank < n) {
+            while (rank--)
+                have &= have - 1;
+            const int at = __builtin_ctzll(have);
+            s = base + at;
+            of.row0 = __builtin_amdgcn_readlane(q.row0, at);
+            of.n = __builtin_amdgcn_readlane(q.n, at);
+            of.ctx = __builtin_amdgcn_readlane(q.ctx, at);
+            return true;
+        }
+        rank -= n;
+    }
+    return false;
+}
+// A tile's ranges.
 __host__ __device__ __forceinline__ void divide(const AttendArgs &a, int splits, TileView &v) {
     v.share = (int)(((uint32_t)v.count + splits - 1) / (uint32_t)splits);
     v.share = v.share > a.min_share ? v.share : a.min_share;

@@ -435,11 +435,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
 
     // ---- the walk over images ----
     const TileView all = IMAGES ? sequence_view(a, q) : view;
-    const bool laid_out = IMAGES && all.count <= a.image_records;
+    const bool laid_out = IMAGES && at.rank < a.image_seqs && all.count <= a.image_records;
     if (laid_out && steps > 0) {
         constexpr int PER = TB / 2, IMG = 128 * D, STAGE = BUF, SLOTS = 4; // records of a stage
         const int count = stop - begin, stages = (count + PER - 1) / PER;
-        const int64_t base = (int64_t)(s * a.c.n_kv_heads + head) * a.image_records;
+        const int64_t base = (int64_t)(at.rank * a.c.n_kv_heads + head) * a.image_records;
         auto image_of = [&](int n) {
             return place_of(all, view_block(view, begin + n));
         };
@@ -704,11 +704,10 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
     const int lane = threadIdx.x & 63;
     const int at = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int unit = quotient(at, a.by_images), k = at - unit * a.image_records;
-    const int s = quotient(unit, a.by_heads), head = unit - s * a.c.n_kv_heads;
-    if (s >= a.c.n_seqs)
-        return;
-    const SeqRows q = seq_rows(a.c, s);
-    if (rows_of(a, q) <= 0)
+    const int rank = quotient(unit, a.by_heads), head = unit - rank * a.c.n_kv_heads;
+    int s;
+    SeqRows q;
+    if (rank >= a.image_seqs || !prompt_of_rank(a, rank, s, q))
         return;
     const TileView all = sequence_view(a, q);
     if (k >= all.count || all.count > a.image_records)
@@ -835,7 +834,7 @@ hipError_t launch_attend_prompt(int head_dim, const AttendArgs &a, hipStream_t s
 }
 
 hipError_t launch_attend_images(int head_dim, const AttendArgs &a, hipStream_t stream) {
-    const int64_t n = (int64_t)a.c.n_seqs * a.c.n_kv_heads * a.image_records;
+    const int64_t n = (int64_t)a.image_seqs * a.c.n_kv_heads * a.image_records;
     const dim3 grid((unsigned)((n + 3) / 4));
     if (head_dim == 64)
         hipLaunchKernelGGL(attend_images_kernel<64>, grid, dim3(256), 0, stream, a);
