@@ -32,7 +32,7 @@ class Operand:
     """[rows][heads][d] on the device with chosen strides inside a buffer
     filled with `fill`; `tokens` outermost, or heads outermost."""
 
-    def __init__(self, rows, heads, d, kind, pad=0, head_major=False, fill=7.0, values=None):
+    def __init__(self, rows, heads, d, kind, pad=0, head_major=False, fill=7.0, values=None, strides=None):
         t = torch()
         run = 8 if kind == "bf16" else 4
         pad = pad * run
@@ -40,6 +40,8 @@ class Operand:
             self.ld, self.head = d + pad, max(rows, 1) * (d + pad) + pad
         else:
             self.head, self.ld = d + pad, heads * (d + pad) + pad
+        if strides:
+            self.ld, self.head = strides
         n = max(rows - 1, 0) * self.ld + (heads - 1) * self.head + d + 64
         self.buf = t.full((n,), fill, dtype=tt(kind), device=DEV)
         self.view = self.buf.as_strided((max(rows, 0), heads, d), (self.ld, self.head, 1))

@@ -130,6 +130,15 @@ LONG = [
     (128, 8, 2, 128, [200, 31], [600, 31], 64, 5, "bf16", 0, False),
     (64, 2, 2, 64, [500], [500], 7, 130, "f32", 0, False),
     (128, 7, 1, 256, [100], [1500], 0, 0, "bf16", 0, False),
+    # four tiles of 128 rows and more: records expanded once for all
+    (128, 8, 2, 64, [130], [130], 0, 0, "f32", 0, False),
+    (128, 28, 4, 64, [100, 3, 70, 60], [400, 50, 60, 60], 0, 0, "bf16", 0, False),
+    (64, 32, 8, 32, [400], [1000], 100, 5, "f32", 1, False),
+    (64, 8, 1, 32, [70, 55], [3000, 900], 0, 0, "bf16", 0, True),
+    (128, 4, 4, 128, [700, 40, 390], [700, 300, 391], 0, 0, "f32", 0, False),
+    (64, 4, 4, 64, [513], [600], 33, 200, "bf16", 0, False),
+    (128, 16, 2, 32, [65, 64], [1025, 64], 1, 0, "f32", 0, False),
+    (128, 12, 1, 32, [43], [2400], 700, 64, "bf16", 0, False),
 ]
 
 
@@ -148,7 +157,7 @@ def test_attend_prompts(d, hq, hkv, page, rows, ctx, window, sinks, okind, pad, 
 def test_generated_tokens_beside_a_prompt(d, hq, hkv, window, sinks):
     """Sequences of one or a few rows in one call with long ones, in any order."""
     g = hq // hkv
-    few = 64 // g  # rows that the kernel of few rows takes
+    few = 48 // g  # rows that the kernel of few rows takes
     rows = [1, 300, 1, few, few + 1, 0, 2, 64 + 130 // g]
     ctx = [700, 300, 1, few + 90, few + 90, 50, 333, 700]
     b = au.Batch(rows, ctx, 64, seed=6, lead=2, tail=2)
@@ -187,7 +196,7 @@ def test_equal_weights_give_the_exact_mean(rows, ctx, d):
             at += c
 
 
-@pytest.mark.parametrize("rows", [1, 3, 70])
+@pytest.mark.parametrize("rows", [1, 3, 70, 130])
 @pytest.mark.parametrize("d", [64, 128])
 def test_tokens_out_of_sight_do_not_count(rows, d):
     """Pages hold NaN (0xFF) wherever no token was written; tokens past a row, or
@@ -220,7 +229,7 @@ def test_tokens_out_of_sight_do_not_count(rows, d):
         au.within(O.get()[rows + i:rows + i + 1], want, err + au.U * np.abs(want) + 1e-38, i)
 
 
-@pytest.mark.parametrize("rows", [2, 50])
+@pytest.mark.parametrize("rows", [2, 50, 200])
 def test_rows_that_see_nothing(rows):
     """Rows before position 0, contexts of zero, tables without pages: zeros."""
     d, hq, hkv, page = 128, 4, 2, 32
@@ -236,7 +245,7 @@ def test_rows_that_see_nothing(rows):
     assert (O.get() == 0).all()
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 110])
 def test_strong_and_weak_logits(rows):
     """Logits hundreds apart in either direction and order, a negative and a zero
     scale: the running maximum follows."""
@@ -276,7 +285,7 @@ def test_equal_calls_give_equal_bits_and_sizes_are_hints():
 def test_large_magnitudes():
     """Keys, values and queries far from one: powers of two from 2^-60 to 2^60."""
     d, hq, hkv, page, c = 128, 8, 2, 64, 300
-    for rows in (1, 64):
+    for rows in (1, 64, 128):
         b = au.Batch([rows], [c], page)
         K, V, q = data(b, hkv, d, hq, 51)
         for ke, ve, qe in ((60, -60, -60), (-60, 60, 60), (0, 100, 0), (0, -100, 0), (20, 16, -20)):
@@ -285,3 +294,90 @@ def test_large_magnitudes():
             au.fill(pages, b, k, v)
             Q, O = run(pages, b, hq, q * 2.0 ** qe, d ** -0.5, 0, 0, "f32")
             check(O, Q, b, k, v, hq, d ** -0.5, 0, 0, "f32", rows > 4)
+
+
+@pytest.mark.parametrize("hint", [1, 64, 300, 620, 10 ** 9])
+def test_prompts_longer_than_they_were_said_to_be(hint):
+    """Records are expanded once for the sequences that the workspace has room
+    for, and per tile for the others: the results are right either way."""
+    d, hq, hkv, page = 128, 8, 2, 64
+    b = au.Batch([200, 150, 1, 120], [250, 610, 70, 130], page)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 71)
+    au.fill(pages, b, K, V)
+    for window, sinks in ((0, 0), (77, 9)):
+        Q, O = run(pages, b, hq, q, d ** -0.5, window, sinks, "f32", max_context=hint)
+        check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, "f32", True)
+
+
+def test_room_for_the_records_of_one_prompt():
+    """Tables for 262144 tokens, of which one sequence's records fill what is taken
+    for them: the others' are expanded per tile."""
+    d, hq, hkv, page = 128, 16, 8, 128
+    b = au.Batch([200, 1, 210, 0, 195], [200, 300, 211, 40, 400], page, extra_cols=2048)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 72)
+    au.fill(pages, b, K, V)
+    Q, O = run(pages, b, hq, q, d ** -0.5, 0, 0, "f32", max_context=262144, max_pages=2048)
+    check(O, Q, b, K, V, hq, d ** -0.5, 0, 0, "f32", True)
+
+
+@pytest.mark.parametrize("rows", [1, 60, 512])
+@pytest.mark.parametrize("ke,ve", [(30, 50), (-30, -50), (0, 100), (0, -100)])
+def test_later_tokens_of_another_magnitude(rows, ke, ve):
+    """The first 256 tokens and the others differ by powers of two: rows among the
+    first are as exact as without the others, rows behind them see both."""
+    d, hq, hkv, page, c, half = 64, 8, 2, 64, 512, 256
+    b = au.Batch([rows], [c], page)
+    K, V, q = data(b, hkv, d, hq, 81)
+    K[half:] *= 2.0 ** ke
+    V[half:] *= 2.0 ** ve
+    q[max(0, rows - (c - half)):] *= 2.0 ** -max(ke, 0)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    au.fill(pages, b, K, V)
+    Q, O = run(pages, b, hq, q, d ** -0.5, 0, 0, "f32")
+    check(O, Q, b, K, V, hq, d ** -0.5, 0, 0, "f32", rows > 12)
+    if rows == c:
+        got, qq = O.get()[:half], Q.get()[:half]
+        k, v = K[:half], V[:half]
+        want, mag = au.attend(qq, au.held(k), au.held(v), d ** -0.5, 0, 0, 0)
+        err = bounds(qq, au.held(k), au.held(v), au.quantise(k)[1:], au.quantise(v)[1:], d ** -0.5, mag, True)
+        au.within(got, want, err + au.U * np.abs(want) + 1e-38)
+
+
+@pytest.mark.parametrize("longest", [1, 3, 300])
+def test_a_thousand_sequences(longest):
+    d, hq, hkv, page = 64, 4, 2, 32
+    r = au.rng(91)
+    rows = [1] * 1100
+    rows[1050], rows[3], rows[77] = longest, 0, 2
+    ctx = [int(x) for x in r.integers(1, 70, 1100)]
+    ctx[1050] = 310
+    b = au.Batch(rows, ctx, page, seed=9, lead=1, tail=1)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 92)
+    au.fill(pages, b, K, V)
+    Q, O = run(pages, b, hq, q, d ** -0.5, 0, 0, "f32")
+    check(O, Q, b, K, V, hq, d ** -0.5, 0, 0, "f32", longest > 24)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 150])
+def test_far_pages_and_strides(rows):
+    """Pages past 2^32 bytes, rows and heads of the operands past 2^31 elements."""
+    d, hq, hkv, page = 64, 8, 2, 4096
+    b = au.Batch([rows], [5000], page)
+    n = 2 ** 32 // (page // 32 * hkv * 36 * d) + 40
+    pages = au.Pages(n, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 95)
+    b.dev[2] = torch().from_numpy(np.int32(n - 1) - b.table).to(DEV)  # the last pages
+    au.fill(pages, b, K, V)
+    far = 2 ** 30 + 8
+    strides = (far, d) if rows == 5 else (hq * d, d) if rows == 1 else (d, 2 ** 29 + 8)
+    Q = au.Operand(b.rows, hq, d, "bf16", strides=strides, values=q)
+    d_ = b.dict()
+    O = au.Operand(b.rows, hq, d, "bf16", strides=strides)
+    nws = tsl.cache_attention_workspace_size(pages.dict, d_, hq)
+    ws = torch().empty(nws, dtype=torch().uint8, device=DEV)
+    tsl.cache_attention(pages.dict, d_, hq, Q.view, Q.ld, Q.head, 0.125, 0, 0, tsl.BF16, O.view, O.ld,
+                        O.head, ws, nws)
+    check(O, Q, b, K, V, hq, 0.125, 0, 0, "bf16", rows > 12)
