@@ -122,7 +122,8 @@ typedef struct tsl_cache {
  *               from row_start[n_seqs] on are not read and left as they were.
  *   max_rows:   no sequence has more rows (rows past it are left as they
  *               were).
- *   max_context: what the work is divided for; longer contexts are right too.
+ *   max_context: what the work is divided and the workspace sized for; longer
+ *               contexts are right too, and slower.
  * The DEVICE arrays are read by the kernels, which go by their bounds: a
  * position before 0, or from max_pages page_tokens on, or in a page outside
  * 0 .. n_pages - 1 is not there (nothing is written to it, nothing read from
@@ -171,7 +172,9 @@ tsl_status cache_read(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dt
                       void *stream);
 
 /* cache_attention_workspace_size -- workspace bytes cache_attention needs (of
- * cache and seqs only the sizes are read).  0 for many calls.  Host only. */
+ * cache and seqs only the sizes are read).  0 for some calls, up to about 1 GiB
+ * more than the partial sums' where prompts of several hundred rows have long
+ * contexts.  Host only. */
 tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs *seqs,
                                           int32_t n_q_heads, int32_t window, int32_t sinks,
                                           size_t *bytes);
@@ -190,11 +193,15 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  *   O: DEVICE [rows][n_q_heads][head_dim], type odtype (F32 or BF16).
  *   workspace: 256-byte aligned, cache_attention_workspace_size() bytes; may
  *      be null when that is 0.  Calls that overlap in time need one each.
- * Products accumulate in binary32, the softmax is binary32; the 4-bit values
- * enter exactly up to binary32 rounding in calls of few rows, and rounded to
- * 11 bits (binary16, scaled by powers of two) in longer ones, as the
- * probabilities are.  Equal calls give equal bits.  O shares no byte with Q,
- * the cache or the workspace.  scale is finite, window and sinks 0 .. 2^30.
+ * Products accumulate in binary32, the softmax is binary32.  For sequences of
+ * up to 48 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
+ * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
+ * exactly up to binary32 rounding; for longer ones rounded to 11 bits
+ * (binary16, scaled by powers of two), as the probabilities are.  Both kinds may
+ * be in one call (generated tokens beside a prompt's chunk).  |Q| stays below
+ * 2^110, and scale sum |q k| of a visible token within binary32's range.  Equal
+ * calls give equal bits.  O shares no byte with Q, the cache or the workspace.
+ * scale is finite, window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
  * n_kv_heads), TSL_ERR_UNSUPPORTED, TSL_ERR_BUFFER_TOO_SMALL,
  * TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides whole 16 bytes),

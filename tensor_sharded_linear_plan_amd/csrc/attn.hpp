@@ -321,6 +321,9 @@ __device__ __forceinline__ bool prompt_tile(const AttendArgs &a, int index, bool
             t.rank += __builtin_popcountll(__ballot(own > 0) & ((1ull << at) - 1));
             t.head = t.unit - f * a.c.n_kv_heads;
             t.tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - f;
+            // (row_start that descends may give any sum)
+            if (t.tile < 0 || t.tile >= __builtin_amdgcn_readlane(own, at))
+                return false;
             t.q.row0 = __builtin_amdgcn_readlane(q.row0, at);
             t.q.n = __builtin_amdgcn_readlane(q.n, at);
             t.q.ctx = __builtin_amdgcn_readlane(q.ctx, at);

@@ -2,25 +2,37 @@
 // (prompts and their chunks): the same pass over the tokens as attend.hip, with
 // each expanded token shared by up to 256 query rows.
 //
-// A workgroup takes 256 query rows of one sequence and K/V head (32 a wave) and
-// walks the records they see, TB at a time: the codes of the next TB records, in
-// registers since the step before, are expanded to binary16 into one half of
-// LDS while the other half is multiplied.  S^T = K Q^T and O^T = V^T P^T on
-// 32x32x16 MFMAs, so a lane holds one query row (column l % 32) throughout and
-// the probabilities leave S^T as O^T's operand.  A record at a time, each
-// product runs beside vector work that does not wait for it: the logits of the
-// next record beside the exponentials of this, the weighted sum beside the
-// expansion of the next step's codes.
+// A workgroup takes 128 query rows of one sequence and K/V head (32 a wave) and
+// walks the records they see.  S^T = K Q^T and O^T = V^T P^T on 32x32x16 MFMAs, so
+// a lane holds one query row (column l % 32) throughout and the probabilities
+// leave S^T as O^T's operand.  The logits of a record are multiplied while the
+// exponentials of the one before it are formed.  Two workgroups share a CU, so
+// that one reads Q and writes O beside the other's products (256 rows, one a CU:
+// prompts of 2500 tokens 264 us, so 247).
+//
+// With four tiles of rows or more, attend_images expands the records of a
+// sequence once for all of them, to the two products' operands as they are read;
+// a workgroup copies them into four stages of LDS (global_load_lds), two ahead.
+// A 4-bit cache's operands are 3.6 times its bytes, but every tile reads them
+// again out of the L2, and expanding them there had been 29% of the time (a chunk
+// of 512 rows after 16000 tokens, 32 heads over 4 of 128: 189 us that way, 153 us
+// so, 890 TFLOP/s where a large library product reaches 1220).  What is left is
+// bound by the matrix and the vector units, which overlap in part: of 158 us, 138
+// were left without the softmax, 139 without the operands' reads, 148 without the
+// copies, 119 of the products alone.
+// With fewer tiles, or where there is no room for the images, the codes of the
+// next TB records, in registers since the step before, are expanded into one half
+// of LDS while the other half is multiplied.
 //
 // Binary16 has 11 bits where bf16 has 8: a bf16 K would move a logit by 2^-9 of
 // its terms, which the exponential passes on to the result at the size of the
 // result's own rounding.  Its range is met with powers of two, as the 4-bit
 // GEMM's is: a row of Q by its largest element, the K and the V values of the
-// records in hand by a bound of theirs (15 |s| + |b|), V's never below that of
-// earlier ones, which the accumulators carry.  Probabilities are 2^9 times their
-// value relative to the running reference, which moves only when a sum of 16 of
-// them comes to 2^15 (none is lost above 2^-33 of the largest): the common step
-// looks for no maximum.
+// records in hand by a bound of theirs (15 |s| + |b|); the accumulators follow
+// V's, down to 2^-64 of the largest so far (images) or never down (codes).
+// Probabilities are 2^9 times their value relative to the running reference,
+// which moves only when a sum of 16 of them comes to 2^15 (none is lost above
+// 2^-33 of the largest): the common step looks for no maximum.
 #include "attn.hpp"
 #include "gemm_common.hpp"
 
