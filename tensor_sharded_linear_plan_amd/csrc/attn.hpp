@@ -114,7 +114,6 @@ struct AttendArgs {
 };
 
 constexpr int kMaxSplits = 1024;
-constexpr int kMaxWaves = 4096;  // parts of a shared call: 16 waves on each of 256 CUs
 constexpr int kMaxShared = 1024; // sequences of a shared call
 constexpr int kJoinWave = 16; // ranges that one wave adds; 16 waves more
 // attend_decode: tiles of 16 / P query rows (P 1, 2, or with head_dim up to 128 4),
