@@ -199,9 +199,10 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * exactly up to binary32 rounding; for longer ones rounded to 11 bits
  * (binary16, scaled by powers of two), as the probabilities are.  Both kinds may
  * be in one call (generated tokens beside a prompt's chunk).  |Q| stays below
- * 2^110, and scale sum |q k| of a visible token within binary32's range.  Equal
+ * 2^110, and scale sum |q k| of a visible token within binary32's range (what
+ * other rows get does not hang on a row that does not keep to it).  Equal
  * calls give equal bits.  O shares no byte with Q, the cache or the workspace.
- * scale is finite, window and sinks 0 .. 2^30.
+ * scale log2(e) is finite, window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
  * n_kv_heads), TSL_ERR_UNSUPPORTED, TSL_ERR_BUFFER_TOO_SMALL,
  * TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides whole 16 bytes),

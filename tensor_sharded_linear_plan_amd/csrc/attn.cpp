@@ -21,6 +21,7 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxTokens = int64_t(1) << 30; // of a page table's row
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxHeads = 1024;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 bool dense_type(int d) { return d == TSL_F32 || d == TSL_BF16; }
 size_t elem(int d) { return d == TSL_F32 ? 4 : 2; }
@@ -460,7 +461,7 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     tsl_status st = attend_check(cache, seqs, n_q_heads, window, sinks, true);
     if (st != TSL_OK)
         return st;
-    if (!Q || !O || !dense_type(odtype) || !isfinite(scale) || ldq < 0 || q_head < 0 || ldo < 0 ||
+    if (!Q || !O || !dense_type(odtype) || !isfinite(scale * kLog2e) || ldq < 0 || q_head < 0 || ldo < 0 ||
         o_head < 0)
         return TSL_ERR_INVALID_ARG;
     const Heads q = {Q, seqs->rows, n_q_heads, cache->head_dim, ldq, q_head, 2};
@@ -493,7 +494,7 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
     a.q_head = q_head;
     a.ldo = ldo;
     a.o_head = o_head;
-    a.scale = scale * 1.44269504088896340736f;
+    a.scale = scale * kLog2e;
     a.group = n_q_heads / cache->n_kv_heads;
     a.window = window;
     a.sinks = sinks;

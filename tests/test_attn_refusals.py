@@ -159,6 +159,7 @@ def test_attention_refusals(tsl_lib):
                   (dict(window=-1), "INVALID_ARG"), (dict(sinks=-1), "INVALID_ARG"),
                   (dict(window=(1 << 30) + 1), "UNSUPPORTED"), (dict(sinks=(1 << 30) + 1), "UNSUPPORTED"),
                   (dict(scale=float("nan")), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
+                  (dict(scale=3e38), "INVALID_ARG"),
                   (dict(odtype=2), "INVALID_ARG"), (dict(ldq=1023), "INVALID_ARG"),
                   (dict(q_head=100), "INVALID_ARG"), (dict(ldo=900), "INVALID_ARG"),
                   (dict(Q=addr(2) + 8), "MISALIGNED"), (dict(O=addr(3) + 2), "MISALIGNED"),

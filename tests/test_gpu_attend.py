@@ -1,8 +1,8 @@
 """cache_attention on the GPU against its definition in binary64 over the values
 that the cache holds.
 
-Tolerance, u = 2^-24, w = 2^-11 (half a step of binary16; operands of calls of
-more than `FEW` query rows are rounded to it, others enter exactly).  With
+Tolerance, u = 2^-24, w = 2^-11 (half a step of binary16; operands of sequences
+of more than `FEW` query rows a K/V head are rounded to it, others enter exactly).  With
 a = sum |q| over a run of 64, the logit's terms s (128 + c) q and 128 s q are
 bounded by 271 |s| a and b q by |b| a; a sum of n terms is off by at most n u of
 their magnitudes, n = 72, so the logit by
@@ -21,6 +21,7 @@ from tensor_sharded_linear_plan_amd import binding as tsl
 pytestmark = pytest.mark.gpu
 
 W16 = 2.0 ** -11
+FEW = 48
 
 
 def run(pages, batch, hq, q, scale, window=0, sinks=0, okind="bf16", pad=0, head_major=False,
@@ -117,7 +118,7 @@ def test_attend_few_rows(d, hq, hkv, page, rows, ctx, window, sinks, okind, pad,
     K, V, q = data(b, hkv, d, hq, d + hq + page)
     au.fill(pages, b, K, V)
     Q, O = run(pages, b, hq, q, d ** -0.5, window, sinks, okind, pad, hm)
-    check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, okind, False)
+    check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, okind, d < 256 and max(rows) * hq // hkv > FEW)
 
 
 LONG = [
@@ -157,7 +158,7 @@ def test_attend_prompts(d, hq, hkv, page, rows, ctx, window, sinks, okind, pad, 
 def test_generated_tokens_beside_a_prompt(d, hq, hkv, window, sinks):
     """Sequences of one or a few rows in one call with long ones, in any order."""
     g = hq // hkv
-    few = 48 // g  # rows that the kernel of few rows takes
+    few = FEW // g  # rows that the kernel of few rows takes
     rows = [1, 300, 1, few, few + 1, 0, 2, 64 + 130 // g]
     ctx = [700, 300, 1, few + 90, few + 90, 50, 333, 700]
     b = au.Batch(rows, ctx, 64, seed=6, lead=2, tail=2)
@@ -381,3 +382,61 @@ def test_far_pages_and_strides(rows):
     tsl.cache_attention(pages.dict, d_, hq, Q.view, Q.ld, Q.head, 0.125, 0, 0, tsl.BF16, O.view, O.ld,
                         O.head, ws, nws)
     check(O, Q, b, K, V, hq, 0.125, 0, 0, "bf16", rows > 12)
+
+
+@pytest.mark.parametrize("rows", [3, 60, 200])
+def test_queries_that_are_not_finite(rows):
+    """A row whose query is NaN or infinite in one head: the other heads of it and
+    the other rows are as they would be."""
+    d, hq, hkv, page, c = 128, 8, 2, 64, 300
+    b = au.Batch([rows, rows], [c, c], page, seed=8)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 97)
+    au.fill(pages, b, K, V)
+    Q = au.Operand(b.rows, hq, d, "bf16", values=q)
+    for bad in (np.nan, np.inf, -np.inf):
+        q2 = q.copy()
+        q2[1, 3, 7], q2[rows + rows // 2, 0, 100] = bad, bad
+        _, O = run(pages, b, hq, q2, d ** -0.5, 0, 0, "f32")
+        got = O.get()
+        for i, x in ((1, 3), (rows + rows // 2, 0)):
+            if np.isnan(bad):
+                assert np.isnan(got[i, x]).all()
+            got[i, x] = 0  # not compared
+        at = 0
+        for s in range(2):
+            qq = Q.get()[s * rows:(s + 1) * rows]
+            k, v = K[at:at + c], V[at:at + c]
+            want, mag = au.attend(qq, au.held(k), au.held(v), d ** -0.5, 0, 0, c - rows)
+            err = bounds(qq, au.held(k), au.held(v), au.quantise(k)[1:], au.quantise(v)[1:], d ** -0.5, mag,
+                         rows * 4 > FEW)
+            i, x = ((1, 3), (rows // 2, 0))[s]
+            want[i, x] = 0
+            au.within(got[s * rows:(s + 1) * rows], want, err + au.U * np.abs(want) + 1e-38, s)
+            at += c
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, the same cache: each as by itself."""
+    t = torch()
+    d, hq, hkv, page = 128, 16, 2, 64
+    b = au.Batch([1, 130, 1, 2], [3000, 900, 40, 700], page, seed=12)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 98)
+    au.fill(pages, b, K, V)
+    kinds = ((1, 0, 0), (-0.5, 100, 4))
+    alone = [run(pages, b, hq, q * f, d ** -0.5, w, s, "f32") for f, w, s in kinds]
+    seqs, calls = b.dict(), []
+    for k in range(8):
+        f, w, s = kinds[k % 2]
+        n = tsl.cache_attention_workspace_size(pages.dict, seqs, hq, w, s)
+        calls.append((w, s, au.Operand(b.rows, hq, d, "bf16", values=q * f), au.Operand(b.rows, hq, d, "f32"),
+                      n, t.empty(max(n, 256), dtype=t.uint8, device=DEV)))
+    streams = [t.cuda.Stream() for _ in kinds]
+    t.cuda.synchronize()
+    for k, (w, s, Q, O, n, ws) in enumerate(calls):
+        tsl.cache_attention(pages.dict, seqs, hq, Q.view, Q.ld, Q.head, d ** -0.5, w, s, tsl.F32, O.view,
+                            O.ld, O.head, ws, n, streams[k % 2].cuda_stream)
+    t.cuda.synchronize()
+    for k, c in enumerate(calls):
+        assert t.equal(c[3].buf, alone[k % 2][1].buf), k
