@@ -31,7 +31,7 @@
 // records in hand by a bound of theirs (15 |s| + |b|); the accumulators follow
 // V's, down to 2^-64 of the largest so far (images) or never down (codes).
 // Probabilities are 2^9 times their value relative to the running reference,
-// which moves only when a sum of 16 of them comes to 2^15 (none is lost above
+// which moves only when a sum of 16 of them comes to 65000 (none is lost above
 // 2^-33 of the largest): the common step looks for no maximum.
 #include "attn.hpp"
 #include "gemm_common.hpp"
@@ -43,7 +43,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kProbScale = 9.f;     // log2
-constexpr float kProbMost = 32768.f;  // of a lane's 16 probabilities together
+constexpr float kProbMost = 65000.f;  // of a lane's 16 probabilities together: binary16 holds each
 constexpr int kWaves = 4; // a workgroup's; two share a CU
 constexpr int kRows = 32 * kWaves;
 static_assert(kRows == kPromptRows, "rows of a tile");
