@@ -187,7 +187,7 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  *     j > i - window  (window 0: all)   or   j < sinks.
  * Query head h reads K/V head h / (n_q_heads / n_kv_heads).  A row that sees
  * no token gets zeros.  A token that a row does not see has no influence on
- * it, whatever its page holds; a visible K run that reads NaN makes the row
+ * it, whatever its page holds (but for the scaling below); a visible K run that reads NaN makes the row
  * NaN, a visible V run its 64 columns.
  *   Q: DEVICE [rows][n_q_heads][head_dim], BF16.
  *   O: DEVICE [rows][n_q_heads][head_dim], type odtype (F32 or BF16).
@@ -197,12 +197,14 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * up to 48 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
  * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
  * exactly up to binary32 rounding; for longer ones rounded to 11 bits
- * (binary16, scaled by powers of two), as the probabilities are.  Both kinds may
- * be in one call (generated tokens beside a prompt's chunk).  |Q| stays below
- * 2^110, and scale sum |q k| of a visible token within binary32's range (what
- * other rows get does not hang on a row that does not keep to it).  Equal
- * calls give equal bits.  O shares no byte with Q, the cache or the workspace.
- * scale log2(e) is finite, window and sinks 0 .. 2^30.
+ * (binary16), as the probabilities are, scaled by a power of two that up to 128
+ * neighbouring tokens which some row of the sequence sees have in common: values
+ * below 2^-22 of the largest of those lose bits.  Both kinds may be in one call
+ * (generated tokens beside a prompt's chunk).  |Q| stays below 2^110, and scale
+ * sum |q k| of a visible token within binary32's range (what other rows get does
+ * not hang on a row that does not keep to it).  Equal calls give equal bits.  O
+ * shares no byte with Q, the cache or the workspace.  scale log2(e) is finite,
+ * window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
  * n_kv_heads), TSL_ERR_UNSUPPORTED, TSL_ERR_BUFFER_TOO_SMALL,
  * TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides whole 16 bytes),

@@ -731,7 +731,7 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
         for (int i = lane; i < 8 * D; i += 64)
             reinterpret_cast<u32x4 *>(img)[i] = u32x4{0, 0, 0, 0};
         if (lane == 0)
-            a.image_info[at] = 256 | 256 << 10;
+            a.image_info[at] = 120 | 120 << 10; // (exponents as those of zeros)
         return;
     }
     const u32x4 *p = reinterpret_cast<const u32x4 *>(rec);

@@ -440,3 +440,29 @@ def test_two_calls_at_once():
     t.cuda.synchronize()
     for k, c in enumerate(calls):
         assert t.equal(c[3].buf, alone[k % 2][1].buf), k
+
+
+@pytest.mark.parametrize("rows", [1, 60, 150])
+@pytest.mark.parametrize("ve", [-100, 90])
+def test_missing_pages_among_values_of_any_magnitude(rows, ve):
+    t = torch()
+    d, hq, hkv, page, c = 64, 8, 2, 32, 320
+    b = au.Batch([rows], [c], page, seed=14)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 99)
+    V = V * 2.0 ** ve
+    au.fill(pages, b, K, V)
+    table = b.table.copy()
+    table[0, [0, 4, 9]] = -1, b.n_pages, -7
+    b.dev[2] = t.from_numpy(table).to(DEV)
+    keep = np.r_[32:128, 160:288]
+    for window, sinks in ((0, 0), (200, 40)):
+        Q, O = run(pages, b, hq, q, d ** -0.5, window, sinks, "f32")
+        got, qq = O.get(), Q.get()
+        for i in range(rows):
+            pos = c - rows + i
+            j = keep[(keep <= pos) & ((keep > pos - window) | (keep < sinks) | (window == 0))]
+            want, mag = au.attend(qq[i:i + 1], au.held(K[j]), au.held(V[j]), d ** -0.5, 0, 0, len(j) - 1)
+            err = bounds(qq[i:i + 1], au.held(K[j]), au.held(V[j]), au.quantise(K[j])[1:],
+                         au.quantise(V[j])[1:], d ** -0.5, mag, rows * 4 > FEW)
+            au.within(got[i:i + 1], want, err + au.U * np.abs(want) + 1e-38, i)
