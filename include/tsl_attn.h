@@ -187,8 +187,8 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  *     j > i - window  (window 0: all)   or   j < sinks.
  * Query head h reads K/V head h / (n_q_heads / n_kv_heads).  A row that sees
  * no token gets zeros.  A token that a row does not see has no influence on
- * it, whatever its page holds (but for the scaling below); a visible K run that reads NaN makes the row
- * NaN, a visible V run its 64 columns.
+ * it, whatever its page holds (but for the scaling below); a visible K run that
+ * reads NaN makes the row NaN, a visible V run its 64 columns.
  *   Q: DEVICE [rows][n_q_heads][head_dim], BF16.
  *   O: DEVICE [rows][n_q_heads][head_dim], type odtype (F32 or BF16).
  *   workspace: 256-byte aligned, cache_attention_workspace_size() bytes; may

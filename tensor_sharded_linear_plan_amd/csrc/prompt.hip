@@ -29,7 +29,8 @@
 // result's own rounding.  Its range is met with powers of two, as the 4-bit
 // GEMM's is: a row of Q by its largest element, the K and the V values of the
 // records in hand by a bound of theirs (15 |s| + |b|); the accumulators follow
-// V's, down to 2^-64 of the largest so far (images) or never down (codes).
+// V's, by multiples of 8 (few neighbours differ, and 22 octaves below the largest
+// value keep all bits), down to 2^-64 of the largest so far.
 // Probabilities are 2^9 times their value relative to the running reference,
 // which moves only when a sum of 16 of them comes to 65000 (none is lost above
 // 2^-33 of the largest): the common step looks for no maximum.
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     // ---- the walk over codes ----
     if (!laid_out) {
     uint64_t there = 0, there1 = 0, clear = 0, clear1 = 0; // of this step, the next
-    int ek = 0, ek1 = 0, ev1 = 0, page = -1;
+    int ek = 0, ek1 = 0, ev1 = 0, top = 0, page = -1;
     bool bad = false, bad1 = false, full1 = false;
     f32x16 x[2];
     if (steps > 0) {
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
         fetch(0, page0, there);
         seen_by(0, there, clear, full);
         exponents(0, full, ek, ev, bad);
+        top = ev = (ev + 7) & ~7;
         expand_k(0, full, ek, lds);
         expand_v(0, full && !bad, ev, lds + 2 * BUF);
         fetch(1, page1, there1);
@@ -636,7 +638,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             if (t == TB - 2) {
                 seen_by(step + 1, there1, clear1, full1);
                 exponents(step + 1, full1, ek1, ev1, bad1);
-                ev1 = ev1 > ev ? ev1 : ev;
+                ev1 = (ev1 + 7) & ~7;
+                top = top > ev1 ? top : ev1;
+                ev1 = ev1 > top - 64 ? ev1 : top - 64;
                 expand_k(step + 1, full1, ek1, kb1);
                 __syncthreads();
             } else if (t == TB - 1) {
@@ -709,8 +713,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
 // operands of its first product, ST pieces of 1 KB in the order in which a wave
 // reads them (lane 32 h + c holds 8 columns of token c), then V as those of the
 // second (column c, 8 tokens), in binary16 by exponents of the record's own.
-// V's are multiples of 8, so that few neighbours differ: 22 octaves below the
-// largest value keep all bits.
 template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(AttendArgs a) {
     constexpr int G = D / 64, W = D / 32;
     const int lane = threadIdx.x & 63;

@@ -466,3 +466,29 @@ def test_missing_pages_among_values_of_any_magnitude(rows, ve):
             err = bounds(qq[i:i + 1], au.held(K[j]), au.held(V[j]), au.quantise(K[j])[1:],
                          au.quantise(V[j])[1:], d ** -0.5, mag, rows * 4 > FEW)
             au.within(got[i:i + 1], want, err + au.U * np.abs(want) + 1e-38, i)
+
+
+@pytest.mark.parametrize("rows", [1, 60, 150])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_without_weight(rows, d):
+    """128 tokens whose logits leave them no weight (e^-512 d / 64) and whose values
+    are 2^40 times the others': the others keep their bits."""
+    hq, hkv, page, c = 4, 1, 64, 600
+    b = au.Batch([rows], [c], page, seed=15)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = data(b, hkv, d, hq, 100, kscale=0.05)
+    q[:] = 1.0
+    for lo in (0, 256):
+        k, v = K.copy(), V.copy()
+        k[lo:lo + 128] = -8.0
+        v[lo:lo + 128] *= 2.0 ** 40
+        rest = np.r_[0:lo, lo + 128:c]
+        au.fill(pages, b, k, v)
+        Q, O = run(pages, b, hq, q, 1.0, 0, 0, "f32")
+        got, qq = O.get(), Q.get()
+        for i in range(0, rows, 7):
+            j = rest[rest <= c - rows + i]
+            want, mag = au.attend(qq[i:i + 1], au.held(k[j]), au.held(v[j]), 1.0, 0, 0, len(j) - 1)
+            err = bounds(qq[i:i + 1], au.held(k[j]), au.held(v[j]), au.quantise(k[j])[1:],
+                         au.quantise(v[j])[1:], 1.0, mag, rows * 4 > FEW)
+            au.within(got[i:i + 1], want, err + au.U * np.abs(want) + 1e-38, (lo, i))
