@@ -115,7 +115,8 @@ struct AttendArgs {
 
 constexpr int kMaxSplits = 1024;
 constexpr int kMaxShared = 1024; // sequences of a shared call
-constexpr int kJoinWave = 16; // ranges that one wave adds; 16 waves more
+constexpr int kJoinWave = 16;  // ranges that one wave adds; 16 waves more
+constexpr int kJoinLanes = 64; // ... that the lanes of a row add, with many rows
 // attend_decode: tiles of 16 / P query rows (P 1, 2, or with head_dim up to 128 4),
 // three stages of a record for each of four waves in a CU's 160 KB of LDS.
 // Workgroups that share a CU (four: a start more a CU does not hide better):
