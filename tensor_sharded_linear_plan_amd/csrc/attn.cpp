@@ -221,11 +221,12 @@ constexpr int kWholeRecords = 6;
 // of 16).
 constexpr int kAttendShare = 1, kPromptShare = 8;
 
-// Tiles of a sequence and head from which on expanding its records once is faster
-// than for each tile (8 sequences of 2000 tokens: 2 tiles 58 us so and 53 without,
-// 4 82 and 85, 8 98 and 104; 5 tiles over 16000 tokens 75 and 82), and the most
-// memory that takes.
-constexpr int kImageTiles = 4;
+// Expanding the records of the sequences once costs a launch and about what two
+// tiles' expansion does: it is done for so many records times the tiles beyond two
+// (8 heads, 500 records: 3 tiles 29.3 us so and 26.7 without, 4 34.2 and 31.3, 5
+// 33.8 and 33.6; 4000 records: 2 tiles 53.8 and 52.2, 3 59.1 and 62.2, 4 66.6 and
+// 76.5, 5 75 and 93), and this is the most memory it takes.
+constexpr int64_t kImageWork = 2048;
 constexpr int64_t kImageBytes = int64_t(1) << 30;
 
 tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int64_t rows, bool few,
@@ -269,17 +270,17 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
     if (p->parts > kMaxBlocks ||
         (p->ranges && (few ? (int64_t)q.n_seqs * c.n_kv_heads * rows : p->units * tile_rows) > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    // with several tiles a sequence's records are expanded once for all of them,
+    // with several tiles a sequence's records may be expanded once for all of them,
     // for as many sequences as there is room for
     p->images = p->image_seqs = 0;
     p->image_bytes = 0;
-    if (!few && p->tiles >= kImageTiles) {
+    if (!few && p->tiles > 2) {
         int64_t n = most_records(std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens),
                                  std::min<int64_t>(q.max_rows, q.rows), window, sinks);
         // (of sequences with more rows than the other kernel's, one has max_rows)
         const int64_t prompts = std::min<int64_t>(q.n_seqs, 1 + std::max<int64_t>(0, q.rows * group - rows) / (kFewRows + 1));
         const int64_t of_one = std::max<int64_t>(n, 1) * c.n_kv_heads, fit = kImageBytes / (of_one * 128 * c.head_dim);
-        if (n > 0 && fit > 0) {
+        if (n > 0 && fit > 0 && of_one * std::min(prompts, fit) >= (kImageWork + p->tiles - 3) / (p->tiles - 2)) {
             p->images = (int32_t)n;
             p->image_seqs = (int32_t)std::min(prompts, fit);
             p->image_bytes = round_up((size_t)(of_one * p->image_seqs) * 128 * c.head_dim, 256) +

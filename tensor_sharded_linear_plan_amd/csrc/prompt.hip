@@ -10,8 +10,8 @@
 // that one reads Q and writes O beside the other's products (256 rows, one a CU:
 // prompts of 2500 tokens 264 us, so 247).
 //
-// With four tiles of rows or more, attend_images expands the records of a
-// sequence once for all of them, to the two products' operands as they are read;
+// With three tiles of rows or more, and enough records to be worth a launch,
+// attend_images expands the records of a sequence once for all of them, to the two products' operands as they are read;
 // a workgroup copies them into four stages of LDS (global_load_lds), two ahead.
 // A 4-bit cache's operands are 3.6 times its bytes, but every tile reads them
 // again out of the L2, and expanding them there had been 29% of the time (a chunk

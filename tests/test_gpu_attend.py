@@ -24,12 +24,29 @@ W16 = 2.0 ** -11
 FEW = 48
 
 
+@pytest.fixture(params=[False, True], ids=["", "roomy"], autouse=True)
+def roomy(request, monkeypatch):
+    """Every test twice: with page tables of the sizes in use, and as wide as for long
+    contexts, by which records of prompts are expanded once for all tiles."""
+    monkeypatch.setitem(globals(), "ROOMY", request.param)
+
+
+def widened(pages, batch, d):
+    t = torch()
+    w = max(2200 * 32 // (pages.page_tokens * pages.heads), 1) + batch.table.shape[1]
+    table = t.full((max(len(batch.n), 1), w), -1, dtype=t.int32, device=DEV)
+    table[:len(batch.n), :batch.max_pages] = d["page_table"][:, :batch.max_pages]
+    d.update(page_table=table, ld_table=w, max_pages=w, max_context=w * pages.page_tokens)
+
+
 def run(pages, batch, hq, q, scale, window=0, sinks=0, okind="bf16", pad=0, head_major=False,
         stream=None, **kw):
     Q = q if isinstance(q, au.Operand) else au.Operand(batch.rows, hq, pages.d, "bf16", pad,
                                                        head_major, values=q)
     O = au.Operand(batch.rows, hq, pages.d, okind, pad, head_major)
     d = batch.dict(**kw)
+    if ROOMY and not kw:
+        widened(pages, batch, d)
     n = tsl.cache_attention_workspace_size(pages.dict, d, hq, window, sinks)
     ws = torch().full((n + 256,), 0xFF, dtype=torch().uint8, device=DEV) if n else None
     tsl.cache_attention(pages.dict, d, hq, Q.view, Q.ld, Q.head, scale, window, sinks, au.DT[okind],
@@ -131,10 +148,11 @@ LONG = [
     (128, 8, 2, 128, [200, 31], [600, 31], 64, 5, "bf16", 0, False),
     (64, 2, 2, 64, [500], [500], 7, 130, "f32", 0, False),
     (128, 7, 1, 256, [100], [1500], 0, 0, "bf16", 0, False),
-    # four tiles of 128 rows and more: records expanded once for all
+    # several tiles of 128 rows, the records expanded for each or once for all
     (128, 8, 2, 64, [130], [130], 0, 0, "f32", 0, False),
     (128, 28, 4, 64, [100, 3, 70, 60], [400, 50, 60, 60], 0, 0, "bf16", 0, False),
-    (64, 32, 8, 32, [400], [1000], 100, 5, "f32", 1, False),
+    (64, 32, 8, 32, [600], [1000], 100, 5, "f32", 1, False),
+    (128, 64, 4, 64, [300, 2, 50], [900, 40, 300], 130, 40, "bf16", 0, False),
     (64, 8, 1, 32, [70, 55], [3000, 900], 0, 0, "bf16", 0, True),
     (128, 4, 4, 128, [700, 40, 390], [700, 300, 391], 0, 0, "f32", 0, False),
     (64, 4, 4, 64, [513], [600], 33, 200, "bf16", 0, False),
@@ -301,7 +319,7 @@ def test_large_magnitudes():
 def test_prompts_longer_than_they_were_said_to_be(hint):
     """Records are expanded once for the sequences that the workspace has room
     for, and per tile for the others: the results are right either way."""
-    d, hq, hkv, page = 128, 8, 2, 64
+    d, hq, hkv, page = 64, 64, 8, 64
     b = au.Batch([200, 150, 1, 120], [250, 610, 70, 130], page)
     pages = au.Pages(b.n_pages, page, hkv, d)
     K, V, q = data(b, hkv, d, hq, 71)
@@ -427,6 +445,8 @@ def test_two_calls_at_once():
     kinds = ((1, 0, 0), (-0.5, 100, 4))
     alone = [run(pages, b, hq, q * f, d ** -0.5, w, s, "f32") for f, w, s in kinds]
     seqs, calls = b.dict(), []
+    if ROOMY:
+        widened(pages, b, seqs)
     for k in range(8):
         f, w, s = kinds[k % 2]
         n = tsl.cache_attention_workspace_size(pages.dict, seqs, hq, w, s)
