@@ -194,7 +194,7 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  *   workspace: 256-byte aligned, cache_attention_workspace_size() bytes; may
  *      be null when that is 0.  Calls that overlap in time need one each.
  * Products accumulate in binary32, the softmax is binary32.  For sequences of
- * up to 48 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
+ * up to 64 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
  * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
  * exactly up to binary32 rounding; for longer ones rounded to 11 bits
  * (binary16), as the probabilities are, scaled by a power of two that up to 128

@@ -208,10 +208,10 @@ struct AttendPlan {
 
 // Query rows of a sequence and K/V head up to which the kernel of few rows takes
 // it, where every tile of 16 expands the records it reads anew.  Of one sequence
-// of 4000 tokens, heads of 128, 32 rows took 21 us with it and 20 with the other,
-// 64 25 and 22, 128 32 and 25; of 16000 tokens 64 33 and 35, 96 41 and 37; of 16
-// sequences of 4000 64 69 and 65, 128 117 and 75.
-constexpr int64_t kFewRows = 48;
+// of 4000 tokens, heads of 128, 48 rows took 22.7 us with it and 24.2 with the
+// other, 64 24.7 and 25.2, 128 32 and 26; of 16000 tokens 64 33 and 40, 96 41 and
+// 38; of 16 sequences of 4000 48 56 and 65, 64 69 and 66, 128 118 and 72.
+constexpr int64_t kFewRows = 64;
 constexpr int64_t kCUs = 256;
 // Records that a wave takes alone, with no join after it: 4 and 8 of them took
 // 9.0 and 12.7 us so, 10.4 and 10.6 divided.

@@ -21,7 +21,7 @@ from tensor_sharded_linear_plan_amd import binding as tsl
 pytestmark = pytest.mark.gpu
 
 W16 = 2.0 ** -11
-FEW = 48
+FEW = 64
 
 
 @pytest.fixture(params=[False, True], ids=["", "roomy"], autouse=True)
