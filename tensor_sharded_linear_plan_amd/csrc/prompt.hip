@@ -712,7 +712,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
 // One wave expands one record that some row of its sequence sees: K as the
 // operands of its first product, ST pieces of 1 KB in the order in which a wave
 // reads them (lane 32 h + c holds 8 columns of token c), then V as those of the
-// second (column c, 8 tokens), in binary16 by exponents of the record's own.
+// second (column c, 8 tokens), in binary16 by exponents of the record's own (16500
+// tokens of 4 heads of 128: 9.6 us for 33 MB, mostly latency).
 template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(AttendArgs a) {
     constexpr int G = D / 64, W = D / 32;
     const int lane = threadIdx.x & 63;

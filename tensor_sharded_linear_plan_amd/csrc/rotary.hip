@@ -2,7 +2,8 @@
 // and attention): columns (x1, x2) of pair p turn by t = position freq[p],
 //     y1 = x1 cos t - x2 sin t,   y2 = x2 cos t + x1 sin t;
 // the backward pass is the turn by -t.  Bound by the bytes of one pass, each
-// value read once and written once.  A workgroup takes a few token rows: its
+// value read once and written once (8192 rows of 72 heads of 128, out of memory:
+// 65.5 us, 4.6 TB/s).  A workgroup takes a few token rows: its
 // threads form the rows' cosines and sines once, into LDS, and every head of
 // every item reads them from there.
 //
@@ -154,9 +155,16 @@ __global__ void __launch_bounds__(kThreads) rotate_any_kernel(RotateArgs a, int 
 
 hipError_t launch_rotate(const RotateArgs &a, hipStream_t stream) {
     const int half = a.rot_dim / 2;
+    // rows of a workgroup: 8192 rows of 72 heads of 128 take 54.6 us with 4 (in
+    // cache; 57.5 with 2, 61.6 with 1, 80.7 with 8), but fewer rows than make 512
+    // workgroups are spread thinner (1531 of 40 heads of 64 in binary32: 8.2 us with
+    // 2, 8.9 with 4)
     int tokens = kTableMax / half;
     tokens = tokens < 1 ? 1 : (tokens > 4 ? 4 : tokens);
-    // few rows: the heads are divided over workgroups too, whose tables repeat
+    while (tokens > 1 && (a.M + tokens - 1) / tokens < 512)
+        tokens /= 2;
+    // and with fewer yet the heads are divided over workgroups too, whose tables
+    // repeat (16 to 250 rows of 32 heads 7.4 us, undivided 8.0)
     const int64_t groups = (a.M + tokens - 1) / tokens;
     int parts = (int)(512 / groups);
     parts = parts < 1 ? 1 : (parts > (a.heads + 3) / 4 ? (a.heads + 3) / 4 : parts);
