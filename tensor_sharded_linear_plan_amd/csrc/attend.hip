@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
     SeqRows q;
     if (MANY) {
         PromptTile at;
-        const int me = blockIdx.x * RPW + (WPR == 1 ? wave : 0);
+        const int me = blockIdx.x; // (WPR 16)
         if (!prompt_tile(a, me / kPromptRows, false, at) || at.splits == 1)
             return; // (its workgroup has written the result)
         s = at.s, head = at.head, tile = at.tile, q = at.q;

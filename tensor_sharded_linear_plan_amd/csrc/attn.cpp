@@ -229,6 +229,27 @@ constexpr int kAttendShare = 1, kPromptShare = 8;
 constexpr int64_t kImageWork = 2048;
 constexpr int64_t kImageBytes = int64_t(1) << 30;
 
+// The plan of the images: for as many sequences as there is room for.
+void plan_images(const tsl_cache &c, const tsl_seqs &q, int64_t group, int32_t window, int32_t sinks,
+                 bool few, AttendPlan *p) {
+    p->images = p->image_seqs = 0;
+    p->image_bytes = 0;
+    const int64_t n =
+        most_records(std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens),
+                     std::min<int64_t>(q.max_rows, q.rows), window, sinks);
+    if (few || p->tiles <= 2 || n == 0)
+        return;
+    // (of sequences with more rows than the other kernel's, one has max_rows)
+    const int64_t others = std::max<int64_t>(0, q.rows * group - p->rows) / (kFewRows + 1);
+    const int64_t one = n * c.n_kv_heads, image = 128 * c.head_dim;
+    const int64_t seqs = std::min({(int64_t)q.n_seqs, 1 + others, kImageBytes / (one * image)});
+    if (seqs * one * (p->tiles - 2) < kImageWork)
+        return;
+    p->images = (int32_t)n;
+    p->image_seqs = (int32_t)seqs;
+    p->image_bytes = round_up((size_t)(one * seqs * image), 256) + round_up((size_t)(one * seqs) * 4, 256);
+}
+
 tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int64_t rows, bool few,
                        int tile_rows, int32_t window, int32_t sinks, AttendPlan *p) {
     p->rows = (int32_t)rows;
@@ -270,23 +291,7 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
     if (p->parts > kMaxBlocks ||
         (p->ranges && (few ? (int64_t)q.n_seqs * c.n_kv_heads * rows : p->units * tile_rows) > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
-    // with several tiles a sequence's records may be expanded once for all of them,
-    // for as many sequences as there is room for
-    p->images = p->image_seqs = 0;
-    p->image_bytes = 0;
-    if (!few && p->tiles > 2) {
-        int64_t n = most_records(std::min<int64_t>(q.max_context, (int64_t)q.max_pages * c.page_tokens),
-                                 std::min<int64_t>(q.max_rows, q.rows), window, sinks);
-        // (of sequences with more rows than the other kernel's, one has max_rows)
-        const int64_t prompts = std::min<int64_t>(q.n_seqs, 1 + std::max<int64_t>(0, q.rows * group - rows) / (kFewRows + 1));
-        const int64_t of_one = std::max<int64_t>(n, 1) * c.n_kv_heads, fit = kImageBytes / (of_one * 128 * c.head_dim);
-        if (n > 0 && fit > 0 && of_one * std::min(prompts, fit) >= (kImageWork + p->tiles - 3) / (p->tiles - 2)) {
-            p->images = (int32_t)n;
-            p->image_seqs = (int32_t)std::min(prompts, fit);
-            p->image_bytes = round_up((size_t)(of_one * p->image_seqs) * 128 * c.head_dim, 256) +
-                             round_up((size_t)(of_one * p->image_seqs) * 4, 256);
-        }
-    }
+    plan_images(c, q, group, window, sinks, few, p);
     p->bytes = p->image_bytes + round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +
                             (p->shared ? (size_t)p->units * 8 : 0),
                         256);
@@ -526,7 +531,8 @@ extern "C" tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *se
             a.by_images = make_div((uint32_t)k.images);
             a.images = ws;
             a.image_info = reinterpret_cast<uint32_t *>(
-                ws + round_up((size_t)k.images * k.image_seqs * cache->n_kv_heads * 128 * cache->head_dim, 256));
+                ws + k.image_bytes -
+                round_up((size_t)k.images * k.image_seqs * cache->n_kv_heads * 4, 256));
         }
         if (k.ranges) {
             char *const at = ws + k.image_bytes;

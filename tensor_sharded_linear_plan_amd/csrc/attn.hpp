@@ -113,7 +113,6 @@ struct AttendArgs {
     Div by_rows, by_tile_rows;
 };
 
-constexpr int kMaxSplits = 1024;
 constexpr int kMaxShared = 1024; // sequences of a shared call
 constexpr int kJoinWave = 16;  // ranges that one wave adds; 16 waves more
 constexpr int kJoinLanes = 64; // ... that the lanes of a row add, with many rows

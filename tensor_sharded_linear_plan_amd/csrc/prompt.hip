@@ -578,98 +578,98 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
 
     // ---- the walk over codes ----
     if (!laid_out) {
-    uint64_t there = 0, there1 = 0, clear = 0, clear1 = 0; // of this step, the next
-    int ek = 0, ek1 = 0, ev1 = 0, top = 0, page = -1;
-    bool bad = false, bad1 = false, full1 = false;
-    f32x16 x[2];
-    if (steps > 0) {
-        bool full;
-        const int page0 = page_of(0), page1 = page_of(1);
-        page = page_of(2);
-        fetch(0, page0, there);
-        seen_by(0, there, clear, full);
-        exponents(0, full, ek, ev, bad);
-        top = ev = (ev + 7) & ~7;
-        expand_k(0, full, ek, lds);
-        expand_v(0, full && !bad, ev, lds + 2 * BUF);
-        fetch(1, page1, there1);
-        __syncthreads();
+        uint64_t there = 0, there1 = 0, clear = 0, clear1 = 0; // of this step, the next
+        int ek = 0, ek1 = 0, ev1 = 0, top = 0, page = -1;
+        bool bad = false, bad1 = false, full1 = false;
+        f32x16 x[2];
+        if (steps > 0) {
+            bool full;
+            const int page0 = page_of(0), page1 = page_of(1);
+            page = page_of(2);
+            fetch(0, page0, there);
+            seen_by(0, there, clear, full);
+            exponents(0, full, ek, ev, bad);
+            top = ev = (ev + 7) & ~7;
+            expand_k(0, full, ek, lds);
+            expand_v(0, full && !bad, ev, lds + 2 * BUF);
+            fetch(1, page1, there1);
+            __syncthreads();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            f16x8 k[HS];
-            read_k(lds, 0, half, k);
-            logits(k, half, x[0]);
-        }
-        mask(0, 0, there, clear, x[0]);
-    }
-    for (int step = 0; step < steps; ++step) {
-        char *kb = lds + (step & 1) * BUF, *vbuf = lds + (2 + (step & 1)) * BUF;
-        char *kb1 = lds + (~step & 1) * BUF, *vb1 = lds + (2 + (~step & 1)) * BUF;
-        // not 0: it meets infinities
-        const float f = fmaxf(ldexpf(fabsf(a.scale), qe + ek), 1.17549435e-38f);
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            f32x16 &now = x[t & 1], &then = x[~t & 1];
-            const char *kn = t + 1 < TB ? kb : kb1;
-            const int tn = (t + 1) % TB;
-            f16x8 k0[HS], k1[HS], v0[DT], v1[DT], p[2];
-            read_k(kn, tn, 0, k0);
-            fence();
-            float sum = probabilities(now, f, p);
-            if (__any(!(sum < kProbMost))) {
-                raise(now, f);
-                sum = probabilities(now, f, p);
+            for (int half = 0; half < 2; ++half) {
+                f16x8 k[HS];
+                read_k(lds, 0, half, k);
+                logits(k, half, x[0]);
             }
-            l += sum;
-            read_k(kn, tn, 1, k1);
-            fence();
-            logits(k0, 0, then);
-            read_v(vbuf, t, 0, v0);
-            fence();
-            logits(k1, 1, then);
-            read_v(vbuf, t, 1, v1);
-            fence();
+            mask(0, 0, there, clear, x[0]);
+        }
+        for (int step = 0; step < steps; ++step) {
+            char *kb = lds + (step & 1) * BUF, *vbuf = lds + (2 + (step & 1)) * BUF;
+            char *kb1 = lds + (~step & 1) * BUF, *vb1 = lds + (2 + (~step & 1)) * BUF;
+            // not 0: it meets infinities
+            const float f = fmaxf(ldexpf(fabsf(a.scale), qe + ek), 1.17549435e-38f);
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                o[d] = mfma32(v0[d], p[0], o[d]);
+            for (int t = 0; t < TB; ++t) {
+                f32x16 &now = x[t & 1], &then = x[~t & 1];
+                const char *kn = t + 1 < TB ? kb : kb1;
+                const int tn = (t + 1) % TB;
+                f16x8 k0[HS], k1[HS], v0[DT], v1[DT], p[2];
+                read_k(kn, tn, 0, k0);
+                fence();
+                float sum = probabilities(now, f, p);
+                if (__any(!(sum < kProbMost))) {
+                    raise(now, f);
+                    sum = probabilities(now, f, p);
+                }
+                l += sum;
+                read_k(kn, tn, 1, k1);
+                fence();
+                logits(k0, 0, then);
+                read_v(vbuf, t, 0, v0);
+                fence();
+                logits(k1, 1, then);
+                read_v(vbuf, t, 1, v1);
+                fence();
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                o[d] = mfma32(v1[d], p[1], o[d]);
-            if (t == TB - 2) {
-                seen_by(step + 1, there1, clear1, full1);
-                exponents(step + 1, full1, ek1, ev1, bad1);
-                ev1 = (ev1 + 7) & ~7;
-                top = top > ev1 ? top : ev1;
-                ev1 = ev1 > top - 64 ? ev1 : top - 64;
-                expand_k(step + 1, full1, ek1, kb1);
-                __syncthreads();
-            } else if (t == TB - 1) {
-                expand_v(step + 1, full1 && !bad1, ev1, vb1);
-                __syncthreads();
+                for (int d = 0; d < DT; ++d)
+                    o[d] = mfma32(v0[d], p[0], o[d]);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = mfma32(v1[d], p[1], o[d]);
+                if (t == TB - 2) {
+                    seen_by(step + 1, there1, clear1, full1);
+                    exponents(step + 1, full1, ek1, ev1, bad1);
+                    ev1 = (ev1 + 7) & ~7;
+                    top = top > ev1 ? top : ev1;
+                    ev1 = ev1 > top - 64 ? ev1 : top - 64;
+                    expand_k(step + 1, full1, ek1, kb1);
+                    __syncthreads();
+                } else if (t == TB - 1) {
+                    expand_v(step + 1, full1 && !bad1, ev1, vb1);
+                    __syncthreads();
+                }
+                if (t + 1 < TB)
+                    mask(step, t + 1, there, clear, then);
+                else
+                    mask(step + 1, 0, there1, clear1, then);
             }
-            if (t + 1 < TB)
-                mask(step, t + 1, there, clear, then);
-            else
-                mask(step + 1, 0, there1, clear1, then);
-        }
-        if (bad && !idle)
-            for (int t = 0; t < TB; ++t)
-                if (bit(there, t))
-                    find_taint(block_at(step, t));
-        if (ev1 != ev) {
-            const float g = ldexpf(1.f, ev - ev1);
+            if (bad && !idle)
+                for (int t = 0; t < TB; ++t)
+                    if (bit(there, t))
+                        find_taint(block_at(step, t));
+            if (ev1 != ev) {
+                const float g = ldexpf(1.f, ev - ev1);
 #pragma unroll
-            for (int t = 0; t < DT; ++t)
-                o[t] *= g;
+                for (int t = 0; t < DT; ++t)
+                    o[t] *= g;
+            }
+            ek = ek1;
+            ev = ev1;
+            bad = bad1;
+            there = there1;
+            clear = clear1;
+            fetch(step + 2, page, there1);
+            page = page_of(step + 3);
         }
-        ek = ek1;
-        ev = ev1;
-        bad = bad1;
-        there = there1;
-        clear = clear1;
-        fetch(step + 2, page, there1);
-        page = page_of(step + 3);
-    }
     }
 
     l += __shfl_xor(l, 32, 64);
