@@ -196,7 +196,9 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * Products accumulate in binary32, the softmax is binary32.  For sequences of
  * up to 64 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
  * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
- * exactly up to binary32 rounding; for longer ones rounded to 11 bits
+ * exactly and a probability times a value's scale with 16 bits (the mean of any
+ * number of independent values is within 2^-14 of its own size, in the 2-norm);
+ * for longer ones rounded to 11 bits
  * (binary16), as the probabilities are, scaled by a power of two that up to 128
  * neighbouring tokens which some row of the sequence sees have in common: values
  * below 2^-22 of the largest of those lose bits.  Both kinds may be in one call
