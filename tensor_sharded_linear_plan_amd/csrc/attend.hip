@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(64 * kWaves, attend_groups(D)) attend_decode_k
         l += __shfl_xor(l, 32, 64);
         l = over_groups<P>(l * f, sum);
         const float inv = !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-        const int64_t slot = (int64_t)(me + unit) * ROWS + c;
+        const int64_t slot = (int64_t)(begin == 0 ? a.parts + me : me) * ROWS + c;
         const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head + 4 * g;
         const bool mine = live && !own;
         if (!complete && mine && g == 0) {
@@ -507,20 +507,19 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
         used = view.used;
         slot0 = (int64_t)at.unit * at.splits;
     } else {
-        const int b = quotient(blockIdx.x * RPW, a.by_rows);
-        rho = blockIdx.x * RPW - b * a.rows_up + (WPR == 1 ? wave : 0);
+        s = blockIdx.z, head = blockIdx.y;
+        rho = blockIdx.x * RPW + (WPR == 1 ? wave : 0);
         if (rho >= a.rows)
             return;
         tile = quotient(rho, a.by_tile_rows);
-        const int unit = b * a.tiles + tile;
-        s = quotient(b, a.by_heads), head = b - s * a.c.n_kv_heads;
+        const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
         const int from = a.spans[2 * unit], last = a.spans[2 * unit + 1];
         q = seq_rows(a.c, s);
         const int rows = rows_of(a, q);
         if (rho >= rows)
             return;
         // the waves that shared it (one that had all of it has written the result)
-        slot0 = from + unit;
+        slot0 = from;
         used = last - from + 1;
         if (view_of(a, q, tile, tile_rows, rows - tile * tile_rows).count == 0)
             used = 0;
@@ -547,7 +546,8 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) attend_join_kernel(
             float to = top;
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                const int k = k0 + i * stride * AT_ONCE, at = k < used ? k : 0;
+                const int k = k0 + i * stride * AT_ONCE, of = k < used ? k : 0;
+                const int at = !MANY && pass == 0 && of == 0 ? a.parts : of; // (attn.hpp, `part`)
                 const f32x4 *p = reinterpret_cast<const f32x4 *>(part + at * step * D) + lane % LPR * 2;
                 f[i] = ml[at * step];
                 w[i][0] = p[0];
@@ -690,17 +690,14 @@ template <int D, int P> hipError_t decode(const AttendArgs &a, hipStream_t strea
 }
 
 template <int D> hipError_t join(int tile_rows, AttendArgs a, hipStream_t stream) {
-    const int64_t rows = a.rows, units = (int64_t)a.c.n_seqs * a.c.n_kv_heads;
-    const bool many = a.parts / (units * a.tiles) > kJoinWave;
-    a.rows_up = (int32_t)(many ? rows : (rows + 3) / 4 * 4);
-    a.by_rows = make_div((uint32_t)a.rows_up);
+    const bool many = a.parts / a.units > kJoinWave;
+    const unsigned rows = (unsigned)(many ? a.rows : (a.rows + 3) / 4);
+    const dim3 grid(rows, (unsigned)a.c.n_kv_heads, (unsigned)a.c.n_seqs);
     a.by_tile_rows = make_div((uint32_t)tile_rows);
     if (many)
-        hipLaunchKernelGGL((attend_join_kernel<D, 16, false>), dim3((unsigned)(units * rows)), dim3(1024), 0,
-                           stream, a, tile_rows);
+        hipLaunchKernelGGL((attend_join_kernel<D, 16, false>), grid, dim3(1024), 0, stream, a, tile_rows);
     else
-        hipLaunchKernelGGL((attend_join_kernel<D, 1, false>), dim3((unsigned)(units * (a.rows_up / 4))),
-                           dim3(256), 0, stream, a, tile_rows);
+        hipLaunchKernelGGL((attend_join_kernel<D, 1, false>), grid, dim3(256), 0, stream, a, tile_rows);
     return hipGetLastError();
 }
 

@@ -213,6 +213,7 @@ struct AttendPlan {
 // 38; of 16 sequences of 4000 48 56 and 65, 64 69 and 66, 128 118 and 72.
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kCUs = 256;
+constexpr int64_t kMaxWaves = 4 * kMaxBlocks; // of the kernel of few rows
 // Records that a wave takes alone, with no join after it: 4 and 8 of them took
 // 9.0 and 12.7 us so, 10.4 and 10.6 divided.
 constexpr int kWholeRecords = 6;
@@ -269,7 +270,7 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
     const int64_t most = std::max<int64_t>(1, (records + p->min_share - 1) / p->min_share);
     p->shared = 0;
     p->splits = 1;
-    p->parts = (int32_t)std::min<int64_t>(p->units, kMaxBlocks + 1);
+    p->parts = (int32_t)std::min<int64_t>(p->units, kMaxWaves + 1);
     p->ranges = 0;
     // (a call of more sequences than that has several tiles for every wave as it
     // is; records are counted in 32 bits)
@@ -278,7 +279,7 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
         p->shared = 1;
         const int64_t places = kCUs * 4 * attend_groups(c.head_dim); // waves that fit
         p->parts = (int32_t)std::min(places, p->units * most);
-        p->ranges = p->parts + p->units;
+        p->ranges = 2 * p->parts;
     }
     if (!few) {
         // one sequence has max_rows; how many ranges there are is for the kernel to say
@@ -288,8 +289,10 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
             p->ranges = std::max(p->units, std::min<int64_t>(kPromptPlaces, p->units * p->splits));
         p->parts = (int32_t)std::min<int64_t>(std::max(p->units, p->ranges), kMaxBlocks + 1);
     }
-    if (p->parts > kMaxBlocks ||
-        (p->ranges && (few ? (int64_t)q.n_seqs * c.n_kv_heads * rows : p->units * tile_rows) > kMaxBlocks))
+    // workgroups of a launch: four waves with few rows, and four rows of the join's
+    // (whose other dimensions are heads and sequences)
+    if (few ? p->parts > kMaxWaves || (p->ranges && rows > kMaxBlocks)
+            : p->parts > kMaxBlocks || (p->ranges && p->units * tile_rows > kMaxBlocks))
         return TSL_ERR_UNSUPPORTED;
     plan_images(c, q, group, window, sinks, few, p);
     p->bytes = p->image_bytes + round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +

@@ -98,10 +98,11 @@ struct AttendArgs {
     int32_t units;     // sequences * heads * tiles; many rows: heads * tiles, at most
     int32_t min_share; // records of a range or part at least
     // sums of ranges: [range][tile rows][head_dim], and of each row its reference
-    // exponent and sum; few rows: range = unit + wave, with unit = (sequence *
-    // heads + head) * tiles + tile; many: range = workgroup
+    // exponent and sum.  Many rows: range = workgroup.  Few: a wave has sums of its
+    // own of two tiles at most, the one that it goes on with (range = wave) and the
+    // one that it begins and does not end (parts + wave)
     float *part, *part_ml;
-    int32_t *spans; // shared: the first and last wave of each unit
+    int32_t *spans; // shared: the first and last wave of each unit, (sequence * heads + head) * tiles + tile
     // many rows, where records are expanded once for the call: of image_seqs
     // sequences and each head up to image_records images of 128 head_dim bytes
     // (0: none), and of each its exponents and flags
@@ -109,8 +110,7 @@ struct AttendArgs {
     uint32_t *image_info;
     int32_t image_records, image_seqs;
     Div by_images;
-    int32_t rows_up; // the join: a unit's rows, rounded up to a workgroup's
-    Div by_rows, by_tile_rows;
+    Div by_tile_rows; // the join
 };
 
 constexpr int kMaxShared = 1024; // sequences of a shared call

@@ -1,0 +1,34 @@
+"""cache_attention at sizes whose products are large though their sums are not.
+Tolerances are those of test_gpu_attend."""
+import pytest
+
+import attn_util as au
+import test_gpu_attend as ta
+
+pytestmark = pytest.mark.gpu
+
+
+def call(monkeypatch, b, hq, hkv, d, window=0, sinks=0, kind="f32", page=32, seed=0, rounded=False, **kw):
+    monkeypatch.setattr(ta, "ROOMY", False, raising=False)
+    pages = au.Pages(b.n_pages, page, hkv, d)
+    K, V, q = ta.data(b, hkv, d, hq, seed)
+    au.fill(pages, b, K, V)
+    Q, O = ta.run(pages, b, hq, q, d ** -0.5, window, sinks, kind, **kw)
+    ta.check(O, Q, b, K, V, hq, d ** -0.5, window, sinks, kind, rounded)
+
+
+def test_a_prompt_of_heads_of_256_beside_hundreds_of_tokens(monkeypatch):
+    rows = [1] * 600
+    rows[411] = 1024
+    b = au.Batch(rows, [1024 if n > 1 else 20 + i % 90 for i, n in enumerate(rows)], 32, seed=2, lead=1, tail=2)
+    call(monkeypatch, b, 32, 4, 256, seed=21)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 40)])
+def test_tiles_over_several_waves_of_heads_of_256(monkeypatch, window, sinks):
+    """Prompts of lengths that leave tiles in every position of a wave's part: begun
+    and ended in it, begun, ended, and neither."""
+    b = au.Batch([1, 300, 17, 2, 90], [2500, 300, 900, 64, 1500], 32, seed=3, lead=2, tail=1)
+    call(monkeypatch, b, 6, 2, 256, window, sinks, seed=22)
+    b = au.Batch([1], [12000], 32, seed=4)  # one tile over all waves
+    call(monkeypatch, b, 2, 1, 256, window, sinks, seed=23)
