@@ -702,7 +702,8 @@ template <int D> hipError_t join(int tile_rows, AttendArgs a, hipStream_t stream
 }
 
 template <int D> hipError_t prompt_join(const AttendArgs &a, hipStream_t stream) {
-    const unsigned rows = (unsigned)a.units * kPromptRows;
+    // (tiles in two ranges or more)
+    const unsigned rows = (unsigned)(a.units < kPromptPlaces / 2 ? a.units : kPromptPlaces / 2) * kPromptRows;
     if (a.splits > kJoinLanes)
         hipLaunchKernelGGL((attend_join_kernel<D, 16, true>), dim3(rows), dim3(1024), 0, stream, a, kPromptRows);
     else

@@ -282,17 +282,18 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
         p->ranges = 2 * p->parts;
     }
     if (!few) {
-        // one sequence has max_rows; how many ranges there are is for the kernel to say
+        // one sequence has max_rows; how many ranges there are is for the kernel to say,
+        // which cuts tiles only while all their ranges fit the places
         p->splits = (int32_t)std::max<int64_t>(
             1, std::min(most, kPromptPlaces / std::max<int64_t>(1, (int64_t)p->tiles * c.n_kv_heads)));
         if (p->splits > 1)
-            p->ranges = std::max(p->units, std::min<int64_t>(kPromptPlaces, p->units * p->splits));
+            p->ranges = std::min<int64_t>(kPromptPlaces, p->units * p->splits);
         p->parts = (int32_t)std::min<int64_t>(std::max(p->units, p->ranges), kMaxBlocks + 1);
     }
     // workgroups of a launch: four waves with few rows, and four rows of the join's
     // (whose other dimensions are heads and sequences)
     if (few ? p->parts > kMaxWaves || (p->ranges && rows > kMaxBlocks)
-            : p->parts > kMaxBlocks || (p->ranges && p->units * tile_rows > kMaxBlocks))
+            : p->parts > kMaxBlocks)
         return TSL_ERR_UNSUPPORTED;
     plan_images(c, q, group, window, sinks, few, p);
     p->bytes = p->image_bytes + round_up((size_t)p->ranges * tile_rows * (size_t)(c.head_dim + 2) * 4 +

@@ -4,7 +4,8 @@ tile that there might be.
 
 Few query rows: a wave leaves at most two tiles' sums, and there are no more waves
 than the chip holds (8 a CU with heads of 128, 16 of 64, 4 of 256); a tile's are
-its rows, of head_dim + 2 values each; and 8 bytes name the waves of each tile."""
+its rows, of head_dim + 2 values each; and 8 bytes name the waves of each tile.  Many: tiles of 128 rows are
+cut into ranges of tokens only while there are no more than 512 of those."""
 import pytest
 
 WAVES = {64: 4096, 128: 2048, 256: 1024}
@@ -44,3 +45,13 @@ def test_one_long_prompt_of_heads_of_256_beside_many_tokens(tsl_lib):
     assert 0 < size(tsl_lib, 256, 32, 4, **kw) <= few_rows(256, 16, 600 * 4 * 512)
     # tiles of the kernel of few rows without partial sums: four a workgroup
     size(tsl_lib, 128, 64, 16, n_seqs=65535, rows=70000, max_rows=1024)
+
+
+@pytest.mark.parametrize("n,rows", [(256, 9), (1024, 9), (16000, 9), (2048, 128), (60000, 33), (65535, 64)])
+def test_many_sequences_of_many_rows(tsl_lib, n, rows):
+    """Up to the stated limits, and no more partial sums than can be; with three
+    tiles or more, 1 GiB of expanded records beside them."""
+    for d, hq, hkv in ((128, 64, 8), (64, 32, 8), (128, 28, 4)):
+        images = (1 << 30) + (1 << 21) if rows * hq // hkv > 256 else 0
+        most = 512 * 128 * (d + 2) * 4 + few_rows(d, 16, n * hkv * 16) + images
+        assert size(tsl_lib, d, hq, hkv, n_seqs=n, rows=min(n * rows, (1 << 22) - 1), max_rows=rows) <= most

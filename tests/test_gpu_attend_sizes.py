@@ -32,3 +32,22 @@ def test_tiles_over_several_waves_of_heads_of_256(monkeypatch, window, sinks):
     call(monkeypatch, b, 6, 2, 256, window, sinks, seed=22)
     b = au.Batch([1], [12000], 32, seed=4)  # one tile over all waves
     call(monkeypatch, b, 2, 1, 256, window, sinks, seed=23)
+
+
+def test_hundreds_of_sequences_of_a_few_more_rows_than_few(monkeypatch):
+    """72 query rows a K/V head each: more tiles than workgroups that run at once."""
+    r = au.rng(6)
+    ctx = [int(x) for x in r.integers(9, 400, 300)]
+    b = au.Batch([9] * 300, ctx, 32, seed=7, lead=1, tail=1)
+    call(monkeypatch, b, 16, 2, 128, seed=24, rounded=True)
+    # ... of which one alone has them, in ranges of tokens
+    rows = [1] * 400
+    rows[123] = 40
+    b = au.Batch(rows, [3000 if n > 1 else 50 for n in rows], 32, seed=8)
+    call(monkeypatch, b, 16, 2, 128, seed=25, rounded=True)
+
+
+def test_two_thousand_prompts(monkeypatch):
+    r = au.rng(9)
+    ctx = [128 + int(x) for x in r.integers(0, 40, 2048)]
+    call(monkeypatch, au.Batch([128] * 2048, ctx, 32, seed=10), 1, 1, 64, seed=26, rounded=True)
