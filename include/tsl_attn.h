@@ -201,7 +201,8 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * for longer ones rounded to 11 bits
  * (binary16), as the probabilities are, scaled by a power of two that up to 128
  * neighbouring tokens which some row of the sequence sees have in common: values
- * below 2^-22 of the largest of those lose bits.  Both kinds may be in one call
+ * below 2^-22 of the largest of those lose bits, and probabilities below 2^-23 of
+ * the row's largest so far (below 2^-31 they are 0).  Both kinds may be in one call
  * (generated tokens beside a prompt's chunk).  |Q| stays below 2^110, and scale
  * sum |q k| of a visible token within binary32's range (what other rows get does
  * not hang on a row that does not keep to it).  Equal calls give equal bits.  O

@@ -29,8 +29,9 @@
 // result's own rounding.  Its range is met with powers of two, as the 4-bit
 // GEMM's is: a row of Q by its largest element, the K and the V values of the
 // records in hand by a bound of theirs (15 |s| + |b|); the accumulators follow
-// V's, by multiples of 8 (few neighbours differ, and 22 octaves below the largest
-// value keep all bits), down to 2^-64 of the largest so far.
+// V's (images' by multiples of 2: fewer neighbours differ), down to 2^-64 of the
+// largest so far.  Values keep their 11 bits 22 octaves below the largest of a record,
+// or of a step's records.
 // Probabilities are 2^9 times their value relative to the running reference,
 // which moves only when a sum of 16 of them comes to 65000 (none is lost above
 // 2^-33 of the largest): the common step looks for no maximum.
@@ -49,16 +50,17 @@ constexpr int kWaves = 4; // a workgroup's; two share a CU
 constexpr int kRows = 32 * kWaves;
 static_assert(kRows == kPromptRows, "rows of a tile");
 
-// 4-bit word -> four pairs of binary16 codes (0 .. 15, exact): 1024 + c has c in
-// its low mantissa bits, 1024 + 16 c four bits up.
+// 4-bit word -> four pairs of binary16 sixteenths of codes (0 .. 15 / 16, exact): 64
+// + c / 16 has c in its low mantissa bits, 64 + c four bits up.  They meet 16 s, which
+// keeps its bits in binary16 four octaves further down than s.
 __device__ __forceinline__ void codes16(uint32_t w, f16x2 (&c)[4]) {
     uint32_t lo, hi, o;
     asm("v_mov_b32 %0, 0x000f000f" : "=v"(lo));
     asm("v_mov_b32 %0, 0x00f000f0" : "=v"(hi));
-    asm("s_mov_b32 %0, 0x64006400" : "=s"(o));
+    asm("s_mov_b32 %0, 0x54005400" : "=s"(o));
     const uint32_t w8 = w >> 8;
-    const f16x2 base = {(_Float16)-1024.f, (_Float16)-1024.f};
-    const f16x2 base16 = {(_Float16)-64.f, (_Float16)-64.f};
+    const f16x2 base = {(_Float16)-64.f, (_Float16)-64.f};
+    const f16x2 base16 = {(_Float16)-4.f, (_Float16)-4.f};
     const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     c[0] = __builtin_bit_cast(f16x2, (w & lo) | o) + base;
     c[1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w & hi) | o), sixteenth, base16);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 sw = ok ? sw : 0u;
                 bw = ok ? bw : 0u;
             }
-            const _Float16 x = (_Float16)ldexpf(bf16_lo(sw), -ek), y = (_Float16)ldexpf(bf16_lo(bw), -ek);
+            const _Float16 x = (_Float16)ldexpf(bf16_lo(sw), 4 - ek), y = (_Float16)ldexpf(bf16_lo(bw), -ek);
             sk[d] = f16x2{x, x};
             bk[d] = f16x2{y, y};
         }
@@ -343,11 +345,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             drop_where(bw, out);
         }
         f16x2 sv[4], bv[4];
-        auto scaled = [&](float x) { return (_Float16)ldexpf(x, -ev); };
+        auto scaled = [&](float x, int e) { return (_Float16)ldexpf(x, e); };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sv[j] = f16x2{scaled(bf16_lo(sw[j])), scaled(bf16_hi(sw[j]))};
-            bv[j] = f16x2{scaled(bf16_lo(bw[j])), scaled(bf16_hi(bw[j]))};
+            sv[j] = f16x2{scaled(bf16_lo(sw[j]), 4 - ev), scaled(bf16_hi(sw[j]), 4 - ev)};
+            bv[j] = f16x2{scaled(bf16_lo(bw[j]), -ev), scaled(bf16_hi(bw[j]), -ev)};
         }
         const int g = lane >> 4; // tokens 4 g ..: operand half h = g % 2, place g / 2
 #pragma unroll
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             fetch(0, page0, there);
             seen_by(0, there, clear, full);
             exponents(0, full, ek, ev, bad);
-            top = ev = (ev + 7) & ~7;
+            top = ev;
             expand_k(0, full, ek, lds);
             expand_v(0, full && !bad, ev, lds + 2 * BUF);
             fetch(1, page1, there1);
@@ -638,7 +640,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 if (t == TB - 2) {
                     seen_by(step + 1, there1, clear1, full1);
                     exponents(step + 1, full1, ek1, ev1, bad1);
-                    ev1 = (ev1 + 7) & ~7;
                     top = top > ev1 ? top : ev1;
                     ev1 = ev1 > top - 64 ? ev1 : top - 64;
                     expand_k(step + 1, full1, ek1, kb1);
@@ -770,7 +771,7 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
     int ek, ev;
     bool bad;
     bounds(kx, vx, lane, ek, ev, bad);
-    ev = (ev + 7) & ~7;
+    ev = (ev + 1) & ~1; // (neighbours differ less often)
     if (lane == 0)
         a.image_info[at] = (uint32_t)(ek + 256) | (uint32_t)(ev + 256) << 10 | (uint32_t)bad << 20 | 1u << 21;
 #pragma unroll
@@ -781,7 +782,7 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
             const int at16 = pc * 4 + n, u = at16 / W, ww = at16 % W, tok = 16 * u + tk;
             const bool ok = full || any_sees(a, all, blk * kBlock + tok);
             const uint32_t sw = ok ? ks[ww / 2][u][0] : 0u, bw = ok ? ks[ww / 2][u][1] : 0u;
-            const _Float16 x = (_Float16)ldexpf(bf16_lo(sw), -ek), y = (_Float16)ldexpf(bf16_lo(bw), -ek);
+            const _Float16 x = (_Float16)ldexpf(bf16_lo(sw), 4 - ek), y = (_Float16)ldexpf(bf16_lo(bw), -ek);
             f16x2 cd[4];
             codes16(kraw[pc][n], cd);
             u32x4 out;
@@ -805,11 +806,11 @@ template <int D> __global__ void __launch_bounds__(256) attend_images_kernel(Att
             drop_where(bw, out);
         }
         f16x2 sv[4], bv[4];
-        auto scaled = [&](float v) { return (_Float16)ldexpf(v, -ev); };
+        auto scaled = [&](float v, int e) { return (_Float16)ldexpf(v, e); };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sv[j] = f16x2{scaled(bf16_lo(sw[j])), scaled(bf16_hi(sw[j]))};
-            bv[j] = f16x2{scaled(bf16_lo(bw[j])), scaled(bf16_hi(bw[j]))};
+            sv[j] = f16x2{scaled(bf16_lo(sw[j]), 4 - ev), scaled(bf16_hi(sw[j]), 4 - ev)};
+            bv[j] = f16x2{scaled(bf16_lo(bw[j]), -ev), scaled(bf16_hi(bw[j]), -ev)};
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
