@@ -198,16 +198,17 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
  * exactly and a probability times a value's scale with 16 bits (the mean of any
  * number of independent values is within 2^-14 of its own size, in the 2-norm);
- * for longer ones rounded to 11 bits
- * (binary16), as the probabilities are, scaled by a power of two that up to 128
- * neighbouring tokens which some row of the sequence sees have in common: values
- * below 2^-22 of the largest of those lose bits, and probabilities below 2^-23 of
- * the row's largest so far (below 2^-31 they are 0).  Both kinds may be in one call
- * (generated tokens beside a prompt's chunk).  |Q| stays below 2^110, and scale
- * sum |q k| of a visible token within binary32's range (what other rows get does
- * not hang on a row that does not keep to it).  Equal calls give equal bits.  O
- * shares no byte with Q, the cache or the workspace.  scale log2(e) is finite,
- * window and sinks 0 .. 2^30.
+ * for longer ones rounded to 11 bits (binary16), as the probabilities are, scaled
+ * by a power of two that up to 128 neighbouring tokens which some row of the
+ * sequence sees have in common: values below 2^-22 of the largest of those lose
+ * bits, as do values below 2^-90 of an earlier one that the row gave weight to;
+ * probabilities below 2^-23 of the row's largest so far lose bits, and below
+ * 2^-31 they are 0.  Both kinds may be in one call (generated tokens beside a
+ * prompt's chunk).  |Q| stays below 2^110, scale sum |q k| of a visible token
+ * within binary32's range, and sum |v| over a row's tokens below 2^110 (what other
+ * rows get does not hang on a row that does not keep to it).  Equal calls give
+ * equal bits.  O shares no byte with Q, the cache or the workspace.  scale log2(e)
+ * is finite, window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
  * n_kv_heads), TSL_ERR_UNSUPPORTED, TSL_ERR_BUFFER_TOO_SMALL,
  * TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides whole 16 bytes),

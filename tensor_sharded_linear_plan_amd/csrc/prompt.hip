@@ -29,9 +29,11 @@
 // result's own rounding.  Its range is met with powers of two, as the 4-bit
 // GEMM's is: a row of Q by its largest element, the K and the V values of the
 // records in hand by a bound of theirs (15 |s| + |b|); the accumulators follow
-// V's (images' by multiples of 2: fewer neighbours differ), down to 2^-64 of the
-// largest so far.  Values keep their 11 bits 22 octaves below the largest of a record,
-// or of a step's records.
+// V's, each row's as far down as what it holds allows (2^-90 of a value that it
+// gave weight to); what is left between them the probabilities take.  Few neighbours
+// differ: images have even exponents, and one step below is left to the
+// probabilities.  Values keep their 11 bits 22 octaves below the largest of a
+// record, or of a step's records.
 // Probabilities are 2^9 times their value relative to the running reference,
 // which moves only when a sum of 16 of them comes to 65000 (none is lost above
 // 2^-33 of the largest): the common step looks for no maximum.
@@ -446,7 +448,35 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 taint |= 1u << g;
         }
     };
-    int ev = 0; // the accumulators' exponent
+    int ev = 0; // the row's accumulators' exponent
+    // ... becomes that of a record's values, or as near as leaves what is there below
+    // 2^100 (a row may hold larger values, or have passed over them without weight:
+    // behind the reference's moves); the probabilities take what is left between the two
+    auto follow = [&](int to) {
+        float big = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                big = fmaxf(big, fabsf(o[d][r]));
+        big = fmaxf(big, __shfl_xor(big, 32, 64));
+        const int low = ev + __builtin_amdgcn_frexp_expf(big) - 100;
+        to = to > low || big == 0.f ? to : low;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                o[d][r] = ldexpf(o[d][r], ev - to);
+        ev = to;
+    };
+    auto meet = [&](int e, f16x8 (&p)[2]) {
+        rare();
+        if (__any(e > ev || e < ev - 2))
+            follow(e);
+        const _Float16 g = (_Float16)ldexpf(1.f, e - ev);
+        p[0] *= g;
+        p[1] *= g;
+    };
 
     // ---- the walk over images ----
     const TileView all = IMAGES ? sequence_view(a, q) : view;
@@ -507,7 +537,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             copy(1);
         uint32_t word = word_of(0);
         ev = (int)(word >> 10 & 1023) - 256;
-        int top = ev;
         arrive(0);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -527,16 +556,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 if ((n + 1) % PER == 0 && n + 1 < count)
                     arrive((n + 1) / PER);
                 const int ek = (int)(word & 1023) - 256, er = (int)(word >> 10 & 1023) - 256;
-                if (er != ev) {
-                    rare();
-                    top = top > er ? top : er;
-                    const int to = er > top - 64 ? er : top - 64;
-                    const float g = ldexpf(1.f, ev - to);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        o[d] *= g;
-                    ev = to;
-                }
                 const float f = fmaxf(ldexpf(fabsf(a.scale), qe + ek), 1.17549435e-38f);
                 f16x8 k0[HS], k1[HS], v0[DT], v1[DT], p[2];
                 read_k(image(n + 1), 0, k0);
@@ -555,12 +574,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                     sum = probabilities(now, f, p);
                 }
                 l += sum;
-                if (er != ev) { // 2^64 below an earlier one's
-                    rare();
-                    const _Float16 g = (_Float16)ldexpf(1.f, er - ev);
-                    p[0] *= g;
-                    p[1] *= g;
-                }
+                if (__any(er != ev))
+                    meet(er, p);
                 if (word >> 20 & 1 && !idle)
                     find_taint(view_block(view, begin + n));
 #pragma unroll
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
     // ---- the walk over codes ----
     if (!laid_out) {
         uint64_t there = 0, there1 = 0, clear = 0, clear1 = 0; // of this step, the next
-        int ek = 0, ek1 = 0, ev1 = 0, top = 0, page = -1;
+        int ek = 0, ek1 = 0, er = 0, er1 = 0, page = -1; // er: of the step's values
         bool bad = false, bad1 = false, full1 = false;
         f32x16 x[2];
         if (steps > 0) {
@@ -591,7 +606,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
             fetch(0, page0, there);
             seen_by(0, there, clear, full);
             exponents(0, full, ek, ev, bad);
-            top = ev;
+            er = ev;
             expand_k(0, full, ek, lds);
             expand_v(0, full && !bad, ev, lds + 2 * BUF);
             fetch(1, page1, there1);
@@ -631,6 +646,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 logits(k1, 1, then);
                 read_v(vbuf, t, 1, v1);
                 fence();
+                if (__any(er != ev))
+                    meet(er, p);
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] = mfma32(v0[d], p[0], o[d]);
@@ -639,13 +656,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                     o[d] = mfma32(v1[d], p[1], o[d]);
                 if (t == TB - 2) {
                     seen_by(step + 1, there1, clear1, full1);
-                    exponents(step + 1, full1, ek1, ev1, bad1);
-                    top = top > ev1 ? top : ev1;
-                    ev1 = ev1 > top - 64 ? ev1 : top - 64;
+                    exponents(step + 1, full1, ek1, er1, bad1);
                     expand_k(step + 1, full1, ek1, kb1);
                     __syncthreads();
                 } else if (t == TB - 1) {
-                    expand_v(step + 1, full1 && !bad1, ev1, vb1);
+                    expand_v(step + 1, full1 && !bad1, er1, vb1);
                     __syncthreads();
                 }
                 if (t + 1 < TB)
@@ -657,14 +672,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 for (int t = 0; t < TB; ++t)
                     if (bit(there, t))
                         find_taint(block_at(step, t));
-            if (ev1 != ev) {
-                const float g = ldexpf(1.f, ev - ev1);
-#pragma unroll
-                for (int t = 0; t < DT; ++t)
-                    o[t] *= g;
-            }
             ek = ek1;
-            ev = ev1;
+            er = er1;
             bad = bad1;
             there = there1;
             clear = clear1;
@@ -696,7 +705,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attend_prompt_kernel(AttendArg
                 put(d * 32 + 8 * r4 + 4 * h, v);
             }
     };
-    const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head;
+    // (its place again, rather than in registers through the walk)
+    int again = tile * kRows + mine;
+    asm volatile("" : "+v"(again));
+    const int oi = quotient(again, a.by_group), oh = head * a.group + again - oi * a.group;
+    const int64_t to = (int64_t)(q.row0 + oi) * a.ldo + oh * a.o_head;
     if (splits > 1)
         each([&](int col, f32x4 v) { *reinterpret_cast<f32x4 *>(a.part + slot * D + col) = v; });
     else if (a.o_bf16)

@@ -59,3 +59,28 @@ def test_small_runs_beside_a_large_one(rows, d, k):
     got, want, mag = setup(rows, d, ctx, big, V, np.ones(rows), kind="f32")
     au.within(got, np.broadcast_to(want, got.shape),
               (2.0 ** -11 + (ctx + 8) * au.U) * mag + 3 * 2.0 ** -25 * 2.0 ** -10.9 * 64.5 + 1e-38, k)
+
+
+@pytest.mark.parametrize("rows", [1, 60, 150])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("be,e", [(40, 0), (100, 0), (100, -60), (98, -100), (-100, 20)])
+@pytest.mark.parametrize("where", ["first", "middle", "turns", "fives"])
+def test_values_without_weight(rows, d, be, e, where):
+    """2^be values that most rows pass over without weight, and every third row
+    gives all its weight, before, among or in turn with the others' 2^e."""
+    ctx = 600
+    t = np.arange(ctx)
+    big = {"first": t < 128, "middle": (t >= 256) & (t < 384), "turns": t // 32 % 2 == 1,
+           "fives": t % 5 == 0}[where]
+    r = au.rng(d + rows)
+    V = au.rne(r.standard_normal((ctx, 1, d)) * np.where(big, 2.0 ** be, 2.0 ** e)[:, None, None], "bf16")
+    signs = np.where(np.arange(rows) % 3 == 1, -1.0, 1.0)
+    got, want, mag = setup(rows, d, ctx, big, V, signs)
+    size = np.where(signs < 0, 2.0 ** be, 2.0 ** e)[:, None, None] * 8
+    if where in ("turns", "fives") and rows > 1:
+        # the two kinds are neighbours: what the large ones leave of the small is not
+        # kept, the large ones are
+        keep = signs < 0 if be > e else signs > 0
+        got, want, mag, size = got[keep], want[keep], mag[keep], size[keep]
+    au.within(got, np.broadcast_to(want, got.shape),
+              (2.0 ** -11 + (ctx + 8) * au.U) * mag + 3 * 2.0 ** -25 * 2.0 ** -10.9 * size + 1e-38, where)
