@@ -175,7 +175,7 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
     a.c = cache_args(*cache, *seqs);
     // a run of n rows touches at most so many records, wherever it starts
     a.seq_blocks = a.c.max_rows > 0 ? (a.c.max_rows + kBlock - 2) / kBlock + 1 : 0;
-    if ((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks > kMaxBlocks)
+    if ((int64_t)a.c.n_kv_heads * a.seq_blocks > kMaxBlocks) // (of a sequence)
         return TSL_ERR_UNSUPPORTED;
     if (!nothing(*seqs) &&
         (meets_cache(k, *cache, *seqs, read) || meets_cache(v, *cache, *seqs, read) ||
@@ -189,7 +189,6 @@ tsl_status move_args(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dty
     a.v_head = v_head;
     a.bf16 = dtype == TSL_BF16;
     a.by_heads = make_div((uint32_t)a.c.n_kv_heads);
-    a.by_blocks = make_div((uint32_t)std::max(a.seq_blocks, 1));
     *out = a;
     return TSL_OK;
 }

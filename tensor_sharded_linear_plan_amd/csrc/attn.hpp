@@ -75,7 +75,7 @@ struct MoveArgs {
     int64_t ldk, k_head, ldv, v_head;
     int32_t bf16;
     int32_t seq_blocks; // records a sequence's rows may span
-    Div by_heads, by_blocks;
+    Div by_heads;
 };
 
 hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream);

@@ -27,9 +27,8 @@ template <int D>
 __device__ __forceinline__ Span span_of(const MoveArgs &a) {
     // neighbouring workgroups take the heads of the same rows
     Span w;
-    const int rest = quotient(blockIdx.x, a.by_heads), s = quotient(rest, a.by_blocks);
-    w.head = blockIdx.x - rest * a.c.n_kv_heads;
-    const int blk_i = rest - s * a.seq_blocks;
+    const int blk_i = quotient(blockIdx.x, a.by_heads), s = blockIdx.y;
+    w.head = blockIdx.x - blk_i * a.c.n_kv_heads;
     const SeqRows q = seq_rows(a.c, s);
     const int n = q.n < a.c.max_rows ? q.n : a.c.max_rows;
     const int start = q.ctx - q.n; // position of row 0
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
 } // namespace
 
 hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks));
+    const dim3 grid((unsigned)(a.c.n_kv_heads * a.seq_blocks), (unsigned)a.c.n_seqs);
     if (head_dim == 64)
         hipLaunchKernelGGL(append_kernel<64>, grid, dim3(kThreads), 0, stream, a);
     else if (head_dim == 128)
@@ -257,7 +256,7 @@ hipError_t launch_cache_append(int head_dim, const MoveArgs &a, hipStream_t stre
 }
 
 hipError_t launch_cache_read(int head_dim, const MoveArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.c.n_seqs * a.c.n_kv_heads * a.seq_blocks));
+    const dim3 grid((unsigned)(a.c.n_kv_heads * a.seq_blocks), (unsigned)a.c.n_seqs);
     if (head_dim == 64)
         hipLaunchKernelGGL(read_kernel<64>, grid, dim3(kThreads), 0, stream, a);
     else if (head_dim == 128)
