@@ -272,11 +272,11 @@ tsl_status plan_kernel(const tsl_cache &c, const tsl_seqs &q, int64_t group, int
     p->parts = (int32_t)std::min<int64_t>(p->units, kMaxWaves + 1);
     p->ranges = 0;
     // (a call of more sequences than that has several tiles for every wave as it
-    // is; records are counted in 32 bits)
+    // is; records, and the waves' number beside them, are counted in 32 bits)
     const int64_t held = ((int64_t)q.max_pages * c.page_tokens + kBlock - 1) / kBlock;
-    if (few && records > kWholeRecords && q.n_seqs <= kMaxShared && p->units * held <= INT32_MAX) {
+    const int64_t places = kCUs * 4 * attend_groups(c.head_dim); // waves that fit
+    if (few && records > kWholeRecords && q.n_seqs <= kMaxShared && p->units * held <= INT32_MAX - places) {
         p->shared = 1;
-        const int64_t places = kCUs * 4 * attend_groups(c.head_dim); // waves that fit
         p->parts = (int32_t)std::min(places, p->units * most);
         p->ranges = 2 * p->parts;
     }

@@ -55,3 +55,10 @@ def test_many_sequences_of_many_rows(tsl_lib, n, rows):
         images = (1 << 30) + (1 << 21) if rows * hq // hkv > 256 else 0
         most = 512 * 128 * (d + 2) * 4 + few_rows(d, 16, n * hkv * 16) + images
         assert size(tsl_lib, d, hq, hkv, n_seqs=n, rows=min(n * rows, (1 << 22) - 1), max_rows=rows) <= most
+
+
+def test_records_are_counted_in_32_bits(tsl_lib):
+    """A call is divided by its records only where their number, rounded up to a
+    multiple of the waves, stays below 2^31: 1023 tiles of 2099202 records do not."""
+    assert size(tsl_lib, 128, 1, 1, page=32, n_seqs=1023, rows=1023, max_pages=2099202) == 0
+    assert size(tsl_lib, 128, 1, 1, page=32, n_seqs=1023, rows=1023, max_pages=2099202 - 5) > 0
