@@ -147,7 +147,8 @@ tsl_status cache_size(const tsl_cache *cache, size_t *bytes);
  *     b = bf16(min x),  s = bf16((max x - b) / 15),
  *     c = clamp(round((x - b) / s), 0, 15)          (s = 0: c = 0)
  * where b and s are formed in binary32 and rounded to nearest even, and the
- * quotient is rounded exactly, ties to even.  A run with a value that is not
+ * quotient is rounded exactly, ties to even.  (Where b, rounded, lies above all of a
+ * narrow run, s is negative and the codes count down from b.)  A run with a value that is not
  * finite, or whose s or b is not (max x - b past binary32's range), has a
  * scale and a bias of NaN: all of it reads NaN.
  *   K, V: DEVICE [rows][n_kv_heads][head_dim] of type dtype (F32 or BF16).
