@@ -147,10 +147,10 @@ tsl_status cache_size(const tsl_cache *cache, size_t *bytes);
  *     b = bf16(min x),  s = bf16((max x - b) / 15),
  *     c = clamp(round((x - b) / s), 0, 15)          (s = 0: c = 0)
  * where b and s are formed in binary32 and rounded to nearest even, and the
- * quotient is rounded exactly, ties to even.  (Where b, rounded, lies above all of a
- * narrow run, s is negative and the codes count down from b.)  A run with a value that is not
- * finite, or whose s or b is not (max x - b past binary32's range), has a
- * scale and a bias of NaN: all of it reads NaN.
+ * quotient is rounded exactly, ties to even.  (Where b, rounded, lies above
+ * all of a narrow run, s is negative and the codes count down from b.)  A run with
+ * a value that is not finite, or whose s or b is not (max x - b past binary32's
+ * range), has a scale and a bias of NaN: all of it reads NaN.
  *   K, V: DEVICE [rows][n_kv_heads][head_dim] of type dtype (F32 or BF16).
  * Other tokens of the pages keep their bits.  A page that a call writes to
  * belongs to one of its sequences (copy a shared page first), and K and V
@@ -204,7 +204,7 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * sequence sees have in common: values below 2^-22 of the largest of those lose
  * bits, as do values below 2^-90 of an earlier one that the row gave weight to;
  * probabilities below 2^-23 of the row's largest so far lose bits, and below
- * 2^-31 they are 0.  Both kinds may be in one call (generated tokens beside a
+ * 2^-31 they are 0; so do elements of Q below 2^-31 of their head's largest.  Both kinds may be in one call (generated tokens beside a
  * prompt's chunk).  |Q| stays below 2^110, scale sum |q k| of a visible token
  * within binary32's range, and sum |v| over a row's tokens below 2^110 (what other
  * rows get does not hang on a row that does not keep to it).  Equal calls give

@@ -185,294 +185,294 @@ __global__ void __launch_bounds__(64 * kWaves, attend_groups(D)) attend_decode_k
         }
     };
     while (true) {
-    const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
-    const int rows = rows_of(a, q) - tile * ROWS; // of this tile and later ones
-    TileView view = {0, 0, 0, 0, 0, 0, 0};
-    if (rows > 0)
-        view = view_of(a, q, tile, ROWS, rows);
-    else if (!a.shared)
-        return;
-    // on to the tile where the part begins, past those without records
-    if (a.shared && at >= view.count) {
-        at -= view.count;
-        next_tile();
-        continue;
-    }
-    const int start = q.ctx - q.n;
-    const int begin = at;
-    const int stop = view.count - at < left ? view.count : at + left;
-    const bool complete = begin == 0 && stop == view.count;
-
-    // the wave's next 64 records, one a lane: where they lie, and as bits which
-    // are there and which all rows of the tile see all of
-    const int n_mine = stop - begin;
-    uint32_t at_lo = 0, at_hi = 0;
-    uint64_t there = 0, clear = 0, next_there = 0, next_clear = 0;
-    auto look_up = [&](int k0) {
-        const int r = begin + k0 + lane;
-        const int blk = view_block(view, r);
-        const char *rec = r < stop ? record_of(a.c, s, head, blk, REC) : nullptr;
-        next_there = __ballot(rec != nullptr);
-        next_clear = __ballot(sees_all(a, view, blk));
-        // one that is not there is read from page 0, and passed over
-        const uint64_t p = reinterpret_cast<uint64_t>(rec ? rec : a.c.pages);
-        at_lo = (uint32_t)p;
-        at_hi = (uint32_t)(p >> 32);
-    };
-    const uint32_t lds0 = (uint32_t)(uintptr_t)&ring[wave][0];
-    auto issue = [&](int k) { // record k of the wave into its stage
-        if ((k & 63) == 0)
-            look_up(k);
-        const uint64_t p = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)at_hi, k & 63) << 32 |
-                           (uint32_t)__builtin_amdgcn_readlane((int)at_lo, k & 63);
-        const char *rec = reinterpret_cast<const char *>(p);
-        const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + (k % kStages) * REC));
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i)
-            if ((i + 1) * 64 <= PIECES || lane < PIECES - i * 64)
-                dma16(rec + i * 1024, (uint32_t)lane * 16, to + i * 1024);
-    };
-    // the lane's query row
-    const bool live = cr < rows;
-    const int rho = tile * ROWS + (live ? cr : 0);
-    const int i = quotient(rho, a.by_group), hq = head * a.group + rho - i * a.group;
-    const int pos = start + i, lo = window_start(a, pos);
-    const uint16_t *qp = a.Q + (int64_t)(q.row0 + i) * a.ldq + hq * a.q_head + 8 * g;
-    bf16x8 qr[W];
-#pragma unroll
-    for (int w = 0; w < W; ++w) // the scale's sign goes to Q: the largest product
-        qr[w] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(qp + 32 * w) ^
-                                               (a.scale < 0.f ? 0x80008000u : 0u)); // is the largest logit
-    const float scale = fmaxf(fabsf(a.scale), 1.17549435e-38f); // not 0: it meets infinities
-
-    f32x4 o[DT], off[G], base[G];
-    float ob[G], qsum[G], m = kNoMax, l = 0.f;
-    const bf16x8 all128 = __builtin_bit_cast(bf16x8, u32x4{0x43004300u, 0x43004300u, 0x43004300u, 0x43004300u});
-    const bf16x8 offsets = __builtin_bit_cast(bf16x8, u32x4{0x43004300u, 0x41804180u, 0x41804180u, 0x41804180u});
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-        o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int d = 0; d < G; ++d) {
-        ob[d] = 0.f;
-        off[d] = base[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // -128 sum(q), in every row of the product: what a product begins with
-#pragma unroll
-        for (int w = 2 * d; w < 2 * d + 2; ++w)
-            base[d] = mfma_bf16(all128, qr[w], base[d]);
-        base[d] = -base[d];
-        qsum[d] = base[d][0] * -0.0078125f;
-    }
-
-    auto settle = [&] {
-        rare();
-#pragma unroll
-        for (int d = 0; d < G; ++d) {
-            ob[d] += __shfl_xor(ob[d], 16, 64);
-            ob[d] += __shfl_xor(ob[d], 32, 64);
-#pragma unroll
-            for (int t = 4 * d; t < 4 * d + 4; ++t)
-                o[t] = (o[t] - off[d]) + ob[d];
-            ob[d] = 0.f;
-            off[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-    };
-
-    // (one place that looks up and copies: cold code is what a start takes long over)
-    for (int k = 1 - kStages; k < n_mine; ++k) {
-        if (k > 0 && k % kSettle == 0)
-            settle();
-        if (k + kStages - 1 < n_mine) {
-            wait_lgkm0(); // the stage was read
-            issue(k + kStages - 1);
-            if (k < 0)
-                continue;
-            wait_copies<(kStages - 1) * COPIES>();
-        } else if (k < 0) {
+        const int unit = (s * a.c.n_kv_heads + head) * a.tiles + tile;
+        const int rows = rows_of(a, q) - tile * ROWS; // of this tile and later ones
+        TileView view = {0, 0, 0, 0, 0, 0, 0};
+        if (rows > 0)
+            view = view_of(a, q, tile, ROWS, rows);
+        else if (!a.shared)
+            return;
+        // on to the tile where the part begins, past those without records
+        if (a.shared && at >= view.count) {
+            at -= view.count;
+            next_tile();
             continue;
-        } else if (kStages > 3 && k + 2 < n_mine) {
-            wait_copies<2 * COPIES>();
-        } else if (kStages > 2 && k + 1 < n_mine) {
-            wait_copies<COPIES>();
-        } else {
-            wait_copies<0>();
         }
-        if ((k & 63) == 0) { // (looked up kStages - 1 records ago)
-            there = next_there;
-            clear = next_clear;
-        }
-        if (!(there >> (k & 63) & 1))
-            continue;
-        const u32x4 *rec = reinterpret_cast<const u32x4 *>(&ring[wave][(k % kStages) * REC]);
-        // scales of the lane's tokens, in pairs
-        typedef uint32_t pairs __attribute__((ext_vector_type(TPL / 2)));
-        auto scales = [&](int d, int kind) {
-            const pairs v = *reinterpret_cast<const pairs *>(reinterpret_cast<const char *>(rec + 2 * D) +
-                                                             d * 256 + kind * 64 + g * 16 + own * TPL * 2);
-            return v;
+        const int start = q.ctx - q.n;
+        const int begin = at;
+        const int stop = view.count - at < left ? view.count : at + left;
+        const bool complete = begin == 0 && stop == view.count;
+
+        // the wave's next 64 records, one a lane: where they lie, and as bits which
+        // are there and which all rows of the tile see all of
+        const int n_mine = stop - begin;
+        uint32_t at_lo = 0, at_hi = 0;
+        uint64_t there = 0, clear = 0, next_there = 0, next_clear = 0;
+        auto look_up = [&](int k0) {
+            const int r = begin + k0 + lane;
+            const int blk = view_block(view, r);
+            const char *rec = r < stop ? record_of(a.c, s, head, blk, REC) : nullptr;
+            next_there = __ballot(rec != nullptr);
+            next_clear = __ballot(sees_all(a, view, blk));
+            // one that is not there is read from page 0, and passed over
+            const uint64_t p = reinterpret_cast<uint64_t>(rec ? rec : a.c.pages);
+            at_lo = (uint32_t)p;
+            at_hi = (uint32_t)(p >> 32);
         };
+        const uint32_t lds0 = (uint32_t)(uintptr_t)&ring[wave][0];
+        auto issue = [&](int k) { // record k of the wave into its stage
+            if ((k & 63) == 0)
+                look_up(k);
+            const uint64_t p = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)at_hi, k & 63) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)at_lo, k & 63);
+            const char *rec = reinterpret_cast<const char *>(p);
+            const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds0 + (k % kStages) * REC));
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i)
+                if ((i + 1) * 64 <= PIECES || lane < PIECES - i * 64)
+                    dma16(rec + i * 1024, (uint32_t)lane * 16, to + i * 1024);
+        };
+        // the lane's query row
+        const bool live = cr < rows;
+        const int rho = tile * ROWS + (live ? cr : 0);
+        const int i = quotient(rho, a.by_group), hq = head * a.group + rho - i * a.group;
+        const int pos = start + i, lo = window_start(a, pos);
+        const uint16_t *qp = a.Q + (int64_t)(q.row0 + i) * a.ldq + hq * a.q_head + 8 * g;
+        bf16x8 qr[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) // the scale's sign goes to Q: the largest product
+            qr[w] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(qp + 32 * w) ^
+                                                   (a.scale < 0.f ? 0x80008000u : 0u)); // is the largest logit
+        const float scale = fmaxf(fabsf(a.scale), 1.17549435e-38f); // not 0: it meets infinities
 
-        float x[TPL]; // products, the scale not yet in them
+        f32x4 o[DT], off[G], base[G];
+        float ob[G], qsum[G], m = kNoMax, l = 0.f;
+        const bf16x8 all128 = __builtin_bit_cast(bf16x8, u32x4{0x43004300u, 0x43004300u, 0x43004300u, 0x43004300u});
+        const bf16x8 offsets = __builtin_bit_cast(bf16x8, u32x4{0x43004300u, 0x41804180u, 0x41804180u, 0x41804180u});
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+            o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < G; ++d) {
-            f32x4 acc[2];
+            ob[d] = 0.f;
+            off[d] = base[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // -128 sum(q), in every row of the product: what a product begins with
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                acc[u] = base[d];
-#pragma unroll
-                for (int w = 2 * d; w < 2 * d + 2; ++w) {
-                    const int n = u * W + w;
-                    acc[u] = mfma_bf16(q4_to_bf16_plus128(rec[(n >> 2) * 64 + lane][n & 3]), qr[w], acc[u]);
-                }
-            }
-            const pairs ks = scales(d, 0), kb = scales(d, 1);
-#pragma unroll
-            for (int e = 0; e < TPL; ++e) {
-                float t = acc[e >> 2][e & 3];
-                if (P == 2)
-                    t = own ? acc[1][e] : acc[0][e];
-                if (P == 4) {
-                    const float lo2 = own & 2 ? acc[1][e] : acc[0][e], hi2 = own & 2 ? acc[1][2 + e] : acc[0][2 + e];
-                    t = own & 1 ? hi2 : lo2;
-                }
-                const float s1 = e & 1 ? bf16_hi(ks[e >> 1]) : bf16_lo(ks[e >> 1]);
-                const float b1 = e & 1 ? bf16_hi(kb[e >> 1]) : bf16_lo(kb[e >> 1]);
-                x[e] = d ? fmaf(b1, qsum[d], x[e]) : b1 * qsum[d];
-                x[e] = fmaf(s1, t, x[e]);
-            }
+            for (int w = 2 * d; w < 2 * d + 2; ++w)
+                base[d] = mfma_bf16(all128, qr[w], base[d]);
+            base[d] = -base[d];
+            qsum[d] = base[d][0] * -0.0078125f;
         }
-        pairs keep; // of the V scales: a hidden token's may be NaN
-#pragma unroll
-        for (int e = 0; e < TPL / 2; ++e)
-            keep[e] = ~0u;
-        const bool all = clear >> (k & 63) & 1;
-        if (!all) {
+
+        auto settle = [&] {
             rare();
-            const int blk = view_block(view, begin + k);
-#pragma unroll
-            for (int e = 0; e < TPL; ++e) {
-                const int at = own * TPL + e;
-                const bool v = sees(a, pos, lo, blk * kBlock + (at >> 2) * 16 + g * 4 + (at & 3));
-                x[e] = v ? x[e] : -__builtin_inff();
-                keep[e >> 1] &= v ? ~0u : (e & 1 ? 0xFFFFu : 0xFFFF0000u);
-            }
-        }
-        float top = x[0];
-#pragma unroll
-        for (int e = 1; e < TPL; ++e)
-            top = fmaxf(top, x[e]);
-        top *= scale;
-        // the reference exponent follows the maximum at a distance of 2^8:
-        // binary32 sums have room for it, and rescaling becomes rare
-        if (__any(top > m + 8.f)) {
-            rare();
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float to = fmaxf(m, top), f = exp2_fast(m - to);
-            m = to;
-            l *= f;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-                o[t] *= f;
 #pragma unroll
             for (int d = 0; d < G; ++d) {
-                ob[d] *= f;
-                off[d] *= f;
+                ob[d] += __shfl_xor(ob[d], 16, 64);
+                ob[d] += __shfl_xor(ob[d], 32, 64);
+#pragma unroll
+                for (int t = 4 * d; t < 4 * d + 4; ++t)
+                    o[t] = (o[t] - off[d]) + ob[d];
+                ob[d] = 0.f;
+                off[d] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
-        }
-        float pr[TPL];
-#pragma unroll
-        for (int e = 0; e < TPL; ++e) {
-            pr[e] = exp2_fast(fmaf(x[e], scale, -m));
-            l += pr[e];
-        }
-#pragma unroll
-        for (int d = 0; d < G; ++d) {
-            pairs vs = scales(d, 2), vb = scales(d, 3);
-            if (!all) {
-                rare();
-                vs &= keep;
-                vb &= keep;
+        };
+
+        // (one place that looks up and copies: cold code is what a start takes long over)
+        for (int k = 1 - kStages; k < n_mine; ++k) {
+            if (k > 0 && k % kSettle == 0)
+                settle();
+            if (k + kStages - 1 < n_mine) {
+                wait_lgkm0(); // the stage was read
+                issue(k + kStages - 1);
+                if (k < 0)
+                    continue;
+                wait_copies<(kStages - 1) * COPIES>();
+            } else if (k < 0) {
+                continue;
+            } else if (kStages > 3 && k + 2 < n_mine) {
+                wait_copies<2 * COPIES>();
+            } else if (kStages > 2 && k + 1 < n_mine) {
+                wait_copies<COPIES>();
+            } else {
+                wait_copies<0>();
             }
-            u32x4 hi = {0, 0, 0, 0}, rem = {0, 0, 0, 0};
+            if ((k & 63) == 0) { // (looked up kStages - 1 records ago)
+                there = next_there;
+                clear = next_clear;
+            }
+            if (!(there >> (k & 63) & 1))
+                continue;
+            const u32x4 *rec = reinterpret_cast<const u32x4 *>(&ring[wave][(k % kStages) * REC]);
+            // scales of the lane's tokens, in pairs
+            typedef uint32_t pairs __attribute__((ext_vector_type(TPL / 2)));
+            auto scales = [&](int d, int kind) {
+                const pairs v = *reinterpret_cast<const pairs *>(reinterpret_cast<const char *>(rec + 2 * D) +
+                                                                 d * 256 + kind * 64 + g * 16 + own * TPL * 2);
+                return v;
+            };
+
+            float x[TPL]; // products, the scale not yet in them
 #pragma unroll
-            for (int h = 0; h < TPL / 2; ++h) {
-                const float w0 = pr[2 * h] * bf16_lo(vs[h]), w1 = pr[2 * h + 1] * bf16_hi(vs[h]);
-                ob[d] = fmaf(pr[2 * h], bf16_lo(vb[h]), ob[d]);
-                ob[d] = fmaf(pr[2 * h + 1], bf16_hi(vb[h]), ob[d]);
-                const uint32_t p16 = pack_pair(w0, w1);
-                const uint32_t r16 = pack_pair(w0 - bf16_lo(p16), w1 - bf16_hi(p16));
+            for (int d = 0; d < G; ++d) {
+                f32x4 acc[2];
 #pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    hi[k * (TPL / 2) + h] = P == 1 || own == k ? p16 : 0u;
-                    rem[k * (TPL / 2) + h] = P == 1 || own == k ? r16 : 0u;
+                for (int u = 0; u < 2; ++u) {
+                    acc[u] = base[d];
+#pragma unroll
+                    for (int w = 2 * d; w < 2 * d + 2; ++w) {
+                        const int n = u * W + w;
+                        acc[u] = mfma_bf16(q4_to_bf16_plus128(rec[(n >> 2) * 64 + lane][n & 3]), qr[w], acc[u]);
+                    }
+                }
+                const pairs ks = scales(d, 0), kb = scales(d, 1);
+#pragma unroll
+                for (int e = 0; e < TPL; ++e) {
+                    float t = acc[e >> 2][e & 3];
+                    if (P == 2)
+                        t = own ? acc[1][e] : acc[0][e];
+                    if (P == 4) {
+                        const float lo2 = own & 2 ? acc[1][e] : acc[0][e], hi2 = own & 2 ? acc[1][2 + e] : acc[0][2 + e];
+                        t = own & 1 ? hi2 : lo2;
+                    }
+                    const float s1 = e & 1 ? bf16_hi(ks[e >> 1]) : bf16_lo(ks[e >> 1]);
+                    const float b1 = e & 1 ? bf16_hi(kb[e >> 1]) : bf16_lo(kb[e >> 1]);
+                    x[e] = d ? fmaf(b1, qsum[d], x[e]) : b1 * qsum[d];
+                    x[e] = fmaf(s1, t, x[e]);
                 }
             }
-            const bf16x8 wh = __builtin_bit_cast(bf16x8, hi), wl = __builtin_bit_cast(bf16x8, rem);
-            // what z + c has over c: the same products with a tile of z
-            off[d] = mfma_bf16(offsets, wh, off[d]);
-            off[d] = mfma_bf16(offsets, wl, off[d]);
-            const u32x4 vc = rec[D + d * 64 + lane];
+            pairs keep; // of the V scales: a hidden token's may be NaN
 #pragma unroll
-            for (int t = 4 * d; t < 4 * d + 4; ++t) {
-                const bf16x8 v = v_codes(vc[t & 3]);
-                o[t] = mfma_bf16(v, wh, o[t]);
-                o[t] = mfma_bf16(v, wl, o[t]);
+            for (int e = 0; e < TPL / 2; ++e)
+                keep[e] = ~0u;
+            const bool all = clear >> (k & 63) & 1;
+            if (!all) {
+                rare();
+                const int blk = view_block(view, begin + k);
+#pragma unroll
+                for (int e = 0; e < TPL; ++e) {
+                    const int at = own * TPL + e;
+                    const bool v = sees(a, pos, lo, blk * kBlock + (at >> 2) * 16 + g * 4 + (at & 3));
+                    x[e] = v ? x[e] : -__builtin_inff();
+                    keep[e >> 1] &= v ? ~0u : (e & 1 ? 0xFFFFu : 0xFFFF0000u);
+                }
+            }
+            float top = x[0];
+#pragma unroll
+            for (int e = 1; e < TPL; ++e)
+                top = fmaxf(top, x[e]);
+            top *= scale;
+            // the reference exponent follows the maximum at a distance of 2^8:
+            // binary32 sums have room for it, and rescaling becomes rare
+            if (__any(top > m + 8.f)) {
+                rare();
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float to = fmaxf(m, top), f = exp2_fast(m - to);
+                m = to;
+                l *= f;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    o[t] *= f;
+#pragma unroll
+                for (int d = 0; d < G; ++d) {
+                    ob[d] *= f;
+                    off[d] *= f;
+                }
+            }
+            float pr[TPL];
+#pragma unroll
+            for (int e = 0; e < TPL; ++e) {
+                pr[e] = exp2_fast(fmaf(x[e], scale, -m));
+                l += pr[e];
+            }
+#pragma unroll
+            for (int d = 0; d < G; ++d) {
+                pairs vs = scales(d, 2), vb = scales(d, 3);
+                if (!all) {
+                    rare();
+                    vs &= keep;
+                    vb &= keep;
+                }
+                u32x4 hi = {0, 0, 0, 0}, rem = {0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < TPL / 2; ++h) {
+                    const float w0 = pr[2 * h] * bf16_lo(vs[h]), w1 = pr[2 * h + 1] * bf16_hi(vs[h]);
+                    ob[d] = fmaf(pr[2 * h], bf16_lo(vb[h]), ob[d]);
+                    ob[d] = fmaf(pr[2 * h + 1], bf16_hi(vb[h]), ob[d]);
+                    const uint32_t p16 = pack_pair(w0, w1);
+                    const uint32_t r16 = pack_pair(w0 - bf16_lo(p16), w1 - bf16_hi(p16));
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        hi[k * (TPL / 2) + h] = P == 1 || own == k ? p16 : 0u;
+                        rem[k * (TPL / 2) + h] = P == 1 || own == k ? r16 : 0u;
+                    }
+                }
+                const bf16x8 wh = __builtin_bit_cast(bf16x8, hi), wl = __builtin_bit_cast(bf16x8, rem);
+                // what z + c has over c: the same products with a tile of z
+                off[d] = mfma_bf16(offsets, wh, off[d]);
+                off[d] = mfma_bf16(offsets, wl, off[d]);
+                const u32x4 vc = rec[D + d * 64 + lane];
+#pragma unroll
+                for (int t = 4 * d; t < 4 * d + 4; ++t) {
+                    const bf16x8 v = v_codes(vc[t & 3]);
+                    o[t] = mfma_bf16(v, wh, o[t]);
+                    o[t] = mfma_bf16(v, wl, o[t]);
+                }
             }
         }
-    }
 
-    // join the lanes and columns of a row
-    settle();
-    {
-        auto more = [](float u, float v) { return fmaxf(u, v); };
-        auto sum = [](float u, float v) { return u + v; };
-        const float top = over_groups<P>(m, more);
-        float f = exp2_fast(m - top);
-        l += __shfl_xor(l, 16, 64);
-        l += __shfl_xor(l, 32, 64);
-        l = over_groups<P>(l * f, sum);
-        const float inv = !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-        const int64_t slot = (int64_t)(begin == 0 ? a.parts + me : me) * ROWS + c;
-        const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head + 4 * g;
-        const bool mine = live && !own;
-        if (!complete && mine && g == 0) {
-            a.part_ml[2 * slot] = top;
-            a.part_ml[2 * slot + 1] = l;
-        }
+        // join the lanes and columns of a row
+        settle();
+        {
+            auto more = [](float u, float v) { return fmaxf(u, v); };
+            auto sum = [](float u, float v) { return u + v; };
+            const float top = over_groups<P>(m, more);
+            float f = exp2_fast(m - top);
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+            l = over_groups<P>(l * f, sum);
+            const float inv = !complete ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            const int64_t slot = (int64_t)(begin == 0 ? a.parts + me : me) * ROWS + c;
+            const int64_t to = (int64_t)(q.row0 + i) * a.ldo + hq * a.o_head + 4 * g;
+            const bool mine = live && !own;
+            if (!complete && mine && g == 0) {
+                a.part_ml[2 * slot] = top;
+                a.part_ml[2 * slot + 1] = l;
+            }
 #pragma unroll
-        for (int d = 0; d < G; ++d) {
+            for (int d = 0; d < G; ++d) {
 #pragma unroll
-            for (int t = 4 * d; t < 4 * d + 4; ++t) {
-                f32x4 v = o[t] * f;
+                for (int t = 4 * d; t < 4 * d + 4; ++t) {
+                    f32x4 v = o[t] * f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = over_groups<P>(v[e], sum) * inv;
-                if (!mine)
-                    continue;
-                if (!complete)
-                    *reinterpret_cast<f32x4 *>(a.part + slot * D + 16 * t + 4 * g) = v;
-                else if (a.o_bf16)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + to + 16 * t) =
-                        u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
-                else
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + to + 16 * t) = v;
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = over_groups<P>(v[e], sum) * inv;
+                    if (!mine)
+                        continue;
+                    if (!complete)
+                        *reinterpret_cast<f32x4 *>(a.part + slot * D + 16 * t + 4 * g) = v;
+                    else if (a.o_bf16)
+                        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.O) + to + 16 * t) =
+                            u32x2{pack_pair(v[0], v[1]), pack_pair(v[2], v[3])};
+                    else
+                        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.O) + to + 16 * t) = v;
+                }
             }
         }
-    }
-    if (!a.shared)
-        return;
-    if (lane == 0) { // for the join: the waves that share the tile
-        if (begin == 0)
-            a.spans[2 * unit] = me;
-        if (stop == view.count)
-            a.spans[2 * unit + 1] = me;
-    }
-    left -= stop - begin;
-    if (left <= 0)
-        return;
-    at = 0;
-    next_tile();
+        if (!a.shared)
+            return;
+        if (lane == 0) { // for the join: the waves that share the tile
+            if (begin == 0)
+                a.spans[2 * unit] = me;
+            if (stop == view.count)
+                a.spans[2 * unit + 1] = me;
+        }
+        left -= stop - begin;
+        if (left <= 0)
+            return;
+        at = 0;
+        next_tile();
     }
 }
 

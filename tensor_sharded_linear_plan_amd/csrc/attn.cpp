@@ -389,7 +389,7 @@ extern "C" tsl_status rotate_heads(int32_t n_items, const tsl_rotate_item *items
         heads += it.n_heads;
         a.item[i] = RotateArgs::Item{it.X,       it.Y,      it.ldx, it.x_head,
                                      it.ldy,     it.y_head, it.n_heads, it.xdtype == TSL_BF16,
-                                     it.ydtype == TSL_BF16, 0};
+                                     it.ydtype == TSL_BF16};
     }
     if (M == 0)
         return TSL_OK;
@@ -410,7 +410,6 @@ extern "C" tsl_status rotate_heads(int32_t n_items, const tsl_rotate_item *items
     a.freq = r.freq;
     a.ld_pos = r.ld_pos;
     a.M = M;
-    a.n_items = n_items;
     a.heads = (int32_t)heads;
     a.rot_dim = r.rot_dim;
     a.head_dim = r.head_dim;

@@ -19,12 +19,12 @@ struct RotateArgs {
         const void *X;
         void *Y;
         int64_t ldx, x_head, ldy, y_head;
-        int32_t n_heads, x_bf16, y_bf16, vec;
+        int32_t n_heads, x_bf16, y_bf16;
     } item[kMaxRotateItems];
     const int32_t *positions;
     const float *freq;
     int64_t ld_pos, M;
-    int32_t n_items, heads; // heads of all items
+    int32_t heads; // of all items
     int32_t rot_dim, head_dim, pairs, inverse;
     int32_t wide; // every item takes the vector form
     uint32_t axis[kMaxHeadDim / 2 / 16]; // two bits a pair

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(MoveArgs a) {
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
     constexpr int LPT = D / 8, TPP = kThreads / LPT, W = D / 32;
-    __shared__ uint32_t codes[8 * D];
+    __shared__ __attribute__((aligned(16))) uint32_t codes[8 * D];
     __shared__ uint16_t sc[D / 64 * 128];
     const Span w = span_of<D>(a);
     const int e = a.bf16 ? 2 : 4;

@@ -1,6 +1,6 @@
 // Attention of query rows over the paged 4-bit cache, for many rows a sequence
 // (prompts and their chunks): the same pass over the tokens as attend.hip, with
-// each expanded token shared by up to 256 query rows.
+// each expanded token shared by up to 128 query rows.
 //
 // A workgroup takes 128 query rows of one sequence and K/V head (32 a wave) and
 // walks the records they see.  S^T = K Q^T and O^T = V^T P^T on 32x32x16 MFMAs, so
@@ -35,8 +35,10 @@
 // probabilities.  Values keep their 11 bits 22 octaves below the largest of a
 // record, or of a step's records.
 // Probabilities are 2^9 times their value relative to the running reference,
-// which moves only when a sum of 16 of them comes to 65000 (none is lost above
-// 2^-33 of the largest): the common step looks for no maximum.
+// which moves only when a sum of 16 of them comes to 65000 (above 2^-23 of the
+// largest they keep their 11 bits, above 2^-31 some): the common step looks for no
+// maximum.  The row's sum is of the rounded ones, in binary32, so that the weights of
+// a row add up to 1.
 #include "attn.hpp"
 #include "gemm_common.hpp"
 

@@ -20,29 +20,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTableMax = 256; // (token, pair) entries of a workgroup
 
-struct Turn {
-    const float2 *cs;
-    int half;
-    bool pairs;
-};
-
-// Columns col .. col + 7 of one head, as 8-column runs.
+// Columns col .. col + 7 of one head, turned as pairs where they are rotated (of
+// halves only columns passed through come here).
 __device__ __forceinline__ f32x8 turned(const void *x, bool bf, int col, int head_dim, int rot,
-                                        const Turn &t) {
+                                        const float2 *cs) {
     f32x8 v = load8<true>(x, bf, col, head_dim);
     if (col >= rot)
         return v;
-    if (t.pairs) {
-        f32x8 y;
+    f32x8 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 w = t.cs[col / 2 + i];
-            y[2 * i] = v[2 * i] * w.x - v[2 * i + 1] * w.y;
-            y[2 * i + 1] = v[2 * i + 1] * w.x + v[2 * i] * w.y;
-        }
-        return y;
+    for (int i = 0; i < 4; ++i) {
+        const float2 w = cs[col / 2 + i];
+        y[2 * i] = v[2 * i] * w.x - v[2 * i + 1] * w.y;
+        y[2 * i + 1] = v[2 * i + 1] * w.x + v[2 * i] * w.y;
     }
-    return v;
+    return y;
 }
 
 // The (cos, sin) of `tokens` rows from m0 on: entry (i, p) at i * half + p.
@@ -82,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(RotateArgs a, int toke
         while (h >= a.item[k].n_heads)
             h -= a.item[k++].n_heads;
         const RotateArgs::Item &it = a.item[k];
-        const Turn t = {cs + i * half, half, a.pairs != 0};
+        const float2 *turn = cs + i * half; // of the row
         const char *x = static_cast<const char *>(it.X) +
                         ((m0 + i) * it.ldx + h * it.x_head) * (it.x_bf16 ? 2 : 4);
         char *y = static_cast<char *>(it.Y) +
@@ -94,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(RotateArgs a, int toke
             f32x8 u, v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 w = t.cs[col + j];
+                const float2 w = turn[col + j];
                 u[j] = p[j] * w.x - r[j] * w.y;
                 v[j] = r[j] * w.x + p[j] * w.y;
             }
@@ -103,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(RotateArgs a, int toke
         } else {
             const int col = a.pairs ? run * 8 : a.rot_dim + (run - half / 8) * 8;
             store8<true>(y, it.y_bf16, col, a.head_dim,
-                         turned(x, it.x_bf16, col, a.head_dim, a.rot_dim, t));
+                         turned(x, it.x_bf16, col, a.head_dim, a.rot_dim, turn));
         }
     }
 }
