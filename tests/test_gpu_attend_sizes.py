@@ -51,3 +51,21 @@ def test_two_thousand_prompts(monkeypatch):
     r = au.rng(9)
     ctx = [128 + int(x) for x in r.integers(0, 40, 2048)]
     call(monkeypatch, au.Batch([128] * 2048, ctx, 32, seed=10), 1, 1, 64, seed=26, rounded=True)
+
+
+@pytest.mark.parametrize("d,hq,hkv,rows,ctx,window", [
+    (64, 300, 1, [1, 2], [900, 40], 0),       # one token's heads over several tiles
+    (128, 260, 2, [1], [3000], 500),
+    (256, 130, 1, [1, 3], [300, 900], 0),
+    (64, 400, 200, [1, 1, 40], [70, 1, 90], 0),
+    (128, 150, 150, [70], [70], 20)])
+def test_many_heads(monkeypatch, d, hq, hkv, rows, ctx, window):
+    b = au.Batch(rows, ctx, 32, seed=11, lead=1, tail=1)
+    call(monkeypatch, b, hq, hkv, d, window, 3, seed=27,
+         rounded=d < 256 and max(rows) * hq // hkv > ta.FEW)
+
+
+def test_told_of_no_context_at_all(monkeypatch):
+    for d, rows in ((64, [1, 3]), (128, [90, 2]), (256, [20, 1])):
+        b = au.Batch(rows, [400, 333], 32, seed=12)
+        call(monkeypatch, b, 4, 2, d, seed=28, rounded=d < 256, max_context=0)
