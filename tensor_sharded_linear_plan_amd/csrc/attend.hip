@@ -33,8 +33,8 @@
 // three stages: two records are on their way while one is multiplied.
 //
 // One row each of 32 sequences of up to 32767 tokens, 64 / 8 heads of 128: 123 us
-// with the join's 6, 4.6 TB/s, the vector units 65% busy; of one of 131000, 28 / 4
-// heads, 29 us with the join's 7; of 64 with windows of 4096, heads of 64, 39 us.
+// with the join's 6, 4.5 TB/s, the vector units 65% busy; of one of 131000, 28 / 4
+// heads, 30 us with the join's 8; of 64 with windows of 4096, heads of 64, 40 us.
 #include "attn.hpp"
 #include "gemm_common.hpp"
 
