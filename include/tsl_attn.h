@@ -155,7 +155,8 @@ tsl_status cache_size(const tsl_cache *cache, size_t *bytes);
  * Other tokens of the pages keep their bits.  A page that a call writes to
  * belongs to one of its sequences (copy a shared page first), and K and V
  * share no byte with the cache.  Errors: TSL_ERR_INVALID_ARG,
- * TSL_ERR_UNSUPPORTED, TSL_ERR_MISALIGNED (K, V 16-byte aligned, strides whole
+ * TSL_ERR_UNSUPPORTED (sizes; n_kv_heads times the records of max_rows tokens from
+ * 2^24 on), TSL_ERR_MISALIGNED (K, V 16-byte aligned, strides whole
  * 16 bytes; pages 256 bytes), TSL_ERR_HIP.
  */
 tsl_status cache_append(const tsl_cache *cache, const tsl_seqs *seqs, tsl_dtype dtype,
@@ -197,23 +198,26 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * Products accumulate in binary32, the softmax is binary32.  For sequences of
  * up to 64 query rows a K/V head (rows times n_q_heads / n_kv_heads; of a lone
  * sequence max_rows times that), and with head_dim 256, the 4-bit values enter
- * exactly and a probability times a value's scale with 16 bits (the mean of any
- * number of independent values is within 2^-14 of its own size, in the 2-norm);
- * for longer ones rounded to 11 bits (binary16), as the probabilities are, scaled
- * by a power of two that up to 128 neighbouring tokens which some row of the
- * sequence sees have in common: values below 2^-22 of the largest of those lose
- * bits, as do values below 2^-90 of an earlier one that the row gave weight to;
- * probabilities below 2^-23 of the row's largest so far lose bits, and below
- * 2^-31 they are 0; so do elements of Q below 2^-31 of their head's largest.  Both kinds may be in one call (generated tokens beside a
- * prompt's chunk).  |Q| stays below 2^110, scale sum |q k| of a visible token
- * within binary32's range, and sum |v| over a row's tokens below 2^110 (what other
- * rows get does not hang on a row that does not keep to it).  Equal calls give
- * equal bits.  O shares no byte with Q, the cache or the workspace.  scale log2(e)
- * is finite, window and sinks 0 .. 2^30.
+ * exactly and a probability times a value's scale with 16 bits (with equal weights
+ * the mean of n independent values, any n, is within 2^-14 of their runs' range,
+ * max - min, over the root of n, in the 2-norm).  For longer ones K, Q and V are
+ * rounded to 11 bits (binary16), as the probabilities are, scaled by a power of
+ * two that up to 128 neighbouring tokens which some row of the sequence sees have
+ * in common: values below 2^-22 of the largest of those lose bits, as do values
+ * below 2^-90 of an earlier one that the row gave weight to, and elements of Q
+ * below 2^-31 of their head's largest; probabilities below 2^-23 of the row's
+ * largest so far lose bits, and below 2^-31 they are 0.  Both kinds may be in one
+ * call (generated tokens beside a prompt's chunk).  |Q| stays below 2^110, scale
+ * sum |q k| of a visible token within binary32's range, and sum |v| over a row's
+ * tokens below 2^110 (what other rows get does not hang on a row that does not keep
+ * to it).  Equal calls give equal bits.  O shares no byte with Q, the cache or the
+ * workspace.  scale log2(e) is finite, window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
- * n_kv_heads), TSL_ERR_UNSUPPORTED, TSL_ERR_BUFFER_TOO_SMALL,
- * TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides whole 16 bytes),
- * TSL_ERR_HIP.
+ * n_kv_heads), TSL_ERR_UNSUPPORTED (sizes; 2^30 query rows of a K/V head; calls
+ * whose sequences, all counted as long as the longest -- with head_dim 64 and 128
+ * as 64 query rows at most --, come to 2^26 tiles of 4 to 16 query rows may be),
+ * TSL_ERR_BUFFER_TOO_SMALL, TSL_ERR_MISALIGNED (Q, O 16-byte aligned, strides
+ * whole 16 bytes), TSL_ERR_HIP.
  */
 tsl_status cache_attention(const tsl_cache *cache, const tsl_seqs *seqs, int32_t n_q_heads,
                            const void *Q, int64_t ldq, int64_t q_head, float scale, int32_t window,
