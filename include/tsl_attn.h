@@ -212,8 +212,8 @@ tsl_status cache_attention_workspace_size(const tsl_cache *cache, const tsl_seqs
  * tokens below 2^110 (what other rows get does not hang on a row that does not keep
  * to it).  Equal calls give equal bits.  O shares no byte with Q, the cache or the
  * workspace.  With head_dim 256 each 16 query rows expand the records they see for
- * themselves, so prompts take thirty times as long as with 128 for the same
- * operations (1024 rows of 8 / 2 heads 159 us).  scale log2(e) is finite, window and sinks 0 .. 2^30.
+ * themselves, so prompts take four to six times as long as with 128 for the same
+ * operations (4096 rows of 16 / 8 heads 868 us).  scale log2(e) is finite, window and sinks 0 .. 2^30.
  * Errors: TSL_ERR_INVALID_ARG, TSL_ERR_NOT_DIVISIBLE (n_q_heads by
  * n_kv_heads), TSL_ERR_UNSUPPORTED (sizes; 2^30 query rows of a K/V head; calls
  * whose sequences, all counted as long as the longest -- with head_dim 64 and 128
